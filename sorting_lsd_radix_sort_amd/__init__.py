@@ -1,4 +1,4 @@
-"""lrsort: a stable LSD radix sort for AMD MI355X (gfx950).
+"""lrsort: a stable LSD radix sort for AMD MI355X (gfx950), and rows moved by it.
 
 Python binding of the C ABI in ``include/lrsort.h`` (ctypes).  Every function
 named ``lrs_*`` here takes the same arguments as the C function of the same name
@@ -9,6 +9,11 @@ there is no fallback, and a missing library raises.
 
 ``sort_keys`` / ``sort_pairs`` are conveniences over the same calls that
 allocate outputs and temp storage as torch tensors.
+
+``group_tokens``, ``dispatch_rows``, ``combine_rows``, ``combine_rows_grad``,
+``embedding`` and ``embedding_grad`` (``rows.py``, ``include/lrsort_rows.h``) move
+and sum the rows of a matrix in the order of small integer keys: tokens sorted by
+expert and back, and an embedding's gradient by sorted tokens.
 """
 from __future__ import annotations
 
@@ -34,7 +39,9 @@ KEY_TYPE_CODES = {"u32": 0, "i32": 1, "f32": 2, "u64": 3, "i64": 4, "f64": 5}
 DIGIT_BITS = (8, 11)
 EXPORTED = SORT_FUNCTIONS + ("lrs_sort_digits", "lrs_status_string", "lrs_device_copy", "lrs_prof_start",
                              "lrs_prof_stop", "lrs_prof_count", "lrs_prof_read",
-                             "lrs_prof_release", "lrs_bench_read", "lrs_sort_digits_noalloc")
+                             "lrs_prof_release", "lrs_bench_read", "lrs_sort_digits_noalloc",
+                             "lrs_group_tokens", "lrs_dispatch_rows", "lrs_combine_rows",
+                             "lrs_combine_rows_grad", "lrs_embedding", "lrs_embedding_grad")
 
 
 class LrsError(RuntimeError):
@@ -84,6 +91,7 @@ def load_library() -> ctypes.CDLL:
     lib.lrs_prof_release.restype = ci
     lib.lrs_bench_read.argtypes = [vp, sz, vp, vp]
     lib.lrs_bench_read.restype = ci
+    rows.declare(lib)
     _lib = lib
     return lib
 
@@ -369,3 +377,9 @@ def sort_pairs(keys, values, begin_bit: int = 0, end_bit: int | None = None, key
     _keep_for(side, t, keys_out, values_out, keys if keys is not ksrc else None,
               values if values is not vsrc else None)
     return keys_out, values_out
+
+
+from . import rows  # noqa: E402  (uses the helpers above)
+from .rows import (combine_rows, combine_rows_grad, dispatch_rows, embedding, embedding_grad,  # noqa: E402,F401
+                   group_tokens, lrs_combine_rows, lrs_combine_rows_grad, lrs_dispatch_rows, lrs_embedding,
+                   lrs_embedding_grad, lrs_group_tokens)

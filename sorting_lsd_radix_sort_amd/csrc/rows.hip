@@ -1,0 +1,403 @@
+// rows.hip -- host side of include/lrsort_rows.h: argument checks, temp-storage
+// layout and kernel launches on the caller's stream.  Where keys have to be
+// sorted it calls the library's own sort (lrs_sort_digits) with part of the
+// caller's temp storage.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "lrsort.h"
+#include "lrsort_rows.h"
+#include "row_kernels.hpp"
+
+#define LRS_API extern "C" __attribute__((visibility("default")))
+
+namespace {
+
+using namespace lrs_rows;
+
+constexpr size_t kAlign = 256;
+constexpr int64_t kMaxCount = 0x7FFFFFFFll;  // positions and offsets are int32
+constexpr int64_t kMaxGridX = 1 << 20, kMaxGridY = 65535;
+
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+// ------------------------------------------------------------------- checks
+
+bool type_ok(lrs_row_type t) { return t == LRS_ROW_F32 || t == LRS_ROW_BF16 || t == LRS_ROW_F16; }
+bool type_ok(lrs_id_type t) { return t == LRS_ID_I32 || t == LRS_ID_I64; }
+int64_t bytes_of(lrs_row_type t) { return t == LRS_ROW_F32 ? 4 : 2; }
+int64_t bytes_of(lrs_id_type t) { return t == LRS_ID_I32 ? 4 : 8; }
+bool count_ok(int64_t n) { return n >= 0 && n <= kMaxCount; }
+
+// Ids [first, first + count) have to exist as int64.
+bool ids_ok(int64_t first, int64_t count) { return count_ok(count) && first <= INT64_MAX - count; }
+
+// A matrix argument: `rows` rows of `row` bytes, `step` bytes apart.  A vector is a
+// matrix of one row.
+struct Span {
+    uintptr_t at;
+    int64_t rows, row, step;
+    bool empty() const { return rows == 0 || row == 0; }
+    __int128 extent() const { return (__int128)(rows - 1) * step + row; }
+};
+
+Span vector_of(const void *p, int64_t n, int64_t bytes) { return {(uintptr_t)p, 1, n * bytes, n * bytes}; }
+Span matrix_of(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t bytes)
+{
+    // (one row has no stride, and ld is checked before it is multiplied)
+    return {(uintptr_t)p, rows, cols * bytes, rows > 1 ? ld * bytes : cols * bytes};
+}
+
+// Strides and sizes that leave address arithmetic well inside 63 bits.
+bool shape_ok(int64_t rows, int64_t cols, int64_t ld)
+{
+    if (!count_ok(rows) || !count_ok(cols)) return false;
+    if (rows <= 1 || cols == 0) return true;
+    return ld >= cols && (__int128)rows * ld <= ((__int128)1 << 56);
+}
+
+// The array is there and aligned, or empty.
+bool array_ok(const Span &s, int64_t bytes) { return s.empty() || (s.at != 0 && s.at % bytes == 0); }
+
+// Whether two arrays share memory.  Rows that are interleaved with equal strides
+// (columns of one buffer) share none if their columns are apart.
+bool overlap(const Span &a, const Span &b)
+{
+    if (a.empty() || b.empty() || a.at == 0 || b.at == 0) return false;
+    if ((__int128)a.at + a.extent() <= (__int128)b.at || (__int128)b.at + b.extent() <= (__int128)a.at) return false;
+    if (a.rows > 1 && b.rows > 1 && a.step == b.step) {
+        const uintptr_t step = (uintptr_t)a.step;
+        const uintptr_t gap = a.at <= b.at ? (b.at - a.at) % step : (step - (a.at - b.at) % step) % step;
+        return gap < (uintptr_t)a.row || gap + (uintptr_t)b.row > step;
+    }
+    return true;
+}
+
+// ------------------------------------------------------------------ launches
+
+lrs_status launched() { return hipGetLastError() == hipSuccess ? LRS_OK : LRS_ERR_HIP; }
+
+// Lanes per row: as many as its vectors, a power of two up to a workgroup.
+Tiling tiling_of(int64_t rows, int64_t cols, int vec)
+{
+    Tiling t;
+    t.vecs = (cols + vec - 1) / vec;
+    t.tx_log2 = 0;
+    while ((1 << t.tx_log2) < kThreads && (1 << t.tx_log2) < t.vecs) ++t.tx_log2;
+    const int64_t ty = kThreads >> t.tx_log2;
+    t.row_tiles = (rows + ty - 1) / ty;
+    t.col_tiles = (t.vecs + (1 << t.tx_log2) - 1) >> t.tx_log2;
+    return t;
+}
+
+dim3 grid_of(const Tiling &t)
+{
+    return dim3((unsigned)std::min(t.col_tiles, kMaxGridX), (unsigned)std::min(t.row_tiles, kMaxGridY));
+}
+
+bool wave_row(const Tiling &t) { return (1 << t.tx_log2) >= kWave; }
+
+unsigned flat_grid(int64_t n) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>((n + kThreads - 1) / kThreads, 8192)); }
+
+// Calls f with a value of the row type.
+template <typename F>
+lrs_status with_type(lrs_row_type t, F &&f)
+{
+    switch (t) {
+    case LRS_ROW_F32: return f(float{});
+    case LRS_ROW_BF16: return f(bf16{});
+    case LRS_ROW_F16: return f(f16{});
+    }
+    return LRS_ERR_INVALID_ARG;
+}
+
+// Nothing that the C++ runtime throws (the sort keeps a small table of its kernels'
+// occupancy) leaves the C boundary.
+template <typename F>
+lrs_status guarded(F &&f)
+{
+    try {
+        return f();
+    } catch (...) {
+        return LRS_ERR_HIP;
+    }
+}
+
+// ------------------------------------------------------------------ grouping
+
+// Temp storage of a grouping: keys and indices before and after the sort, and the
+// sort's own.
+struct GroupLayout {
+    size_t off_keys = 0, off_index = 0, off_sorted = 0, off_order = 0, off_sort = 0, sort_bytes = 0, total = 0;
+    int bits = 0;
+};
+
+lrs_status group_layout(int64_t n, int64_t groups, GroupLayout *L)
+{
+    L->bits = 0;
+    while (((int64_t)1 << L->bits) <= groups) ++L->bits;  // keys are 0..groups
+    const size_t words = align_up((size_t)n * 4);
+    size_t off = 0;
+    L->off_keys = off, off += words;
+    L->off_index = off, off += words;
+    L->off_sorted = off, off += words;
+    L->off_order = off, off += words;
+    L->off_sort = off;
+    // the size depends on n and the bit range alone: any distinct pointers will do
+    const uintptr_t some = (uintptr_t)1 << 40;
+    const lrs_status st = lrs_sort_digits(LRS_KEY_U32, 8, nullptr, &L->sort_bytes, (const void *)some,
+                                          (const uint32_t *)(2 * some), (void *)(3 * some), (uint32_t *)(4 * some), n,
+                                          0, L->bits, nullptr);
+    L->total = off + L->sort_bytes;
+    return st;
+}
+
+// The sorted keys and their indices in temp storage (indices also in `order` if it
+// is not NULL: it is then where they are).
+lrs_status sort_ids(const GroupLayout &L, char *temp, lrs_id_type id_type, const void *ids, int64_t n, int64_t first,
+                    int64_t groups, int32_t *order, const uint32_t **sorted, const uint32_t **index, hipStream_t stream)
+{
+    uint32_t *keys = (uint32_t *)(temp + L.off_keys), *at = (uint32_t *)(temp + L.off_index);
+    uint32_t *out = (uint32_t *)(temp + L.off_sorted);
+    uint32_t *ord = order != nullptr ? (uint32_t *)order : (uint32_t *)(temp + L.off_order);
+    *sorted = out, *index = ord;
+    if (n == 0) return LRS_OK;
+    if (id_type == LRS_ID_I32)
+        group_keys_kernel<int32_t><<<flat_grid(n), kThreads, 0, stream>>>((const int32_t *)ids, n, first, (uint32_t)groups,
+                                                                         keys, at);
+    else
+        group_keys_kernel<int64_t><<<flat_grid(n), kThreads, 0, stream>>>((const int64_t *)ids, n, first, (uint32_t)groups,
+                                                                         keys, at);
+    const lrs_status st = launched();
+    if (st != LRS_OK) return st;
+    size_t bytes = L.sort_bytes;
+    return lrs_sort_digits(LRS_KEY_U32, 8, temp + L.off_sort, &bytes, keys, at, out, ord, n, 0, L.bits, stream);
+}
+
+// The two-phase temp storage convention: LRS_OK with *temp NULL after a query.
+lrs_status take_temp(void *d_temp, size_t *temp_bytes, size_t total, char **temp)
+{
+    *temp = nullptr;
+    if (d_temp == nullptr) {
+        *temp_bytes = total + (kAlign - 1);
+        return LRS_OK;
+    }
+    const size_t pad = (kAlign - (uintptr_t)d_temp % kAlign) % kAlign;
+    if (*temp_bytes < total + pad) return LRS_ERR_TEMP_TOO_SMALL;
+    *temp = (char *)d_temp + pad;
+    return LRS_OK;
+}
+
+lrs_status group_entry(void *d_temp, size_t *temp_bytes, lrs_id_type id_type, const void *d_ids, int64_t n,
+                       int64_t first, int64_t groups, int32_t *order, int32_t *position, int32_t *offsets,
+                       hipStream_t stream)
+{
+    if (temp_bytes == nullptr || !type_ok(id_type) || !count_ok(n) || !ids_ok(first, groups) || groups >= kMaxCount)
+        return LRS_ERR_INVALID_ARG;
+    const Span ids = vector_of(d_ids, n, bytes_of(id_type));
+    const Span outs[3] = {vector_of(order, order ? n : 0, 4), vector_of(position, position ? n : 0, 4),
+                          vector_of(offsets, offsets ? groups + 1 : 0, 4)};
+    if (!array_ok(ids, bytes_of(id_type))) return LRS_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i) {
+        if (!array_ok(outs[i], 4) || overlap(outs[i], ids)) return LRS_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], outs[j])) return LRS_ERR_INVALID_ARG;
+    }
+    GroupLayout L;
+    lrs_status st = group_layout(n, groups, &L);
+    if (st != LRS_OK) return st;
+    char *temp;
+    st = take_temp(d_temp, temp_bytes, L.total, &temp);
+    if (st != LRS_OK || temp == nullptr) return st;
+    const uint32_t *sorted, *index;
+    st = sort_ids(L, temp, id_type, d_ids, n, first, groups, order, &sorted, &index, stream);
+    if (st != LRS_OK || (position == nullptr && offsets == nullptr)) return st;
+    group_finish_kernel<<<flat_grid(std::max(n, groups + 1)), kThreads, 0, stream>>>(sorted, index, n, (uint32_t)groups,
+                                                                                     position, offsets);
+    return launched();
+}
+
+// Slots: tokens * slots flat indices, int32.
+bool slots_ok(int64_t tokens, int64_t slots)
+{
+    return count_ok(tokens) && count_ok(slots) && (__int128)tokens * slots <= kMaxCount;
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------- exports
+
+LRS_API lrs_status lrs_group_tokens(void *d_temp, size_t *temp_bytes, lrs_id_type id_type, const void *d_ids, int64_t n,
+                                    int64_t first_id, int64_t num_groups, int32_t *d_order, int32_t *d_position,
+                                    int32_t *d_offsets, hipStream_t stream)
+{
+    return guarded([&] {
+        return group_entry(d_temp, temp_bytes, id_type, d_ids, n, first_id, num_groups, d_order, d_position, d_offsets,
+                           stream);
+    });
+}
+
+LRS_API lrs_status lrs_dispatch_rows(lrs_row_type type, const void *d_x, int64_t ld_x, const int32_t *d_position,
+                                     int64_t tokens, int64_t slots, int64_t cols, void *d_rows, int64_t ld_rows,
+                                     int64_t num_rows, hipStream_t stream)
+{
+    if (!type_ok(type) || !slots_ok(tokens, slots) || !shape_ok(tokens, cols, ld_x) ||
+        !shape_ok(num_rows, cols, ld_rows))
+        return LRS_ERR_INVALID_ARG;
+    const int64_t b = bytes_of(type);
+    if (tokens == 0 || slots == 0 || cols == 0 || num_rows == 0) return LRS_OK;
+    const Span x = matrix_of(d_x, tokens, cols, ld_x, b), rows = matrix_of(d_rows, num_rows, cols, ld_rows, b);
+    const Span pos = vector_of(d_position, tokens * slots, 4);
+    if (!array_ok(x, b) || !array_ok(rows, b) || !array_ok(pos, 4) || overlap(rows, x) || overlap(rows, pos))
+        return LRS_ERR_INVALID_ARG;
+    auto run = [&](auto word) {
+        using W = decltype(word);
+        const Tiling t = tiling_of(tokens, cols, kVec<W>);
+        auto *k = wave_row(t) ? dispatch_kernel<W, true> : dispatch_kernel<W, false>;
+        k<<<grid_of(t), kThreads, 0, stream>>>((const W *)d_x, ld_x, d_position, tokens, (int)slots, cols, (W *)d_rows,
+                                               ld_rows, (uint32_t)num_rows, t);
+        return launched();
+    };
+    return b == 4 ? run(uint32_t{}) : run(uint16_t{});
+}
+
+LRS_API lrs_status lrs_combine_rows(lrs_row_type type, const void *d_rows, int64_t ld_rows, int64_t num_rows,
+                                    const int32_t *d_position, lrs_row_type weight_type, const void *d_weights,
+                                    int64_t tokens, int64_t slots, int64_t cols, void *d_y, int64_t ld_y,
+                                    hipStream_t stream)
+{
+    if (!type_ok(type) || (d_weights && !type_ok(weight_type)) || !slots_ok(tokens, slots) ||
+        !shape_ok(num_rows, cols, ld_rows) || !shape_ok(tokens, cols, ld_y))
+        return LRS_ERR_INVALID_ARG;
+    const int64_t b = bytes_of(type), n = tokens * slots;
+    if (tokens == 0 || cols == 0) return LRS_OK;
+    const Span rows = matrix_of(d_rows, num_rows, cols, ld_rows, b), y = matrix_of(d_y, tokens, cols, ld_y, b);
+    const Span pos = vector_of(d_position, n, 4);
+    const Span w = vector_of(d_weights, d_weights ? n : 0, bytes_of(weight_type));
+    if (!array_ok(rows, b) || !array_ok(y, b) || !array_ok(pos, 4) || !array_ok(w, bytes_of(weight_type)) ||
+        overlap(y, rows) || overlap(y, pos) || overlap(y, w))
+        return LRS_ERR_INVALID_ARG;
+    return with_type(type, [&](auto elem) {
+        using T = decltype(elem);
+        const Tiling t = tiling_of(tokens, cols, kVec<T>);
+        auto *k = wave_row(t) ? combine_kernel<T, true> : combine_kernel<T, false>;
+        k<<<grid_of(t), kThreads, 0, stream>>>((const T *)d_rows, ld_rows, (uint32_t)num_rows, d_position,
+                                               (int)weight_type, d_weights, tokens, (int)slots, cols, (T *)d_y, ld_y, t);
+        return launched();
+    });
+}
+
+LRS_API lrs_status lrs_combine_rows_grad(lrs_row_type type, const void *d_grad_y, int64_t ld_grad_y, const void *d_rows,
+                                         int64_t ld_rows, int64_t num_rows, const int32_t *d_position,
+                                         lrs_row_type weight_type, const void *d_weights, int64_t tokens, int64_t slots,
+                                         int64_t cols, void *d_grad_rows, int64_t ld_grad_rows, void *d_grad_weights,
+                                         hipStream_t stream)
+{
+    if (!type_ok(type) || ((d_weights || d_grad_weights) && !type_ok(weight_type)) || !slots_ok(tokens, slots) ||
+        !shape_ok(tokens, cols, ld_grad_y) || !shape_ok(num_rows, cols, ld_grad_rows) ||
+        (d_grad_weights && !shape_ok(num_rows, cols, ld_rows)))
+        return LRS_ERR_INVALID_ARG;
+    const int64_t b = bytes_of(type), wb = bytes_of(weight_type), n = tokens * slots;
+    if (n == 0) return LRS_OK;
+    const Span gy = matrix_of(d_grad_y, tokens, cols, ld_grad_y, b);
+    const Span rows = matrix_of(d_rows, d_grad_weights ? num_rows : 0, cols, ld_rows, b);
+    const Span gr = matrix_of(d_grad_rows, num_rows, cols, ld_grad_rows, b);
+    const Span pos = vector_of(d_position, n, 4), w = vector_of(d_weights, d_weights ? n : 0, wb);
+    const Span gw = vector_of(d_grad_weights, d_grad_weights ? n : 0, wb);
+    if (!array_ok(gy, b) || !array_ok(rows, b) || !array_ok(gr, b) || !array_ok(pos, 4) || !array_ok(w, wb) ||
+        !array_ok(gw, wb))
+        return LRS_ERR_INVALID_ARG;
+    const bool in_place = !rows.empty() && rows.at == gr.at && rows.step == gr.step;
+    if (overlap(gr, gy) || (!in_place && overlap(gr, rows)) || overlap(gr, pos) || overlap(gr, w) || overlap(gw, gy) ||
+        overlap(gw, rows) || overlap(gw, gr) || overlap(gw, pos) || overlap(gw, w))
+        return LRS_ERR_INVALID_ARG;
+    return with_type(type, [&](auto elem) {
+        using T = decltype(elem);
+        combine_grad_kernel<T><<<(unsigned)std::min(n, kMaxGridX), kThreads, 0, stream>>>(
+            (const T *)d_grad_y, ld_grad_y, (const T *)d_rows, ld_rows, (uint32_t)num_rows, d_position, (int)weight_type,
+            d_weights, n, (int)slots, cols, (T *)d_grad_rows, ld_grad_rows, d_grad_weights);
+        return launched();
+    });
+}
+
+LRS_API lrs_status lrs_embedding(lrs_row_type type, const void *d_table, int64_t ld_table, int64_t num_ids,
+                                 lrs_id_type id_type, const void *d_ids, int64_t n, int64_t first_id, float scale,
+                                 int64_t cols, void *d_y, int64_t ld_y, hipStream_t stream)
+{
+    if (!type_ok(type) || !type_ok(id_type) || !ids_ok(first_id, num_ids) || !shape_ok(num_ids, cols, ld_table) ||
+        !shape_ok(n, cols, ld_y))
+        return LRS_ERR_INVALID_ARG;
+    const int64_t b = bytes_of(type), ib = bytes_of(id_type);
+    if (n == 0 || cols == 0) return LRS_OK;
+    const Span table = matrix_of(d_table, num_ids, cols, ld_table, b), y = matrix_of(d_y, n, cols, ld_y, b);
+    const Span ids = vector_of(d_ids, n, ib);
+    if (!array_ok(table, b) || !array_ok(y, b) || !array_ok(ids, ib) || overlap(y, table) || overlap(y, ids))
+        return LRS_ERR_INVALID_ARG;
+    return with_type(type, [&](auto elem) {
+        using T = decltype(elem);
+        auto run = [&](auto id) {
+            using ID = decltype(id);
+            const Tiling t = tiling_of(n, cols, kVec<T>);
+            auto *k = wave_row(t) ? embedding_kernel<T, ID, true> : embedding_kernel<T, ID, false>;
+            k<<<grid_of(t), kThreads, 0, stream>>>((const T *)d_table, ld_table, (uint32_t)num_ids, (const ID *)d_ids, n,
+                                                   first_id, scale, cols, (T *)d_y, ld_y, t);
+            return launched();
+        };
+        return id_type == LRS_ID_I32 ? run(int32_t{}) : run(int64_t{});
+    });
+}
+
+namespace {
+
+lrs_status embedding_grad_entry(void *d_temp, size_t *temp_bytes, lrs_row_type type, const void *d_grad_y,
+                                int64_t ld_grad_y, lrs_id_type id_type, const void *d_ids, int64_t n, int64_t first,
+                                float scale, lrs_row_type grad_type, void *d_grad, int64_t ld_grad, int64_t num_ids,
+                                int64_t cols, int accumulate, hipStream_t stream)
+{
+    if (temp_bytes == nullptr || !type_ok(type) || !type_ok(id_type) || !type_ok(grad_type) ||
+        (grad_type != type && grad_type != LRS_ROW_F32) || !ids_ok(first, num_ids) || num_ids >= kMaxCount ||
+        !shape_ok(n, cols, ld_grad_y) || !shape_ok(num_ids, cols, ld_grad))
+        return LRS_ERR_INVALID_ARG;
+    const int64_t b = bytes_of(type), gb = bytes_of(grad_type), ib = bytes_of(id_type);
+    const Span gy = matrix_of(d_grad_y, n, cols, ld_grad_y, b), grad = matrix_of(d_grad, num_ids, cols, ld_grad, gb);
+    const Span ids = vector_of(d_ids, cols > 0 ? n : 0, ib);
+    if (!array_ok(gy, b) || !array_ok(grad, gb) || !array_ok(ids, ib) || overlap(grad, gy) || overlap(grad, ids))
+        return LRS_ERR_INVALID_ARG;
+    GroupLayout L;
+    lrs_status st = group_layout(n, num_ids, &L);
+    if (st != LRS_OK) return st;
+    char *temp;
+    st = take_temp(d_temp, temp_bytes, L.total, &temp);
+    if (st != LRS_OK || temp == nullptr) return st;
+    if (num_ids == 0 || cols == 0 || (n == 0 && accumulate)) return LRS_OK;
+    const uint32_t *sorted, *index;
+    st = sort_ids(L, temp, id_type, d_ids, n, first, num_ids, nullptr, &sorted, &index, stream);
+    if (st != LRS_OK) return st;
+    return with_type(type, [&](auto elem) {
+        using T = decltype(elem);
+        auto run = [&](auto gelem) {
+            using G = decltype(gelem);
+            const Tiling t = tiling_of(num_ids, cols, kVec<G>);
+            auto *k = wave_row(t) ? embedding_grad_kernel<T, G, true> : embedding_grad_kernel<T, G, false>;
+            k<<<grid_of(t), kThreads, 0, stream>>>((const T *)d_grad_y, ld_grad_y, sorted, index, n, scale, (G *)d_grad,
+                                                   ld_grad, num_ids, cols, accumulate, t);
+            return launched();
+        };
+        return grad_type == LRS_ROW_F32 ? run(float{}) : run(elem);
+    });
+}
+
+}  // namespace
+
+LRS_API lrs_status lrs_embedding_grad(void *d_temp, size_t *temp_bytes, lrs_row_type type, const void *d_grad_y,
+                                      int64_t ld_grad_y, lrs_id_type id_type, const void *d_ids, int64_t n,
+                                      int64_t first_id, float scale, lrs_row_type grad_type, void *d_grad,
+                                      int64_t ld_grad, int64_t num_ids, int64_t cols, int accumulate,
+                                      hipStream_t stream)
+{
+    return guarded([&] {
+        return embedding_grad_entry(d_temp, temp_bytes, type, d_grad_y, ld_grad_y, id_type, d_ids, n, first_id, scale,
+                                    grad_type, d_grad, ld_grad, num_ids, cols, accumulate, stream);
+    });
+}
