@@ -325,39 +325,220 @@ __global__ __launch_bounds__(kThreads) void embedding_kernel(const T *__restrict
     }
 }
 
-// One row of the table's gradient per row of the grid: the run of its id in the
-// sorted keys is found by bisection and its rows are summed in order.
+// The gradient's sums.  The sorted ids are cut into pieces of `piece` slots, one
+// piece of a column tile per unit of work, whatever the ids: a run of equal ids may
+// be one slot or all of them, and pieces stay equal.  A run inside a piece is summed
+// in registers and stored at once.  A run that crosses pieces leaves one float32
+// partial sum in each: slot 0 of a piece for a run that began earlier, slot 1 for one
+// that begins in it and goes on; embedding_join_kernel adds them up, in order.
+struct Pieces {
+    int64_t n;        // sorted slots
+    int piece;        // slots per piece
+    int64_t count;    // pieces
+    uint32_t groups;  // ids at or above it are of no row (sorted last)
+};
+
+template <typename G, int E>
+__device__ __forceinline__ void store_values(G *p, const float (&v)[E], int valid)
+{
+#pragma unroll
+    for (int q = 0; q < E; q += kVec<G>) {
+        float part[kVec<G>];
+#pragma unroll
+        for (int e = 0; e < kVec<G>; ++e) part[e] = v[q + e];
+        if (valid > q) store_raw<G>(p + q, pack<G>(part), valid - q);
+    }
+}
+
+// scale * sum, added to what is there if `accumulate`, rounded once.
+template <typename G, int E>
+__device__ __forceinline__ void store_grad(G *p, const float (&sum)[E], float scale, int accumulate, int valid)
+{
+    float v[E];
+    if (accumulate) {
+#pragma unroll
+        for (int q = 0; q < E; q += kVec<G>) {
+            const u32x4 old = load_raw<G>(p + q, valid - q);
+#pragma unroll
+            for (int e = 0; e < kVec<G>; ++e) v[q + e] = __builtin_fmaf(scale, sum[q + e], element<G>(old, e));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = scale * sum[e];
+    }
+    store_values<G, E>(p, v, valid);
+}
+
+template <typename T, typename G, bool WAVE_ROW>
+__device__ void sum_piece(const T *__restrict__ grad_y, int64_t ld_grad_y, const uint32_t *__restrict__ keys,
+                          const uint32_t *__restrict__ order, Pieces pc, float scale, G *__restrict__ grad,
+                          int64_t ld_grad, int64_t cols, int64_t cols_padded, float *__restrict__ partial,
+                          int accumulate, int64_t piece, int64_t vec)
+{
+    constexpr int E = kVec<T>;
+    constexpr int UNROLL = 8;  // rows in flight per lane
+    const int64_t c = vec * E;
+    const int valid = valid_of(cols, c, E);
+    const int64_t lo = piece * pc.piece;
+    int64_t hi = lo + pc.piece < pc.n ? lo + pc.piece : pc.n;
+    uint32_t run = keys[lo];
+    bool here = lo == 0 || keys[lo - 1] != run;  // the run begins in this piece
+    float sum[E] = {};
+    auto leave = [&](bool goes_on) {
+        if (run >= pc.groups) return;
+        if (here && !goes_on)
+            store_grad<G, E>(grad + (int64_t)run * ld_grad + c, sum, scale, accumulate, valid);
+        else  // (padded rows of whole vectors: no partial store)
+            store_values<float, E>(partial + (piece * 2 + (here ? 1 : 0)) * cols_padded + c, sum, E);
+    };
+    for (int64_t j = lo; j < hi && run < pc.groups; j += UNROLL) {
+        u32x4 r[UNROLL];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u)
+            if (j + u < hi && keys[j + u] < pc.groups)
+                r[u] = load_raw<T>(grad_y + (int64_t)order[j + u] * ld_grad_y + c, valid);
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            if (j + u < hi) {
+                const uint32_t k = keys[j + u];
+                if (k != run) {
+                    leave(false);
+                    run = k;
+                    here = true;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) sum[e] = 0.0f;
+                }
+                if (k < pc.groups) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) sum[e] += element<T>(r[u], e);
+                }
+            }
+        }
+    }
+    leave(hi < pc.n && keys[hi] == run);
+}
+
+// Rows that no id names are zeros.  A workgroup looks kFillRows rows up in the
+// sorted ids (one lane each) and stores those that are not there.
+constexpr int kFillRows = 32;
+
+template <typename G>
+__device__ void fill_rows(const uint32_t *__restrict__ keys, int64_t n, G *__restrict__ grad, int64_t ld_grad,
+                          int64_t num_ids, int64_t cols, int64_t tile)
+{
+    __shared__ int s_named[kFillRows];
+    __syncthreads();
+    if (threadIdx.x < kFillRows) {
+        const int64_t v = tile * kFillRows + threadIdx.x;
+        int named = 1;
+        if (v < num_ids) {
+            const int64_t j = lower_bound(keys, n, (uint32_t)v);
+            named = j < n && keys[j] == (uint32_t)v;
+        }
+        s_named[threadIdx.x] = named;
+    }
+    __syncthreads();
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+    for (int q = 0; q < kFillRows; ++q) {
+        if (s_named[q]) continue;
+        G *row = grad + (tile * kFillRows + q) * ld_grad;
+        for (int64_t c = (int64_t)threadIdx.x * kVec<G>; c < cols; c += kThreads * kVec<G>)
+            store_raw<G>(row + c, zero, valid_of(cols, c, kVec<G>));
+    }
+}
+
+// The first `sum_blocks` workgroups sum pieces, the others write the empty rows.
 template <typename T, typename G, bool WAVE_ROW>
 __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(const T *__restrict__ grad_y, int64_t ld_grad_y,
                                                                   const uint32_t *__restrict__ keys,
-                                                                  const uint32_t *__restrict__ order, int64_t n,
+                                                                  const uint32_t *__restrict__ order, Pieces pc,
                                                                   float scale, G *__restrict__ grad, int64_t ld_grad,
-                                                                  int64_t num_ids, int64_t cols, int accumulate,
-                                                                  Tiling tl)
+                                                                  int64_t num_ids, int64_t cols, int64_t cols_padded,
+                                                                  float *__restrict__ partial, int accumulate,
+                                                                  uint32_t sum_blocks, Tiling tl)
 {
-    LRS_FOR_TILES(tl, num_ids, v, vec)
-    {
-        const int64_t c = vec * kVec<G>;
-        const int valid = valid_of(cols, c, kVec<G>);
-        int64_t j = lower_bound(keys, n, (uint32_t)v);
-        const bool any = j < n && keys[j] == (uint32_t)v;
-        if (accumulate && !any) continue;
-        float sum[kVec<G>] = {};
-        for (; j < n && keys[j] == (uint32_t)v; ++j) {
-            const T *src = grad_y + (int64_t)order[j] * ld_grad_y + c;
-#pragma unroll
-            for (int e = 0; e < kVec<G>; ++e)
-                if (e < valid) sum[e] += (float)src[e];
+    if (blockIdx.x < sum_blocks) {
+        const int64_t units = tl.row_tiles * tl.col_tiles;
+        for (int64_t unit = blockIdx.x; unit < units; unit += sum_blocks) {
+            const int64_t piece = row_of<WAVE_ROW>(tl, unit / tl.col_tiles);
+            const int64_t vec = ((unit % tl.col_tiles) << tl.tx_log2) + (threadIdx.x & ((1 << tl.tx_log2) - 1));
+            if (piece < pc.count && vec < tl.vecs)
+                sum_piece<T, G, WAVE_ROW>(grad_y, ld_grad_y, keys, order, pc, scale, grad, ld_grad, cols, cols_padded,
+                                          partial, accumulate, piece, vec);
         }
-        if (accumulate) {
-            const u32x4 old = load_raw<G>(grad + v * ld_grad + c, valid);
-#pragma unroll
-            for (int e = 0; e < kVec<G>; ++e) sum[e] = __builtin_fmaf(scale, sum[e], element<G>(old, e));
-        } else {
-#pragma unroll
-            for (int e = 0; e < kVec<G>; ++e) sum[e] *= scale;
+    } else {
+        const int64_t tiles = (num_ids + kFillRows - 1) / kFillRows;
+        for (int64_t t = blockIdx.x - sum_blocks; t < tiles; t += gridDim.x - sum_blocks)
+            fill_rows<G>(keys, pc.n, grad, ld_grad, num_ids, cols, t);
+    }
+}
+
+// Adds the partial sums of each run that crosses pieces: the workgroup of the piece
+// in which the run begins takes that piece's partial and those of the pieces after
+// it, four waves a quarter of them each, their sums joined in order.  64 vectors of
+// four columns per workgroup.
+template <typename G>
+__global__ __launch_bounds__(kThreads) void embedding_join_kernel(const uint32_t *__restrict__ keys, Pieces pc,
+                                                                  float scale, G *__restrict__ grad, int64_t ld_grad,
+                                                                  int64_t cols, int64_t cols_padded,
+                                                                  const float *__restrict__ partial, int accumulate,
+                                                                  int64_t col_tiles)
+{
+    constexpr int SLICES = kThreads / kWave;
+    __shared__ float s_sum[SLICES][kWave][4];
+    const int64_t units = (pc.count - 1) * col_tiles;
+    const int lane = threadIdx.x & (kWave - 1), slice = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int64_t piece = unit / col_tiles;
+        const int64_t lo = piece * pc.piece, hi = lo + pc.piece;  // (the last piece is not among them)
+        const uint32_t run = keys[hi - 1];
+        if (run >= pc.groups || keys[hi] != run || (keys[lo] == run && lo > 0 && keys[lo - 1] == run)) continue;
+        // the run's last slot, then its last piece
+        int64_t a = hi, b = pc.n;  // keys[a] == run; b: past the end
+        while (b - a > 1) {
+            const int64_t mid = (a + b) >> 1;
+            if (keys[mid] == run)
+                a = mid;
+            else
+                b = mid;
         }
-        store_raw<G>(grad + v * ld_grad + c, pack<G>(sum), valid);
+        const int64_t last = a / pc.piece, more = last - piece;  // pieces after the first
+        const int64_t per = (more + SLICES - 1) / SLICES;
+        const int64_t from = piece + 1 + slice * per, to = from + per < last + 1 ? from + per : last + 1;
+        const int64_t c = ((unit % col_tiles) * kWave + lane) * 4;
+        float sum[4] = {};
+        if (c < cols) {
+            if (slice == 0) {
+                const u32x4 r = load_raw<float>(partial + (piece * 2 + 1) * cols_padded + c, 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] = element<float>(r, e);
+            }
+#pragma unroll 8
+            for (int64_t p = from; p < to; ++p) {
+                const u32x4 r = load_raw<float>(partial + p * 2 * cols_padded + c, 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] += element<float>(r, e);
+            }
+        }
+        if (more > 1) {  // else the first wave has it all
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s_sum[slice][lane][e] = sum[e];
+            __syncthreads();
+            if (slice == 0) {
+                for (int w = 1; w < SLICES; ++w)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum[e] += s_sum[w][lane][e];
+            }
+        }
+        if (slice == 0 && c < cols) {
+            const int valid = valid_of(cols, c, 4);
+            G *p = grad + (int64_t)run * ld_grad + c;
+            // (four columns are half a vector of 16-bit elements: element by element)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < valid) p[e] = (G)(accumulate ? __builtin_fmaf(scale, sum[e], (float)p[e]) : scale * sum[e]);
+        }
     }
 }
 

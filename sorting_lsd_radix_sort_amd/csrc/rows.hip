@@ -350,6 +350,26 @@ LRS_API lrs_status lrs_embedding(lrs_row_type type, const void *d_table, int64_t
 
 namespace {
 
+// How an embedding's gradient cuts the sorted ids: pieces of 16 to 512 slots, so
+// many that the chip has some 8192 waves of 64 vectors (a part of the rows in a
+// piece, twice as many partial sums at most), and the partial sums' place.
+struct SumLayout {
+    int piece = 16;
+    int64_t count = 0, cols_padded = 0;
+    size_t bytes = 0;
+};
+
+SumLayout sum_layout(int64_t n, int64_t cols, int vec)
+{
+    SumLayout S;
+    const int64_t waves = std::max<int64_t>(1, ((cols + vec - 1) / vec + kWave - 1) / kWave);
+    while (S.piece < 512 && n / S.piece > 8192 / waves) S.piece *= 2;
+    S.count = (n + S.piece - 1) / S.piece;
+    S.cols_padded = (cols + vec - 1) / vec * vec;
+    S.bytes = S.count > 1 ? (size_t)S.count * 2 * (size_t)S.cols_padded * 4 : 0;
+    return S;
+}
+
 lrs_status embedding_grad_entry(void *d_temp, size_t *temp_bytes, lrs_row_type type, const void *d_grad_y,
                                 int64_t ld_grad_y, lrs_id_type id_type, const void *d_ids, int64_t n, int64_t first,
                                 float scale, lrs_row_type grad_type, void *d_grad, int64_t ld_grad, int64_t num_ids,
@@ -367,21 +387,34 @@ lrs_status embedding_grad_entry(void *d_temp, size_t *temp_bytes, lrs_row_type t
     GroupLayout L;
     lrs_status st = group_layout(n, num_ids, &L);
     if (st != LRS_OK) return st;
+    const SumLayout S = sum_layout(n, cols, (int)(16 / b));
     char *temp;
-    st = take_temp(d_temp, temp_bytes, L.total, &temp);
+    st = take_temp(d_temp, temp_bytes, align_up(L.total) + S.bytes, &temp);
     if (st != LRS_OK || temp == nullptr) return st;
     if (num_ids == 0 || cols == 0 || (n == 0 && accumulate)) return LRS_OK;
     const uint32_t *sorted, *index;
     st = sort_ids(L, temp, id_type, d_ids, n, first, num_ids, nullptr, &sorted, &index, stream);
     if (st != LRS_OK) return st;
+    float *partial = (float *)(temp + align_up(L.total));
+    const Pieces pc{n, S.piece, S.count, (uint32_t)num_ids};
     return with_type(type, [&](auto elem) {
         using T = decltype(elem);
         auto run = [&](auto gelem) {
             using G = decltype(gelem);
-            const Tiling t = tiling_of(num_ids, cols, kVec<G>);
+            const Tiling t = tiling_of(S.count, cols, kVec<T>);
+            const unsigned sums = (unsigned)std::min(t.row_tiles * t.col_tiles, kMaxGridX);
+            const unsigned fills =
+                accumulate ? 0u : (unsigned)std::min((num_ids + kFillRows - 1) / kFillRows, kMaxGridX);
             auto *k = wave_row(t) ? embedding_grad_kernel<T, G, true> : embedding_grad_kernel<T, G, false>;
-            k<<<grid_of(t), kThreads, 0, stream>>>((const T *)d_grad_y, ld_grad_y, sorted, index, n, scale, (G *)d_grad,
-                                                   ld_grad, num_ids, cols, accumulate, t);
+            k<<<sums + fills, kThreads, 0, stream>>>((const T *)d_grad_y, ld_grad_y, sorted, index, pc, scale,
+                                                     (G *)d_grad, ld_grad, num_ids, cols, S.cols_padded, partial,
+                                                     accumulate, sums, t);
+            const lrs_status st = launched();
+            if (st != LRS_OK || S.count < 2) return st;
+            const int64_t join_tiles = (cols + 4 * kWave - 1) / (4 * kWave);
+            const unsigned joins = (unsigned)std::min((S.count - 1) * join_tiles, kMaxGridX);
+            embedding_join_kernel<G><<<joins, kThreads, 0, stream>>>(sorted, pc, scale, (G *)d_grad, ld_grad, cols,
+                                                                     S.cols_padded, partial, accumulate, join_tiles);
             return launched();
         };
         return grad_type == LRS_ROW_F32 ? run(float{}) : run(elem);

@@ -156,6 +156,8 @@ def test_empty_calls_need_no_device():
     embed(cols=0, table=None, y=None)
     need = embed_grad(num_ids=0, grad=None)
     assert embed_grad(temp=T, nbytes=need, num_ids=0, grad=None) == need
+    need = embed_grad(cols=0, grad_y=None, ids=None, grad=None)
+    assert embed_grad(temp=T, nbytes=need, cols=0, grad_y=None, ids=None, grad=None) == need
     need = embed_grad(n=0, grad_y=None, ids=None, accumulate=1)
     assert embed_grad(temp=T, nbytes=need, n=0, grad_y=None, ids=None, accumulate=1) == need
 
