@@ -3,7 +3,8 @@
 Run ``python -m sorting_lsd_radix_sort_amd.build``; ``__graft_entry__.build()``
 calls :func:`build` too.  The library is two translation units, compiled side
 by side: the sort (``csrc/lrsort.hip`` with the kernels of ``csrc/kernels.hpp``)
-and the row operators (``csrc/rows.hip`` with those of ``csrc/row_kernels.hpp``).
+and the row operators (``csrc/rows.hip`` with those of ``csrc/row_kernels.hpp``
+and ``csrc/group_kernels.hpp``).
 """
 from __future__ import annotations
 
@@ -17,6 +18,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", "lrsort.hip"), os.path.join(PKG, "csrc", "rows.hip")]
 DEPS = SOURCES + [os.path.join(PKG, "csrc", "kernels.hpp"), os.path.join(PKG, "csrc", "row_kernels.hpp"),
+                  os.path.join(PKG, "csrc", "group_kernels.hpp"),
                   os.path.join(ROOT, "include", "lrsort.h"), os.path.join(ROOT, "include", "lrsort_prof.h"),
                   os.path.join(ROOT, "include", "lrsort_rows.h")]
 LIB = os.path.join(PKG, "liblrsort.so")

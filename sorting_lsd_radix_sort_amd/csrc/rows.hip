@@ -6,6 +6,7 @@
 
 #include <algorithm>
 
+#include "group_kernels.hpp"
 #include "lrsort.h"
 #include "lrsort_rows.h"
 #include "row_kernels.hpp"
@@ -189,6 +190,64 @@ lrs_status take_temp(void *d_temp, size_t *temp_bytes, size_t total, char **temp
     return LRS_OK;
 }
 
+// Groupings of few groups and slots take one counting pass of their own; the others
+// the sort (several passes, and a kernel before and after them).
+constexpr int kFewBins = 513, kManyBins = 2049;
+constexpr int64_t kDirectGroups = kManyBins - 1, kDirectSlots = 1 << 20;
+
+// Blocks of 1024 slots, or 4096 from 32K slots (a block reads every block's counts,
+// so few blocks; a wave's ranking is what they share, so not too few).  Up to 4096
+// slots one block does without the count launch.
+constexpr int64_t kOneBlockSlots = 4 * kPlaceThreads, kSmallBlockSlots = 32 * kPlaceThreads;
+
+int place_items(int64_t n) { return n <= kPlaceThreads || (n > kOneBlockSlots && n <= kSmallBlockSlots) ? 1 : 4; }
+int place_blocks(int64_t n)
+{
+    const int64_t slots = (int64_t)kPlaceThreads * place_items(n);
+    return (int)std::max<int64_t>(1, (n + slots - 1) / slots);
+}
+
+template <int MAX_BINS, int ITEMS, typename SRC>
+lrs_status run_pass(const SRC &src, const Pass &ps, uint32_t *counts, const PlaceOut &out, hipStream_t stream)
+{
+    const int blocks = place_blocks(ps.n);
+    if (blocks > 1) {
+        count_kernel<SRC, MAX_BINS, ITEMS><<<blocks, kPlaceThreads, 0, stream>>>(src, ps, counts);
+        const lrs_status st = launched();
+        if (st != LRS_OK) return st;
+    }
+    place_kernel<SRC, MAX_BINS, ITEMS><<<blocks, kPlaceThreads, 0, stream>>>(src, ps, blocks > 1 ? counts : nullptr,
+                                                                             blocks, out);
+    return launched();
+}
+
+template <typename SRC>
+lrs_status run_pass(const SRC &src, const Pass &ps, uint32_t *counts, const PlaceOut &out, hipStream_t stream)
+{
+    const bool one = place_items(ps.n) == 1;
+    if (ps.bins <= kFewBins)
+        return one ? run_pass<kFewBins, 1>(src, ps, counts, out, stream)
+                   : run_pass<kFewBins, 4>(src, ps, counts, out, stream);
+    return one ? run_pass<kManyBins, 1>(src, ps, counts, out, stream)
+               : run_pass<kManyBins, 4>(src, ps, counts, out, stream);
+}
+
+int bits_of(int64_t values)  // bits that hold 0..values - 1
+{
+    int bits = 0;
+    while (((int64_t)1 << bits) < values) ++bits;
+    return bits;
+}
+
+template <typename ID>
+lrs_status group_direct(const void *ids, int64_t n, int64_t first, int64_t groups, uint32_t *counts, int32_t *order,
+                        int32_t *position, int32_t *offsets, hipStream_t stream)
+{
+    const IdSource<ID> src{(const ID *)ids, first, (uint32_t)groups};
+    const Pass ps{n, 0, bits_of(groups + 1), ~0u, (uint32_t)groups + 1};
+    return run_pass(src, ps, counts, PlaceOut{nullptr, (uint32_t *)order, position, offsets}, stream);
+}
+
 lrs_status group_entry(void *d_temp, size_t *temp_bytes, lrs_id_type id_type, const void *d_ids, int64_t n,
                        int64_t first, int64_t groups, int32_t *order, int32_t *position, int32_t *offsets,
                        hipStream_t stream)
@@ -204,12 +263,23 @@ lrs_status group_entry(void *d_temp, size_t *temp_bytes, lrs_id_type id_type, co
         for (int j = 0; j < i; ++j)
             if (overlap(outs[i], outs[j])) return LRS_ERR_INVALID_ARG;
     }
+    const bool direct = groups <= kDirectGroups && n <= kDirectSlots;
     GroupLayout L;
-    lrs_status st = group_layout(n, groups, &L);
+    lrs_status st = LRS_OK;
+    if (direct)
+        L.total = (size_t)place_blocks(n) * (size_t)(groups + 1) * 4;
+    else
+        st = group_layout(n, groups, &L);
     if (st != LRS_OK) return st;
     char *temp;
     st = take_temp(d_temp, temp_bytes, L.total, &temp);
     if (st != LRS_OK || temp == nullptr) return st;
+    if (order == nullptr && position == nullptr && offsets == nullptr) return LRS_OK;
+    if (direct) {
+        if (id_type == LRS_ID_I32)
+            return group_direct<int32_t>(d_ids, n, first, groups, (uint32_t *)temp, order, position, offsets, stream);
+        return group_direct<int64_t>(d_ids, n, first, groups, (uint32_t *)temp, order, position, offsets, stream);
+    }
     const uint32_t *sorted, *index;
     st = sort_ids(L, temp, id_type, d_ids, n, first, groups, order, &sorted, &index, stream);
     if (st != LRS_OK || (position == nullptr && offsets == nullptr)) return st;

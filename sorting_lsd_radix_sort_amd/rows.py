@@ -16,15 +16,12 @@ just written there can be passed.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
-from . import _check, _ptr, _stream, _temp_tensor, load_library
+from . import _check, _ptr, _stream, load_library
 
 ID_TYPE_CODES = {"i32": 0, "i64": 1}
 ROW_TYPE_CODES = {"f32": 0, "bf16": 1, "f16": 2}
-_ID_SUFFIX = {"torch.int32": "i32", "torch.int64": "i64"}
-_ROW_SUFFIX = {"torch.float32": "f32", "torch.bfloat16": "bf16", "torch.float16": "f16"}
 
 _VP, _SZ, _I64, _CI, _F = (ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t), ctypes.c_int64, ctypes.c_int,
                            ctypes.c_float)
@@ -119,67 +116,92 @@ def lrs_embedding_grad(d_temp, temp_bytes, row_type, d_grad_y, ld_grad_y, id_typ
 
 
 # ------------------------------------------------------------- conveniences
+#
+# A decode step's calls take a few microseconds on the GPU, so what the host does for
+# each is kept short: type codes are looked up by the dtype itself, the C functions
+# are called with plain addresses, and the temp bytes of a size are asked for once.
+
+_types = None  # {torch dtype: code}: (ids, rows)
+_needs: dict = {}  # temp bytes by sizes and types, which alone decide them
 
 
-def _id_suffix(t) -> str:
-    try:
-        return _ID_SUFFIX[str(t.dtype)]
-    except KeyError:
-        raise TypeError("ids must be int32 or int64, not %s" % t.dtype) from None
+def _type_codes():
+    global _types
+    import torch
+    _types = ({torch.int32: 0, torch.int64: 1}, {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}, torch.int32)
+    return _types
 
 
-def _row_suffix(name, dtype) -> str:
-    try:
-        return _ROW_SUFFIX[str(dtype)]
-    except KeyError:
-        raise TypeError("%s must be float32, bfloat16 or float16, not %s" % (name, dtype)) from None
+def _id_code(t) -> int:
+    code = (_types or _type_codes())[0].get(t.dtype)
+    if code is None:
+        raise TypeError("ids must be int32 or int64, not %s" % t.dtype)
+    return code
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+def _row_code(name, dtype) -> int:
+    code = (_types or _type_codes())[1].get(dtype)
+    if code is None:
+        raise TypeError("%s must be float32, bfloat16 or float16, not %s" % (name, dtype))
+    return code
 
 
-def _rows_in(t):
-    """A matrix argument as the library reads it: elements of a row next to each
-    other (a copy where they are not), any stride between rows."""
-    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        return t.contiguous()
-    return t
-
-
-def _ld(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _same_device(device, name, t):
+    if t is not None and t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
 
 
 def _matrix(name, t):
+    """(rows, cols) of a matrix argument."""
     if t.dim() != 2:
         raise ValueError("%s must have two dimensions, not %d" % (name, t.dim()))
-    return t
+    return t.shape
+
+
+def _row_stride(t):
+    """Elements from one row to the next, or None if a row's elements are not next to
+    each other or rows share memory."""
+    rows, cols = t.shape
+    step, one = t.stride()
+    if cols > 1 and one != 1:
+        return None
+    if rows > 1:
+        return step if step >= cols else None
+    return cols
+
+
+def _rows_in(t):
+    """A matrix argument as the library reads it, and its row stride: a copy where a
+    row's elements are not next to each other."""
+    ld = _row_stride(t)
+    if ld is None:
+        t = t.contiguous()
+        ld = t.shape[1]
+    return t, ld
 
 
 def _out_matrix(name, t, rows, cols, dtype, device):
-    """An output matrix: that shape (rows None: any number), type and device, each
-    row contiguous and no two overlapping."""
-    _matrix(name, t)
+    """Row stride of an output matrix, which must have that shape (rows None: any
+    number), type and device."""
     if t.dtype != dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
+    r, c = _matrix(name, t)
+    if c != cols or (rows is not None and r != rows):
         raise ValueError("%s has shape %s, expected (%s, %d)" % (name, tuple(t.shape), "any" if rows is None else rows,
                                                                  cols))
-    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    ld = _row_stride(t)
+    if ld is None:
         raise ValueError("%s must be contiguous within each row" % name)
-    _same_device(device, **{name: t})
-    return t
+    _same_device(device, name, t)
+    return ld
 
 
 def _position(position, device):
-    if str(position.dtype) != "torch.int32":
+    if position.dtype is not (_types or _type_codes())[2]:
         raise TypeError("position must be int32, not %s" % position.dtype)
     if position.dim() != 2:
         raise ValueError("position must have the shape (tokens, slots), not %s" % (tuple(position.shape),))
-    _same_device(device, position=position)
+    _same_device(device, "position", position)
     return position.contiguous()
 
 
@@ -188,25 +210,22 @@ def _weights(weights, position):
         return None, 0
     if weights.shape != position.shape:
         raise ValueError("weights have shape %s, position %s" % (tuple(weights.shape), tuple(position.shape)))
-    _same_device(position.device, weights=weights)
-    return weights.contiguous(), ROW_TYPE_CODES[_row_suffix("weights", weights.dtype)]
+    _same_device(position.device, "weights", weights)
+    return weights.contiguous(), _row_code("weights", weights.dtype)
 
 
 class _On:
-    """Where a call runs: its device made current, and the stream's handle.  On
-    another stream than the current one, the work waits for what the current one
-    holds (inputs copied and outputs allocated there), and `keep` records tensors
-    on it, so that the caching allocator does not hand their memory on while it is
-    in use there."""
+    """Where a call runs if that is not simply the current stream of the current
+    device: the tensors' device is made current, and on another stream than the
+    current one the work waits for what the current one holds (inputs copied and
+    outputs allocated there), and the tensors are recorded on it, so that the caching
+    allocator does not hand their memory on while it is in use there."""
 
     def __init__(self, device, stream):
         import torch
-        if device.type != "cuda":
-            raise ValueError("lrsort needs device tensors, got a tensor on %s" % device)
-        self.guard = contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-        current = torch.cuda.current_stream(device)
-        self.side = None
-        self.handle = current.cuda_stream
+        self.device, self.side = device, None
+        self.current = torch.cuda.current_stream(device)
+        self.handle = self.current.cuda_stream
         if stream is not None:
             handle = stream if isinstance(stream, int) else stream.cuda_stream
             if handle != self.handle:
@@ -214,22 +233,72 @@ class _On:
                 if self.side.device != device:
                     raise ValueError("stream is on %s, the tensors on %s" % (self.side.device, device))
                 self.handle = handle
-        self.current = current
 
-    def __enter__(self):
-        self.guard.__enter__()
+    def call(self, fn, tensors, args) -> int:
+        import torch
         if self.side is not None:
             self.side.wait_stream(self.current)
-        return self
-
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
-
-    def keep(self, *tensors):
+        with torch.cuda.device(self.device):
+            status = fn(*args, self.handle or None)
         if self.side is not None:
             for t in tensors:
                 if t is not None:
                     t.record_stream(self.side)
+        return status
+
+
+def _on(device, stream):
+    """None for the current stream of the current device, else an _On."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError("lrsort needs device tensors, got a tensor on %s" % device)
+    if stream is None and torch.cuda.current_device() == device.index:
+        return None
+    return _On(device, stream)
+
+
+def _current_handle(device) -> int:
+    """Handle of the device's current stream: torch's own shortcut to it where there
+    is one (the Stream object that the public call builds takes 2 us)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _run(on, device, name, tensors, args) -> None:
+    """Calls the C function `name` with `args` and the stream; `tensors` are in use
+    until the stream has done it."""
+    fn = getattr(load_library(), name)
+    if on is None:
+        status = fn(*args, _current_handle(device) or None)
+    else:
+        status = on.call(fn, tensors, args)
+    if status:
+        _check(status, name)
+
+
+def _at(t):
+    """Address of a tensor's first element (None for None and for empty tensors)."""
+    return None if t is None else t.data_ptr() or None
+
+
+def _temp(name, sizes, args, device, temp):
+    """Temp storage for the C call `name` (args: what follows temp_bytes, without the
+    stream), and its size.  `sizes`: what the size depends on."""
+    import torch
+    key = (name,) + sizes
+    need = _needs.get(key)
+    if need is None:
+        tb = ctypes.c_size_t(0)
+        _check(getattr(load_library(), name)(None, ctypes.byref(tb), *args, None), name)
+        if len(_needs) >= 4096:
+            _needs.clear()
+        need = _needs[key] = tb.value
+    if temp is not None:
+        size = temp.numel() * temp.element_size()
+        if size >= need:
+            return temp, size
+    return torch.empty(need, dtype=torch.uint8, device=device), need
 
 
 def group_tokens(ids, num_groups: int, first_id: int = 0, temp=None, stream=None):
@@ -239,21 +308,18 @@ def group_tokens(ids, num_groups: int, first_id: int = 0, temp=None, stream=None
     the shape of ids, where each stands in that order, or -1; offsets
     (num_groups + 1), where each group begins and the last ends."""
     import torch
-    code = ID_TYPE_CODES[_id_suffix(ids)]
-    _same_device(ids.device, temp=temp)
-    on = _On(ids.device, stream)
-    shape = ids.shape
+    code = _id_code(ids)
+    device = ids.device
+    _same_device(device, "temp", temp)
+    on = _on(device, stream)
+    shape, n, num_groups = ids.shape, ids.numel(), int(num_groups)
     ids = ids.contiguous()
-    n = ids.numel()
-    order = torch.empty(n, dtype=torch.int32, device=ids.device)
-    position = torch.empty(shape, dtype=torch.int32, device=ids.device)
-    offsets = torch.empty(max(int(num_groups), 0) + 1, dtype=torch.int32, device=ids.device)
-    need = lrs_group_tokens(None, 0, code, ids, n, first_id, num_groups, order, position, offsets)
-    t = _temp_tensor(need, ids.device, temp)
-    with on:
-        lrs_group_tokens(t, t.numel() * t.element_size(), code, ids, n, first_id, num_groups, order, position, offsets,
-                         on.handle)
-    on.keep(ids, t, order, position, offsets)
+    order = torch.empty(n, dtype=torch.int32, device=device)
+    position = torch.empty(shape, dtype=torch.int32, device=device)
+    offsets = torch.empty(max(num_groups, 0) + 1, dtype=torch.int32, device=device)
+    args = (code, _at(ids), n, int(first_id), num_groups, _at(order), _at(position), _at(offsets))
+    t, size = _temp("lrs_group_tokens", (code, n, num_groups), args, device, temp)
+    _run(on, device, "lrs_group_tokens", (ids, t, order, position, offsets), (_at(t), ctypes.byref(ctypes.c_size_t(size))) + args)
     return order, position, offsets
 
 
@@ -264,20 +330,19 @@ def dispatch_rows(x, position, num_rows: int | None = None, out=None, stream=Non
     that no position names are left as they were: unset in a new matrix.
     The gradient with respect to x is combine_rows(grad_rows, position)."""
     import torch
-    sfx = _row_suffix("x", _matrix("x", x).dtype)
-    pos = _position(position, x.device)
-    if pos.shape[0] != x.shape[0]:
-        raise ValueError("position is for %d tokens, x has %d" % (pos.shape[0], x.shape[0]))
-    if out is not None:
-        _out_matrix("out", out, num_rows, x.shape[1], x.dtype, x.device)
-    on = _On(x.device, stream)
+    code = _row_code("x", x.dtype)
+    device = x.device
+    tokens, cols = _matrix("x", x)
+    pos = _position(position, device)
+    if pos.shape[0] != tokens:
+        raise ValueError("position is for %d tokens, x has %d" % (pos.shape[0], tokens))
+    ld_out = cols if out is None else _out_matrix("out", out, num_rows, cols, x.dtype, device)
+    on = _on(device, stream)
     if out is None:
-        out = torch.empty(pos.numel() if num_rows is None else int(num_rows), x.shape[1], dtype=x.dtype, device=x.device)
-    x = _rows_in(x)
-    with on:
-        lrs_dispatch_rows(ROW_TYPE_CODES[sfx], x, _ld(x), pos, x.shape[0], pos.shape[1], x.shape[1], out, _ld(out),
-                          out.shape[0], on.handle)
-    on.keep(x, pos, out)
+        out = torch.empty(pos.numel() if num_rows is None else int(num_rows), cols, dtype=x.dtype, device=device)
+    x, ld = _rows_in(x)
+    _run(on, device, "lrs_dispatch_rows", (x, pos, out),
+           (code, _at(x), ld, _at(pos), tokens, pos.shape[1], cols, _at(out), ld_out, out.shape[0]))
     return out
 
 
@@ -286,19 +351,19 @@ def combine_rows(rows, position, weights=None, out=None, stream=None):
     ones; float32, bfloat16 or float16, of the shape of position).  Slots of
     position -1 add nothing.  Returns y, of the type of rows."""
     import torch
-    sfx = _row_suffix("rows", _matrix("rows", rows).dtype)
-    pos = _position(position, rows.device)
+    code = _row_code("rows", rows.dtype)
+    device = rows.device
+    num_rows, cols = _matrix("rows", rows)
+    pos = _position(position, device)
     w, wcode = _weights(weights, pos)
-    if out is not None:
-        _out_matrix("out", out, pos.shape[0], rows.shape[1], rows.dtype, rows.device)
-    on = _On(rows.device, stream)
+    tokens, slots = pos.shape
+    ld_out = cols if out is None else _out_matrix("out", out, tokens, cols, rows.dtype, device)
+    on = _on(device, stream)
     if out is None:
-        out = torch.empty(pos.shape[0], rows.shape[1], dtype=rows.dtype, device=rows.device)
-    rows = _rows_in(rows)
-    with on:
-        lrs_combine_rows(ROW_TYPE_CODES[sfx], rows, _ld(rows), rows.shape[0], pos, wcode, w, pos.shape[0], pos.shape[1],
-                         rows.shape[1], out, _ld(out), on.handle)
-    on.keep(rows, pos, w, out)
+        out = torch.empty(tokens, cols, dtype=rows.dtype, device=device)
+    rows, ld = _rows_in(rows)
+    _run(on, device, "lrs_combine_rows", (rows, pos, w, out),
+           (code, _at(rows), ld, num_rows, _at(pos), wcode, _at(w), tokens, slots, cols, _at(out), ld_out))
     return out
 
 
@@ -310,25 +375,26 @@ def combine_rows_grad(grad_y, rows, position, weights, grad_rows=None, stream=No
     (zeros in a new one); grad_weights of the type of weights, zero where position
     is -1, None where weights is None."""
     import torch
-    sfx = _row_suffix("rows", _matrix("rows", rows).dtype)
-    pos = _position(position, rows.device)
+    code = _row_code("rows", rows.dtype)
+    device = rows.device
+    num_rows, cols = _matrix("rows", rows)
+    pos = _position(position, device)
     w, wcode = _weights(weights, pos)
-    _matrix("grad_y", grad_y)
-    if grad_y.dtype != rows.dtype or tuple(grad_y.shape) != (pos.shape[0], rows.shape[1]):
+    tokens, slots = pos.shape
+    if grad_y.dtype != rows.dtype or _matrix("grad_y", grad_y) != (tokens, cols):
         raise ValueError("grad_y is %s %s, expected %s %s" % (grad_y.dtype, tuple(grad_y.shape), rows.dtype,
-                                                              (pos.shape[0], rows.shape[1])))
-    _same_device(rows.device, grad_y=grad_y)
-    if grad_rows is not None:
-        _out_matrix("grad_rows", grad_rows, rows.shape[0], rows.shape[1], rows.dtype, rows.device)
-    on = _On(rows.device, stream)
+                                                              (tokens, cols)))
+    _same_device(device, "grad_y", grad_y)
+    ld_out = cols if grad_rows is None else _out_matrix("grad_rows", grad_rows, num_rows, cols, rows.dtype, device)
+    on = _on(device, stream)
     if grad_rows is None:
-        grad_rows = torch.zeros(rows.shape, dtype=rows.dtype, device=rows.device)
+        grad_rows = torch.zeros(num_rows, cols, dtype=rows.dtype, device=device)
     grad_w = None if w is None else torch.empty_like(w)
-    grad_y, rows = _rows_in(grad_y), _rows_in(rows)
-    with on:
-        lrs_combine_rows_grad(ROW_TYPE_CODES[sfx], grad_y, _ld(grad_y), rows, _ld(rows), rows.shape[0], pos, wcode, w,
-                              pos.shape[0], pos.shape[1], rows.shape[1], grad_rows, _ld(grad_rows), grad_w, on.handle)
-    on.keep(grad_y, rows, pos, w, grad_rows, grad_w)
+    grad_y, ld_y = _rows_in(grad_y)
+    rows, ld = _rows_in(rows)
+    _run(on, device, "lrs_combine_rows_grad", (grad_y, rows, pos, w, grad_rows, grad_w),
+           (code, _at(grad_y), ld_y, _at(rows), ld, num_rows, _at(pos), wcode, _at(w), tokens, slots, cols,
+            _at(grad_rows), ld_out, _at(grad_w)))
     return grad_rows, grad_w
 
 
@@ -337,25 +403,28 @@ def embedding(table, ids, scale: float = 1.0, first_id: int = 0, out=None, strea
     [first_id, first_id + number of rows).  ids: int32 or int64, any shape; y has
     that shape with the row length appended."""
     import torch
-    sfx = _row_suffix("table", _matrix("table", table).dtype)
-    code = ID_TYPE_CODES[_id_suffix(ids)]
-    _same_device(table.device, ids=ids)
-    n, cols, shape = ids.numel(), table.shape[1], tuple(ids.shape)
+    code, id_code = _row_code("table", table.dtype), _id_code(ids)
+    device = table.device
+    num_ids, cols = _matrix("table", table)
+    _same_device(device, "ids", ids)
+    n, shape = ids.numel(), (*ids.shape, cols)
+    y, ld_y = out, cols
     if out is not None:
-        if tuple(out.shape) != shape + (cols,):
-            raise ValueError("out has shape %s, expected %s" % (tuple(out.shape), shape + (cols,)))
-        if out.dim() != 2 and not out.is_contiguous():
-            raise ValueError("out must be contiguous")
-        y = _out_matrix("out", out if out.dim() == 2 else out.view(n, cols), n, cols, table.dtype, table.device)
-    on = _On(table.device, stream)
+        if out.shape != shape:
+            raise ValueError("out has shape %s, expected %s" % (tuple(out.shape), shape))
+        if len(shape) != 2:
+            if not out.is_contiguous():
+                raise ValueError("out must be contiguous")
+            y = out.view(n, cols)
+        ld_y = _out_matrix("out", y, n, cols, table.dtype, device)
+    on = _on(device, stream)
     if out is None:
-        y = torch.empty(n, cols, dtype=table.dtype, device=table.device)
-    table, ids = _rows_in(table), ids.contiguous()
-    with on:
-        lrs_embedding(ROW_TYPE_CODES[sfx], table, _ld(table), table.shape[0], code, ids, n, first_id, scale, cols, y,
-                      _ld(y), on.handle)
-    on.keep(table, ids, y)
-    return y.view(shape + (cols,)) if out is None else out
+        y = out = torch.empty(shape, dtype=table.dtype, device=device)
+    table, ld = _rows_in(table)
+    ids = ids.contiguous()
+    _run(on, device, "lrs_embedding", (table, ids, y),
+           (code, _at(table), ld, num_ids, id_code, _at(ids), n, int(first_id), float(scale), cols, _at(y), ld_y))
+    return out
 
 
 def embedding_grad(grad_y, ids, num_ids: int, scale: float = 1.0, first_id: int = 0, dtype=None, grad=None,
@@ -367,29 +436,29 @@ def embedding_grad(grad_y, ids, num_ids: int, scale: float = 1.0, first_id: int 
     `grad`, and rows that no id names are not touched; otherwise every row is
     written."""
     import torch
-    sfx = _row_suffix("grad_y", grad_y.dtype)
-    code = ID_TYPE_CODES[_id_suffix(ids)]
-    _same_device(grad_y.device, ids=ids, temp=temp)
-    if grad_y.dim() < 1 or tuple(grad_y.shape[:-1]) != tuple(ids.shape):
+    code, id_code = _row_code("grad_y", grad_y.dtype), _id_code(ids)
+    device, num_ids = grad_y.device, int(num_ids)
+    _same_device(device, "ids", ids)
+    _same_device(device, "temp", temp)
+    if grad_y.dim() < 1 or grad_y.shape[:-1] != ids.shape:
         raise ValueError("grad_y has shape %s for ids of shape %s" % (tuple(grad_y.shape), tuple(ids.shape)))
     n, cols = ids.numel(), grad_y.shape[-1]
-    dtype = dtype if dtype is not None else grad.dtype if grad is not None else grad_y.dtype
+    if dtype is None:
+        dtype = grad.dtype if grad is not None else grad_y.dtype
     if dtype not in (grad_y.dtype, torch.float32):
         raise TypeError("the gradient must be %s or float32, not %s" % (grad_y.dtype, dtype))
     if grad is not None:
-        _out_matrix("grad", grad, int(num_ids), cols, dtype, grad_y.device)
+        ld_grad = _out_matrix("grad", grad, num_ids, cols, dtype, device)
     elif accumulate:
         raise ValueError("accumulate needs the gradient to add to")
-    on = _On(grad_y.device, stream)
+    on = _on(device, stream)
     if grad is None:
-        grad = torch.empty(max(int(num_ids), 0), cols, dtype=dtype, device=grad_y.device)
-    g2 = _rows_in(grad_y if grad_y.dim() == 2 else grad_y.reshape(n, cols))
+        grad, ld_grad = torch.empty(max(num_ids, 0), cols, dtype=dtype, device=device), cols
+    g2, ld = _rows_in(grad_y if grad_y.dim() == 2 else grad_y.reshape(n, cols))
     ids = ids.contiguous()
-    args = (ROW_TYPE_CODES[sfx], g2, _ld(g2), code, ids, n, first_id, scale, ROW_TYPE_CODES[_row_suffix("grad", dtype)],
-            grad, _ld(grad), num_ids, cols, accumulate)
-    need = lrs_embedding_grad(None, 0, *args)
-    t = _temp_tensor(need, grad_y.device, temp)
-    with on:
-        lrs_embedding_grad(t, t.numel() * t.element_size(), *args, on.handle)
-    on.keep(g2, ids, t, grad)
+    grad_code = _row_code("grad", dtype)
+    args = (code, _at(g2), ld, id_code, _at(ids), n, int(first_id), float(scale), grad_code, _at(grad), ld_grad, num_ids,
+            cols, 1 if accumulate else 0)
+    t, size = _temp("lrs_embedding_grad", (code, id_code, n, grad_code, num_ids, cols), args, device, temp)
+    _run(on, device, "lrs_embedding_grad", (g2, ids, t, grad), (_at(t), ctypes.byref(ctypes.c_size_t(size))) + args)
     return grad
