@@ -10,6 +10,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace lrs_rows {
 
 constexpr int kWave = 64;
@@ -64,6 +66,27 @@ __device__ __forceinline__ void store_raw(T *p, u32x4 r, int valid)
                 reinterpret_cast<uint16_t *>(p)[e] = (uint16_t)(r[e / 2] >> (16 * (e & 1)));
         }
     }
+}
+
+// The same past the caches (NT): for rows that are read or written once and more of
+// them than the L2 holds.
+template <bool NT, typename T>
+__device__ __forceinline__ u32x4 load_once(const T *p, int valid)
+{
+    if constexpr (NT)
+        if (valid >= kVec<T>) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(p));
+    return load_raw<T>(p, valid);
+}
+
+template <bool NT, typename T>
+__device__ __forceinline__ void store_once(T *p, u32x4 r, int valid)
+{
+    if constexpr (NT)
+        if (valid >= kVec<T>) {
+            __builtin_nontemporal_store((u32x4_any)r, reinterpret_cast<u32x4_any *>(p));
+            return;
+        }
+    store_raw<T>(p, r, valid);
 }
 
 // Element e of a vector in float32 (exact for all three types).
@@ -218,8 +241,9 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(const T *__restrict_
     }
 }
 
-// A token's rows are summed in the order of its slots, in float32.
-template <typename T, bool WAVE_ROW>
+// A token's rows are summed in the order of its slots, in float32, SLOTS of them in
+// flight per lane.
+template <typename T, bool WAVE_ROW, int SLOTS, bool NT>
 __global__ __launch_bounds__(kThreads) void combine_kernel(const T *__restrict__ rows, int64_t ld_rows,
                                                            uint32_t num_rows, const int32_t *__restrict__ position,
                                                            int weight_type, const void *__restrict__ weights,
@@ -231,76 +255,110 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const T *__restrict__
         const int64_t c = vec * kVec<T>;
         const int valid = valid_of(cols, c, kVec<T>);
         float sum[kVec<T>] = {};
-        for (int k = 0; k < slots; ++k) {
-            const uint32_t p = (uint32_t)position[t * slots + k];
-            if (p >= num_rows) continue;
-            const u32x4 r = load_raw<T>(rows + (int64_t)p * ld_rows + c, valid);
-            const float w = weights != nullptr ? load_scalar(weights, weight_type, t * slots + k) : 1.0f;
+        for (int k0 = 0; k0 < slots; k0 += SLOTS) {
+            uint32_t p[SLOTS];
+            u32x4 r[SLOTS];
+            float w[SLOTS];
 #pragma unroll
-            for (int e = 0; e < kVec<T>; ++e) sum[e] = __builtin_fmaf(w, element<T>(r, e), sum[e]);
+            for (int u = 0; u < SLOTS; ++u) {
+                p[u] = k0 + u < slots ? (uint32_t)position[t * slots + k0 + u] : ~0u;
+                if (p[u] < num_rows) {
+                    r[u] = load_once<NT>(rows + (int64_t)p[u] * ld_rows + c, valid);
+                    w[u] = weights != nullptr ? load_scalar(weights, weight_type, t * slots + k0 + u) : 1.0f;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < SLOTS; ++u)
+                if (p[u] < num_rows) {
+#pragma unroll
+                    for (int e = 0; e < kVec<T>; ++e) sum[e] = __builtin_fmaf(w[u], element<T>(r[u], e), sum[e]);
+                }
         }
-        store_raw<T>(y + t * ld_y + c, pack<T>(sum), valid);
+        store_once<NT>(y + t * ld_y + c, pack<T>(sum), valid);
     }
 }
 
-// Sum over the workgroup, in a fixed order; every thread calls it.
-__device__ __forceinline__ float block_sum(float v, float *s_part)
+// Sum over the lanes of a row: a whole wave (WAVE_ROW) or 2^tx_log2 lanes of it, in
+// a fixed order, the same for every lane.
+template <bool WAVE_ROW>
+__device__ __forceinline__ float lanes_sum(float v, int tx_log2)
 {
-#pragma unroll
-    for (int x = 32; x >= 1; x >>= 1) v += __shfl_xor(v, x);
-    __syncthreads();
-    if ((threadIdx.x & (kWave - 1)) == 0) s_part[threadIdx.x / kWave] = v;
-    __syncthreads();
-    float all = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kThreads / kWave; ++w) all += s_part[w];
-    return all;
+    if constexpr (WAVE_ROW) {
+        auto add = [&](auto ctrl, auto rows) {
+            const int other = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), ctrl.value, rows.value, 0xf, false);
+            v += __builtin_bit_cast(float, other);
+        };
+        using std::integral_constant;
+        add(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // row_shr:1
+        add(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});  // row_shr:2
+        add(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});  // row_shr:4
+        add(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});  // row_shr:8
+        add(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});  // row_bcast:15
+        add(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});  // row_bcast:31
+        return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+    } else {
+        for (int x = 1 << tx_log2 >> 1; x >= 1; x >>= 1) v += __shfl_xor(v, x);
+        return v;
+    }
 }
 
-// One workgroup per slot: its row of grad_rows is w times the token's grad_y, and
-// the weight's gradient their inner product.  rows and grad_rows may be the same
-// memory: a thread reads each element before it stores there.
-template <typename T>
+// A row tile serves whole tokens, slot by slot (grid.x of their slots at once): a
+// slot's row is read, its inner product with the token's grad_y formed, and its
+// gradient stored; grad_y comes from cache after the first slot.  rows and grad_rows
+// may be the same memory: a thread reads each element before it stores there.
+template <typename T, bool WAVE_ROW, bool NT>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(const T *__restrict__ grad_y, int64_t ld_grad_y,
                                                                 const T *rows, int64_t ld_rows, uint32_t num_rows,
                                                                 const int32_t *__restrict__ position, int weight_type,
-                                                                const void *__restrict__ weights, int64_t n, int slots,
-                                                                int64_t cols, T *grad_rows, int64_t ld_grad_rows,
-                                                                void *__restrict__ grad_weights)
+                                                                const void *__restrict__ weights, int64_t tokens,
+                                                                int slots, int64_t cols, T *grad_rows,
+                                                                int64_t ld_grad_rows, void *__restrict__ grad_weights,
+                                                                Tiling tl)
 {
     __shared__ float s_part[kThreads / kWave];
-    const int64_t vecs = (cols + kVec<T> - 1) / kVec<T>;
-    for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
-        const uint32_t p = (uint32_t)position[i];
-        const bool there = p < num_rows;
-        float dot = 0.0f;
-        if (there) {
-            const float w = weights != nullptr ? load_scalar(weights, weight_type, i) : 1.0f;
-            for (int64_t vec = threadIdx.x; vec < vecs; vec += kThreads) {
-                const int64_t c = vec * kVec<T>;
-                const int valid = valid_of(cols, c, kVec<T>);
-                const u32x4 g = load_raw<T>(grad_y + i / slots * ld_grad_y + c, valid);
-                if (grad_weights != nullptr) {
-                    const u32x4 r = load_raw<T>(rows + (int64_t)p * ld_rows + c, valid);
+    const int lane = threadIdx.x & ((1 << tl.tx_log2) - 1);
+    const int waves = 1 << tl.tx_log2 >> 6;  // per token; 0 where a wave serves several
+    for (int64_t tile = blockIdx.y; tile < tl.row_tiles; tile += gridDim.y) {
+        const int64_t t = row_of<WAVE_ROW>(tl, tile);
+        for (int64_t k = blockIdx.x; k < slots; k += gridDim.x) {
+            const uint32_t p = t < tokens ? (uint32_t)position[t * slots + k] : ~0u;
+            float dot = 0.0f;
+            if (p < num_rows) {
+                const float w = weights != nullptr ? load_scalar(weights, weight_type, t * slots + k) : 1.0f;
+                for (int64_t vec = lane; vec < tl.vecs; vec += 1 << tl.tx_log2) {
+                    const int64_t c = vec * kVec<T>;
+                    const int valid = valid_of(cols, c, kVec<T>);
+                    const u32x4 g = load_raw<T>(grad_y + t * ld_grad_y + c, valid);
+                    if (grad_weights != nullptr) {
+                        const u32x4 r = load_once<NT>(rows + (int64_t)p * ld_rows + c, valid);
 #pragma unroll
-                    for (int e = 0; e < kVec<T>; ++e) dot = __builtin_fmaf(element<T>(g, e), element<T>(r, e), dot);
+                        for (int e = 0; e < kVec<T>; ++e) dot = __builtin_fmaf(element<T>(g, e), element<T>(r, e), dot);
+                    }
+                    float out[kVec<T>];
+#pragma unroll
+                    for (int e = 0; e < kVec<T>; ++e) out[e] = w * element<T>(g, e);
+                    store_once<NT>(grad_rows + (int64_t)p * ld_grad_rows + c, pack<T>(out), valid);
                 }
-                float out[kVec<T>];
-#pragma unroll
-                for (int e = 0; e < kVec<T>; ++e) out[e] = w * element<T>(g, e);
-                store_raw<T>(grad_rows + (int64_t)p * ld_grad_rows + c, pack<T>(out), valid);
             }
-        }
-        if (grad_weights != nullptr) {
-            dot = block_sum(dot, s_part);
-            if (threadIdx.x == 0) store_scalar(grad_weights, weight_type, i, dot);
+            if (grad_weights == nullptr) continue;
+            dot = lanes_sum<WAVE_ROW>(dot, tl.tx_log2);
+            if (waves > 1) {
+                __syncthreads();  // (the last slot's parts have been read)
+                if ((threadIdx.x & (kWave - 1)) == 0) s_part[threadIdx.x / kWave] = dot;
+                __syncthreads();
+                if (lane == 0) {
+                    dot = 0.0f;
+                    for (int v = 0; v < waves; ++v) dot += s_part[threadIdx.x / kWave + v];
+                }
+            }
+            if (lane == 0 && t < tokens) store_scalar(grad_weights, weight_type, t * slots + k, dot);
         }
     }
 }
 
 // ----------------------------------------------------------------- embedding
 
-template <typename T, typename ID, bool WAVE_ROW>
+template <typename T, typename ID, bool WAVE_ROW, bool NT>
 __global__ __launch_bounds__(kThreads) void embedding_kernel(const T *__restrict__ table, int64_t ld_table,
                                                              uint32_t num_ids, const ID *__restrict__ ids, int64_t n,
                                                              int64_t first, float scale, int64_t cols,
@@ -321,7 +379,7 @@ __global__ __launch_bounds__(kThreads) void embedding_kernel(const T *__restrict
                 r = pack<T>(out);
             }
         }
-        store_raw<T>(y + i * ld_y + c, r, valid);
+        store_once<NT>(y + i * ld_y + c, r, valid);
     }
 }
 
