@@ -110,9 +110,12 @@ __device__ __forceinline__ uint32_t wave_rank(uint32_t digit, bool valid, int bi
 }
 
 // Digit counts of block b = slots [b * 1024 * ITEMS, ...), one row of `bins` each.
+// `clear`, where given, is a word set to zero for a later kernel.
 template <typename SRC, int MAX_BINS, int ITEMS>
-__global__ __launch_bounds__(kPlaceThreads) void count_kernel(SRC src, Pass ps, uint32_t *__restrict__ counts)
+__global__ __launch_bounds__(kPlaceThreads) void count_kernel(SRC src, Pass ps, uint32_t *__restrict__ counts,
+                                                              uint32_t *clear)
 {
+    if (clear != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *clear = 0;
     __shared__ uint32_t s_count[MAX_BINS];
     for (uint32_t b = threadIdx.x; b < ps.bins; b += kPlaceThreads) s_count[b] = 0;
     __syncthreads();
@@ -138,27 +141,28 @@ __global__ __launch_bounds__(kPlaceThreads) void count_kernel(SRC src, Pass ps, 
     for (uint32_t b = threadIdx.x; b < ps.bins; b += kPlaceThreads) counts[(int64_t)blockIdx.x * ps.bins + b] = s_count[b];
 }
 
-// Stable placement of block b's slots.  `counts` holds every block's digit counts
-// (from count_kernel), or is NULL for a pass of one block, which counts as it ranks.
-// Each wave ranks 64 * ITEMS slots in a row; a slot's place is its bin's start, plus
+// LDS of a placement by 1024 threads.
+template <int MAX_BINS>
+struct PlaceSmem {
+    uint32_t wave[kPlaceWaves * MAX_BINS];  // per wave: counts, then the slots of earlier waves
+    uint32_t all[MAX_BINS], start[MAX_BINS];
+    uint32_t tmp[kPlaceWaves];
+};
+
+// Places of a block's slots, slot i of lane l of wave w being the block's
+// w * 64 * ITEMS + i * 64 + l, `valid` or not: a slot's place is its bin's start, plus
 // the bin's slots in earlier blocks, in earlier waves of the block and before it in
-// its wave.
-template <typename SRC, int MAX_BINS, int ITEMS>
-__global__ __launch_bounds__(kPlaceThreads) void place_kernel(SRC src, Pass ps, const uint32_t *__restrict__ counts,
-                                                              int blocks, PlaceOut out)
+// its wave.  `counts` holds every block's digit counts, or is NULL for a pass of one
+// block, which counts as it ranks.  Every thread calls it.
+template <int MAX_BINS, int ITEMS>
+__device__ __forceinline__ void place_slots(const Pass &ps, const uint32_t (&key)[ITEMS], const bool (&valid)[ITEMS],
+                                            const uint32_t *__restrict__ counts, int block, int blocks,
+                                            int32_t *offsets, PlaceSmem<MAX_BINS> &s, uint32_t (&to)[ITEMS])
 {
     constexpr int PER = (MAX_BINS + kPlaceThreads - 1) / kPlaceThreads;
-    __shared__ uint32_t s_wave[kPlaceWaves * MAX_BINS];  // per wave: counts, then the slots of earlier waves
-    __shared__ uint32_t s_all[MAX_BINS], s_start[MAX_BINS];
-    __shared__ uint32_t s_tmp[kPlaceWaves];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t first = (int64_t)blockIdx.x * kPlaceThreads * ITEMS + wave * 64 * ITEMS + lane;
-    uint32_t key[ITEMS], rank[ITEMS];
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i)
-        if (first + i * 64 < ps.n) key[i] = src.key(first + i * 64);
-    for (uint32_t b = tid; b < kPlaceWaves * ps.bins; b += kPlaceThreads) s_wave[b] = 0;
-    for (uint32_t b = tid; b < ps.bins; b += kPlaceThreads) s_all[b] = 0, s_start[b] = 0;
+    const int tid = threadIdx.x, wave = tid >> 6;
+    for (uint32_t b = tid; b < kPlaceWaves * ps.bins; b += kPlaceThreads) s.wave[b] = 0;
+    for (uint32_t b = tid; b < ps.bins; b += kPlaceThreads) s.all[b] = 0, s.start[b] = 0;
     __syncthreads();
     if (counts != nullptr) {
         // each bin's slots in all blocks and in earlier ones: 1024 / bins lanes per
@@ -172,58 +176,114 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(SRC src, Pass ps, 
             for (int r = part; r < blocks; r += parts) {
                 const uint32_t c = counts[(int64_t)r * ps.bins + b];
                 all += c;
-                before += r < (int)blockIdx.x ? c : 0u;
+                before += r < block ? c : 0u;
             }
-            atomicAdd(&s_all[b], all);
-            atomicAdd(&s_start[b], before);
+            atomicAdd(&s.all[b], all);
+            atomicAdd(&s.start[b], before);
         }
     }
+    uint32_t rank[ITEMS];
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        const bool valid = first + i * 64 < ps.n;
-        rank[i] = wave_rank(valid ? digit_in(ps, key[i]) : 0u, valid, ps.bits, s_wave + wave * ps.bins);
-    }
+    for (int i = 0; i < ITEMS; ++i)
+        rank[i] = wave_rank(valid[i] ? digit_in(ps, key[i]) : 0u, valid[i], ps.bits, s.wave + wave * ps.bins);
     __syncthreads();
     for (uint32_t b = tid; b < ps.bins; b += kPlaceThreads) {
         uint32_t sum = 0;
 #pragma unroll
         for (int w = 0; w < kPlaceWaves; ++w) {
-            const uint32_t c = s_wave[w * ps.bins + b];
-            s_wave[w * ps.bins + b] = sum;
+            const uint32_t c = s.wave[w * ps.bins + b];
+            s.wave[w * ps.bins + b] = sum;
             sum += c;
         }
-        if (counts == nullptr) s_all[b] = sum;
+        if (counts == nullptr) s.all[b] = sum;
     }
     __syncthreads();
     uint32_t mine[PER], total = 0;
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
         const uint32_t b = tid * PER + q;
-        mine[q] = b < ps.bins ? s_all[b] : 0u;
+        mine[q] = b < ps.bins ? s.all[b] : 0u;
         total += mine[q];
     }
-    uint32_t start = place_scan(total, s_tmp);
+    uint32_t start = place_scan(total, s.tmp);
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
         const uint32_t b = tid * PER + q;
         if (b < ps.bins) {
-            s_start[b] += start;
-            if (out.offsets != nullptr && blockIdx.x == 0) out.offsets[b] = (int32_t)start;
+            s.start[b] += start;
+            if (offsets != nullptr && block == 0) offsets[b] = (int32_t)start;
         }
         start += mine[q];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        const int64_t at = first + i * 64;
-        if (at < ps.n) {
+    for (int i = 0; i < ITEMS; ++i)
+        if (valid[i]) {
             const uint32_t d = digit_in(ps, key[i]);
-            const uint32_t to = s_start[d] + s_wave[wave * ps.bins + d] + rank[i];
-            if (out.keys != nullptr) out.keys[to] = key[i];
-            if (out.values != nullptr) out.values[to] = src.value(at);
-            if (out.position != nullptr) out.position[at] = d + 1 < ps.bins ? (int32_t)to : -1;
+            to[i] = s.start[d] + s.wave[wave * ps.bins + d] + rank[i];
         }
+}
+
+// One block's share of a pass: slots [block * 1024 * ITEMS, ...).
+template <typename SRC, int MAX_BINS, int ITEMS>
+__global__ __launch_bounds__(kPlaceThreads) void place_kernel(SRC src, Pass ps, const uint32_t *__restrict__ counts,
+                                                              int blocks, PlaceOut out)
+{
+    __shared__ PlaceSmem<MAX_BINS> s;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t first = (int64_t)blockIdx.x * kPlaceThreads * ITEMS + wave * 64 * ITEMS + lane;
+    uint32_t key[ITEMS], to[ITEMS];
+    bool valid[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        valid[i] = first + i * 64 < ps.n;
+        if (valid[i]) key[i] = src.key(first + i * 64);
     }
+    place_slots<MAX_BINS, ITEMS>(ps, key, valid, counts, blockIdx.x, blocks, out.offsets, s, to);
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        if (!valid[i]) continue;
+        const int64_t at = first + i * 64;
+        if (out.keys != nullptr) out.keys[to[i]] = key[i];
+        if (out.values != nullptr) out.values[to[i]] = src.value(at);
+        if (out.position != nullptr) out.position[at] = digit_in(ps, key[i]) + 1 < ps.bins ? (int32_t)to[i] : -1;
+    }
+}
+
+// The whole order of up to 1024 * ITEMS ids by one block: pass after pass of
+// `digit_bits` bits from the lowest, the pairs kept in LDS between them.
+template <typename ID, int MAX_BINS, int ITEMS>
+__global__ __launch_bounds__(kPlaceThreads) void order_kernel(IdSource<ID> src, int n, int bits, int digit_bits,
+                                                              uint32_t *__restrict__ sorted,
+                                                              uint32_t *__restrict__ index, uint32_t *clear)
+{
+    if (clear != nullptr && threadIdx.x == 0) *clear = 0;
+    __shared__ PlaceSmem<MAX_BINS> s;
+    __shared__ uint32_t s_key[kPlaceThreads * ITEMS], s_value[kPlaceThreads * ITEMS];
+    const int first = (threadIdx.x >> 6) * 64 * ITEMS + (threadIdx.x & 63);
+    uint32_t key[ITEMS], value[ITEMS], to[ITEMS];
+    bool valid[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        valid[i] = first + i * 64 < n;
+        value[i] = (uint32_t)(first + i * 64);
+        if (valid[i]) key[i] = src.key(first + i * 64);
+    }
+    for (int shift = 0; shift < bits; shift += digit_bits) {
+        const int width = digit_bits < bits - shift ? digit_bits : bits - shift;
+        const Pass ps{n, shift, width, (1u << width) - 1u, 1u << width};
+        place_slots<MAX_BINS, ITEMS>(ps, key, valid, nullptr, 0, 1, nullptr, s, to);
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+            if (valid[i]) s_key[to[i]] = key[i], s_value[to[i]] = value[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+            if (valid[i]) key[i] = s_key[first + i * 64], value[i] = s_value[first + i * 64];
+    }
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+        if (valid[i]) sorted[first + i * 64] = key[i], index[first + i * 64] = value[i];
 }
 
 }  // namespace lrs_rows

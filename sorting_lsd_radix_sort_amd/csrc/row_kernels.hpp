@@ -32,61 +32,105 @@ typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 template <typename T>
 constexpr int kVec = 16 / (int)sizeof(T);  // elements of one 16-byte vector
 
-// `valid` elements (at most a vector's) from p; the others are zero.
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32_any __attribute__((aligned(2)));
+
+// One vector of a row: the elements from column c, `valid` of them (the last vector of
+// a row may be short).  A short one is loaded as the 16 bytes that end with the row,
+// `back` elements early, and shifted into place once they are there: no byte beyond
+// the row is touched, and the loads of several rows are in flight together.  Only in
+// a row shorter than a vector (back 0, valid short) are elements loaded one by one.
+struct Col {
+    int64_t c;
+    int valid, back;
+};
+
 template <typename T>
-__device__ __forceinline__ u32x4 load_raw(const T *p, int valid)
+__device__ __forceinline__ Col col_of(int64_t cols, int64_t c)
 {
-    if (valid >= kVec<T>) return *reinterpret_cast<const u32x4_any *>(p);
+    const int valid = cols - c < kVec<T> ? (int)(cols - c) : kVec<T>;
+    return {c, valid, valid > 0 && c >= kVec<T> - valid ? kVec<T> - valid : 0};
+}
+
+// Right shift of 16 bytes by a number of elements, zeros shifted in.
+template <typename T>
+__device__ __forceinline__ u32x4 shift_down(u32x4 r, int elements)
+{
+    const int bytes = elements * (int)sizeof(T);
+    if (bytes & 8) r = u32x4{r[2], r[3], 0u, 0u};
+    if (bytes & 4) r = u32x4{r[1], r[2], r[3], 0u};
+    if constexpr (sizeof(T) == 2)
+        if (bytes & 2)
+            r = u32x4{r[0] >> 16 | r[1] << 16, r[1] >> 16 | r[2] << 16, r[2] >> 16 | r[3] << 16, r[3] >> 16};
+    return r;
+}
+
+// Loads a vector of a row.  NT: past the caches, for rows that are read once and more
+// of them than the L2s hold.  settle() puts what was loaded into place: elements
+// 0..valid - 1, zeros after them.
+template <typename T, bool NT = false>
+__device__ __forceinline__ u32x4 issue(const T *row, const Col &col)
+{
+    if (col.valid + col.back == kVec<T>) {
+        const u32x4_any *p = reinterpret_cast<const u32x4_any *>(row + (col.c - col.back));
+        if constexpr (NT) return __builtin_nontemporal_load(p);
+        return *p;
+    }
     u32x4 r = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int e = 0; e < kVec<T>; ++e) {
-        if (e < valid) {
+    for (int e = 0; e < kVec<T>; ++e)
+        if (e < col.valid) {
             if constexpr (sizeof(T) == 4)
-                r[e] = reinterpret_cast<const uint32_t *>(p)[e];
+                r[e] = reinterpret_cast<const uint32_t *>(row + col.c)[e];
             else
-                r[e / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[e] << (16 * (e & 1));
+                r[e / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(row + col.c)[e] << (16 * (e & 1));
         }
-    }
     return r;
 }
 
 template <typename T>
+__device__ __forceinline__ u32x4 settle(u32x4 r, const Col &col)
+{
+    return col.back > 0 ? shift_down<T>(r, col.back) : r;
+}
+
+template <typename T, bool NT = false>
+__device__ __forceinline__ u32x4 load_col(const T *row, const Col &col)
+{
+    return settle<T>(issue<T, NT>(row, col), col);
+}
+
+// Stores `valid` elements at p: one store, or one for each bit of a short count.
+template <typename T, bool NT = false>
 __device__ __forceinline__ void store_raw(T *p, u32x4 r, int valid)
 {
     if (valid >= kVec<T>) {
-        *reinterpret_cast<u32x4_any *>(p) = r;
+        u32x4_any *q = reinterpret_cast<u32x4_any *>(p);
+        if constexpr (NT)
+            __builtin_nontemporal_store((u32x4_any)r, q);
+        else
+            *q = r;
         return;
     }
+    if (valid <= 0) return;
+    const int words = valid * (int)sizeof(T) / 4;  // whole ones
+    char *at = reinterpret_cast<char *>(p);
+    if (words & 2) *reinterpret_cast<u32x2_any *>(at) = u32x2_any{r[0], r[1]};
+    if (words & 1) *reinterpret_cast<u32_any *>(at + (words & 2) * 4) = words & 2 ? r[2] : r[0];
+    if constexpr (sizeof(T) == 2) {
+        if (valid & 1) {
+            uint32_t q = 0u;
 #pragma unroll
-    for (int e = 0; e < kVec<T>; ++e) {
-        if (e < valid) {
-            if constexpr (sizeof(T) == 4)
-                reinterpret_cast<uint32_t *>(p)[e] = r[e];
-            else
-                reinterpret_cast<uint16_t *>(p)[e] = (uint16_t)(r[e / 2] >> (16 * (e & 1)));
+            for (int w = 0; w < 4; ++w) q |= w == words ? r[w] : 0u;
+            reinterpret_cast<uint16_t *>(at)[valid - 1] = (uint16_t)q;
         }
     }
 }
 
-// The same past the caches (NT): for rows that are read or written once and more of
-// them than the L2 holds.
-template <bool NT, typename T>
-__device__ __forceinline__ u32x4 load_once(const T *p, int valid)
+template <typename T, bool NT = false>
+__device__ __forceinline__ void store_col(T *row, u32x4 r, const Col &col)
 {
-    if constexpr (NT)
-        if (valid >= kVec<T>) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(p));
-    return load_raw<T>(p, valid);
-}
-
-template <bool NT, typename T>
-__device__ __forceinline__ void store_once(T *p, u32x4 r, int valid)
-{
-    if constexpr (NT)
-        if (valid >= kVec<T>) {
-            __builtin_nontemporal_store((u32x4_any)r, reinterpret_cast<u32x4_any *>(p));
-            return;
-        }
-    store_raw<T>(p, r, valid);
+    store_raw<T, NT>(row + col.c, r, col.valid);
 }
 
 // Element e of a vector in float32 (exact for all three types).
@@ -170,20 +214,17 @@ __device__ __forceinline__ int64_t row_of(const Tiling &tl, int64_t tile)
                 if (const int64_t vec = (ct_ << (tl).tx_log2) + (threadIdx.x & ((1 << (tl).tx_log2) - 1)); \
                     vec < (tl).vecs)
 
-__device__ __forceinline__ int valid_of(int64_t cols, int64_t c, int vec)
-{
-    return cols - c < vec ? (int)(cols - c) : vec;
-}
-
 // ------------------------------------------------------------------ grouping
 
 // Keys of the grouping sort: id - first where that is below `groups`, else
-// `groups` (sorted last), and the indices that travel with them.
+// `groups` (sorted last), and the indices that travel with them.  `clear`, where
+// given, is a word that the first kernel of an order sets to zero for a later one.
 template <typename ID>
 __global__ __launch_bounds__(kThreads) void group_keys_kernel(const ID *__restrict__ ids, int64_t n, int64_t first,
                                                               uint32_t groups, uint32_t *__restrict__ keys,
-                                                              uint32_t *__restrict__ index)
+                                                              uint32_t *__restrict__ index, uint32_t *clear)
 {
+    if (clear != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *clear = 0;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
         const uint64_t g = (uint64_t)ids[i] - (uint64_t)first;
         keys[i] = g < groups ? (uint32_t)g : groups;
@@ -231,12 +272,11 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(const T *__restrict_
 {
     LRS_FOR_TILES(tl, tokens, t, vec)
     {
-        const int64_t c = vec * kVec<T>;
-        const int valid = valid_of(cols, c, kVec<T>);
-        const u32x4 v = load_raw<T>(x + t * ld_x + c, valid);
+        const Col col = col_of<T>(cols, vec * kVec<T>);
+        const u32x4 v = load_col<T>(x + t * ld_x, col);
         for (int k = 0; k < slots; ++k) {
             const uint32_t p = (uint32_t)position[t * slots + k];
-            if (p < num_rows) store_raw<T>(rows + (int64_t)p * ld_rows + c, v, valid);
+            if (p < num_rows) store_col<T>(rows + (int64_t)p * ld_rows, v, col);
         }
     }
 }
@@ -252,8 +292,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const T *__restrict__
 {
     LRS_FOR_TILES(tl, tokens, t, vec)
     {
-        const int64_t c = vec * kVec<T>;
-        const int valid = valid_of(cols, c, kVec<T>);
+        const Col col = col_of<T>(cols, vec * kVec<T>);
         float sum[kVec<T>] = {};
         for (int k0 = 0; k0 < slots; k0 += SLOTS) {
             uint32_t p[SLOTS];
@@ -263,18 +302,19 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const T *__restrict__
             for (int u = 0; u < SLOTS; ++u) {
                 p[u] = k0 + u < slots ? (uint32_t)position[t * slots + k0 + u] : ~0u;
                 if (p[u] < num_rows) {
-                    r[u] = load_once<NT>(rows + (int64_t)p[u] * ld_rows + c, valid);
+                    r[u] = issue<T, NT>(rows + (int64_t)p[u] * ld_rows, col);
                     w[u] = weights != nullptr ? load_scalar(weights, weight_type, t * slots + k0 + u) : 1.0f;
                 }
             }
 #pragma unroll
             for (int u = 0; u < SLOTS; ++u)
                 if (p[u] < num_rows) {
+                    const u32x4 v = settle<T>(r[u], col);
 #pragma unroll
-                    for (int e = 0; e < kVec<T>; ++e) sum[e] = __builtin_fmaf(w[u], element<T>(r[u], e), sum[e]);
+                    for (int e = 0; e < kVec<T>; ++e) sum[e] = __builtin_fmaf(w[u], element<T>(v, e), sum[e]);
                 }
         }
-        store_once<NT>(y + t * ld_y + c, pack<T>(sum), valid);
+        store_col<T, NT>(y + t * ld_y, pack<T>(sum), col);
     }
 }
 
@@ -326,18 +366,19 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(const T *__restr
             if (p < num_rows) {
                 const float w = weights != nullptr ? load_scalar(weights, weight_type, t * slots + k) : 1.0f;
                 for (int64_t vec = lane; vec < tl.vecs; vec += 1 << tl.tx_log2) {
-                    const int64_t c = vec * kVec<T>;
-                    const int valid = valid_of(cols, c, kVec<T>);
-                    const u32x4 g = load_raw<T>(grad_y + t * ld_grad_y + c, valid);
-                    if (grad_weights != nullptr) {
-                        const u32x4 r = load_once<NT>(rows + (int64_t)p * ld_rows + c, valid);
-#pragma unroll
-                        for (int e = 0; e < kVec<T>; ++e) dot = __builtin_fmaf(element<T>(g, e), element<T>(r, e), dot);
-                    }
+                    const Col col = col_of<T>(cols, vec * kVec<T>);
+                    u32x4 g = issue<T>(grad_y + t * ld_grad_y, col);
+                    u32x4 r = {0u, 0u, 0u, 0u};
+                    if (grad_weights != nullptr) r = issue<T, NT>(rows + (int64_t)p * ld_rows, col);
+                    g = settle<T>(g, col);
+                    r = settle<T>(r, col);
                     float out[kVec<T>];
 #pragma unroll
-                    for (int e = 0; e < kVec<T>; ++e) out[e] = w * element<T>(g, e);
-                    store_once<NT>(grad_rows + (int64_t)p * ld_grad_rows + c, pack<T>(out), valid);
+                    for (int e = 0; e < kVec<T>; ++e) {
+                        dot = __builtin_fmaf(element<T>(g, e), element<T>(r, e), dot);
+                        out[e] = w * element<T>(g, e);
+                    }
+                    store_col<T, NT>(grad_rows + (int64_t)p * ld_grad_rows, pack<T>(out), col);
                 }
             }
             if (grad_weights == nullptr) continue;
@@ -366,12 +407,11 @@ __global__ __launch_bounds__(kThreads) void embedding_kernel(const T *__restrict
 {
     LRS_FOR_TILES(tl, n, i, vec)
     {
-        const int64_t c = vec * kVec<T>;
-        const int valid = valid_of(cols, c, kVec<T>);
+        const Col col = col_of<T>(cols, vec * kVec<T>);
         const uint64_t v = (uint64_t)ids[i] - (uint64_t)first;
         u32x4 r = {0u, 0u, 0u, 0u};
         if (v < num_ids) {
-            r = load_raw<T>(table + (int64_t)v * ld_table + c, valid);
+            r = load_col<T>(table + (int64_t)v * ld_table, col);
             if (scale != 1.0f) {
                 float out[kVec<T>];
 #pragma unroll
@@ -379,21 +419,27 @@ __global__ __launch_bounds__(kThreads) void embedding_kernel(const T *__restrict
                 r = pack<T>(out);
             }
         }
-        store_once<NT>(y + i * ld_y + c, r, valid);
+        store_col<T, NT>(y + i * ld_y, r, col);
     }
 }
 
 // The gradient's sums.  The sorted ids are cut into pieces of `piece` slots, one
 // piece of a column tile per unit of work, whatever the ids: a run of equal ids may
-// be one slot or all of them, and pieces stay equal.  A run inside a piece is summed
-// in registers and stored at once.  A run that crosses pieces leaves one float32
-// partial sum in each: slot 0 of a piece for a run that began earlier, slot 1 for one
-// that begins in it and goes on; embedding_join_kernel adds them up, in order.
+// be one slot or all of them, and no unit sums more than two pieces' slots.  A run is
+// summed in registers and stored at once by the piece in which it begins, also where
+// it goes on into the next one (which passes over it).  Only a run that goes on
+// beyond that is left as float32 partial sums, one for each piece that it touches:
+// slot 1 of the piece in which it begins, slot 0 of those after it.  The piece in
+// which it begins also enters itself in a list (in any order: each run is joined by
+// itself), and embedding_join_kernel adds the run's sums up, in order.
+constexpr int kKeyPad = 16;
+
 struct Pieces {
     int64_t n;        // sorted slots
     int piece;        // slots per piece
     int64_t count;    // pieces
     uint32_t groups;  // ids at or above it are of no row (sorted last)
+    uint32_t *list;   // its length (0 before), then the pieces in which a long run begins
 };
 
 template <typename G, int E>
@@ -404,116 +450,178 @@ __device__ __forceinline__ void store_values(G *p, const float (&v)[E], int vali
         float part[kVec<G>];
 #pragma unroll
         for (int e = 0; e < kVec<G>; ++e) part[e] = v[q + e];
-        if (valid > q) store_raw<G>(p + q, pack<G>(part), valid - q);
+        store_raw<G>(p + q, pack<G>(part), valid - q);
     }
 }
 
-// scale * sum, added to what is there if `accumulate`, rounded once.
+// scale * sum, added to what is there if `accumulate`, rounded once.  The columns are
+// those of a vector of E elements, one vector of G or two.
 template <typename G, int E>
-__device__ __forceinline__ void store_grad(G *p, const float (&sum)[E], float scale, int accumulate, int valid)
+__device__ __forceinline__ void store_grad(G *row, const float (&sum)[E], float scale, int accumulate, int64_t cols,
+                                           const Col &col)
 {
     float v[E];
     if (accumulate) {
+        u32x4 old[E / kVec<G>];
 #pragma unroll
-        for (int q = 0; q < E; q += kVec<G>) {
-            const u32x4 old = load_raw<G>(p + q, valid - q);
+        for (int q = 0; q < E / kVec<G>; ++q) old[q] = issue<G>(row, col_of<G>(cols, col.c + q * kVec<G>));
 #pragma unroll
-            for (int e = 0; e < kVec<G>; ++e) v[q + e] = __builtin_fmaf(scale, sum[q + e], element<G>(old, e));
+        for (int q = 0; q < E / kVec<G>; ++q) {
+            const u32x4 r = settle<G>(old[q], col_of<G>(cols, col.c + q * kVec<G>));
+#pragma unroll
+            for (int e = 0; e < kVec<G>; ++e)
+                v[q * kVec<G> + e] = __builtin_fmaf(scale, sum[q * kVec<G> + e], element<G>(r, e));
         }
     } else {
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = scale * sum[e];
     }
-    store_values<G, E>(p, v, valid);
+    store_values<G, E>(row + col.c, v, col.valid);
 }
 
-template <typename T, typename G, bool WAVE_ROW>
-__device__ void sum_piece(const T *__restrict__ grad_y, int64_t ld_grad_y, const uint32_t *__restrict__ keys,
+template <typename T, typename G, bool NT>
+__device__ __forceinline__ void sum_piece(const T *__restrict__ grad_y, int64_t ld_grad_y, const uint32_t *__restrict__ keys,
                           const uint32_t *__restrict__ order, Pieces pc, float scale, G *__restrict__ grad,
                           int64_t ld_grad, int64_t cols, int64_t cols_padded, float *__restrict__ partial,
                           int accumulate, int64_t piece, int64_t vec)
 {
     constexpr int E = kVec<T>;
-    constexpr int UNROLL = 8;  // rows in flight per lane
-    const int64_t c = vec * E;
-    const int valid = valid_of(cols, c, E);
+        constexpr int UNROLL = 8;  // rows in flight per lane (4: 16,384 x 2048 added in 75 us instead of 69)
+    const Col col = col_of<T>(cols, vec * E);
     const int64_t lo = piece * pc.piece;
-    int64_t hi = lo + pc.piece < pc.n ? lo + pc.piece : pc.n;
+    const int64_t hi = lo + pc.piece < pc.n ? lo + pc.piece : pc.n;
     uint32_t run = keys[lo];
     bool here = lo == 0 || keys[lo - 1] != run;  // the run begins in this piece
+    // It began in the piece before and ends in this one, or with it: passed over.
+    bool passed = !here && (lo == pc.piece || keys[lo - pc.piece - 1] != run) && (hi == pc.n || keys[hi] != run);
+    // The piece's last run is its own to the end if it began here and ends in the next.
+    const uint32_t last = keys[hi - 1];
+    int64_t more = hi;
+    bool goes_on = false;
+    if (hi < pc.n && keys[hi] == last) {
+        const int64_t next = hi + pc.piece < pc.n ? hi + pc.piece : pc.n;
+        goes_on = (lo > 0 && keys[lo - 1] == last) || (next < pc.n && keys[next] == last);
+        if (!goes_on) more = next;
+    }
     float sum[E] = {};
-    auto leave = [&](bool goes_on) {
-        if (run >= pc.groups) return;
-        if (here && !goes_on)
-            store_grad<G, E>(grad + (int64_t)run * ld_grad + c, sum, scale, accumulate, valid);
+    auto leave = [&](bool partly) {
+        if (run >= pc.groups || passed) return;
+        if (here && !partly)
+            store_grad<G, E>(grad + (int64_t)run * ld_grad, sum, scale, accumulate, cols, col);
         else  // (padded rows of whole vectors: no partial store)
-            store_values<float, E>(partial + (piece * 2 + (here ? 1 : 0)) * cols_padded + c, sum, E);
+            store_values<float, E>(partial + (piece * 2 + (here ? 1 : 0)) * cols_padded + col.c, sum, E);
     };
-    for (int64_t j = lo; j < hi && run < pc.groups; j += UNROLL) {
+    bool on = true;
+    for (int64_t j = lo; on; j += UNROLL) {
+        // (keys and order have kKeyPad words more than the slots)
+        uint32_t key[UNROLL], at[UNROLL];
         u32x4 r[UNROLL];
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u)
-            if (j + u < hi && keys[j + u] < pc.groups)
-                r[u] = load_raw<T>(grad_y + (int64_t)order[j + u] * ld_grad_y + c, valid);
+        for (int u = 0; u < UNROLL; ++u) key[u] = keys[j + u], at[u] = order[j + u];
+        bool of[UNROLL];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
-            if (j + u < hi) {
-                const uint32_t k = keys[j + u];
-                if (k != run) {
+            on = on && key[u] < pc.groups && (j + u < hi || (j + u < more && key[u] == last));
+            of[u] = on;
+            if (on && !(passed && key[u] == run)) r[u] = issue<T, NT>(grad_y + (int64_t)at[u] * ld_grad_y, col);
+        }
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            if (of[u]) {
+                if (key[u] != run) {
                     leave(false);
-                    run = k;
+                    run = key[u];
                     here = true;
+                    passed = false;
 #pragma unroll
                     for (int e = 0; e < E; ++e) sum[e] = 0.0f;
                 }
-                if (k < pc.groups) {
+                if (!passed) {
+                    const u32x4 v = settle<T>(r[u], col);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) sum[e] += element<T>(r[u], e);
+                    for (int e = 0; e < E; ++e) sum[e] += element<T>(v, e);
                 }
             }
         }
     }
-    leave(hi < pc.n && keys[hi] == run);
+    // (ids of no row may follow the last run summed, and be a long run themselves)
+    goes_on = goes_on && run == last && run < pc.groups;
+    leave(goes_on);
+    if (goes_on && here && vec == 0) pc.list[1 + atomicAdd(pc.list, 1u)] = (uint32_t)piece;
+}
+
+// First j with keys[j] >= g, by a whole wave: 64 probes a step.
+__device__ __forceinline__ int64_t wave_lower_bound(const uint32_t *__restrict__ keys, int64_t n, uint32_t g)
+{
+    const int lane = threadIdx.x & (kWave - 1);
+    int64_t lo = 0, hi = n;  // keys[lo - 1] < g <= keys[hi]
+    while (lo < hi) {
+        const int64_t step = (hi - lo + kWave - 1) / kWave, at = lo + (lane + 1) * step - 1;
+        const int below = __popcll(__ballot(at < hi && keys[at] < g));  // the first `below` probes
+        lo += below * step;
+        hi = lo + step - 1 < hi ? lo + step - 1 : hi;
+    }
+    return lo;
 }
 
 // Rows that no id names are zeros.  A workgroup looks kFillRows rows up in the
-// sorted ids (one lane each) and stores those that are not there.
-constexpr int kFillRows = 32;
+// sorted ids and stores those that are not there: two waves find where the first and
+// the row past the last belong, and a lane per row looks between.
+constexpr int kFillRows = 16;
 
 template <typename G>
-__device__ void fill_rows(const uint32_t *__restrict__ keys, int64_t n, G *__restrict__ grad, int64_t ld_grad,
-                          int64_t num_ids, int64_t cols, int64_t tile)
+__device__ __forceinline__ void fill_rows(const uint32_t *__restrict__ keys, int64_t n, G *__restrict__ grad, int64_t ld_grad,
+                          int64_t num_ids, int64_t cols, int64_t tile, const Tiling &tl)
 {
+    __shared__ int64_t s_range[2];
     __shared__ int s_named[kFillRows];
+    __syncthreads();
+    if (threadIdx.x < 2 * kWave) {
+        const int end = threadIdx.x / kWave;
+        const int64_t v = (tile + end) * kFillRows;
+        const int64_t j = wave_lower_bound(keys, n, (uint32_t)(v < num_ids ? v : num_ids));
+        if ((threadIdx.x & (kWave - 1)) == 0) s_range[end] = j;
+    }
     __syncthreads();
     if (threadIdx.x < kFillRows) {
         const int64_t v = tile * kFillRows + threadIdx.x;
         int named = 1;
         if (v < num_ids) {
-            const int64_t j = lower_bound(keys, n, (uint32_t)v);
-            named = j < n && keys[j] == (uint32_t)v;
+            int64_t lo = s_range[0], hi = s_range[1];
+            const int64_t end = hi;
+            while (lo < hi) {
+                const int64_t mid = (lo + hi) >> 1;
+                if (keys[mid] < (uint32_t)v)
+                    lo = mid + 1;
+                else
+                    hi = mid;
+            }
+            named = lo < end && keys[lo] == (uint32_t)v;
         }
         s_named[threadIdx.x] = named;
     }
     __syncthreads();
     const u32x4 zero = {0u, 0u, 0u, 0u};
-    for (int q = 0; q < kFillRows; ++q) {
+    const int rows_at_once = kThreads >> tl.tx_log2, lane = threadIdx.x & ((1 << tl.tx_log2) - 1);
+    for (int q = threadIdx.x >> tl.tx_log2; q < kFillRows; q += rows_at_once) {
         if (s_named[q]) continue;
         G *row = grad + (tile * kFillRows + q) * ld_grad;
-        for (int64_t c = (int64_t)threadIdx.x * kVec<G>; c < cols; c += kThreads * kVec<G>)
-            store_raw<G>(row + c, zero, valid_of(cols, c, kVec<G>));
+        for (int64_t vec = lane; vec < tl.vecs; vec += 1 << tl.tx_log2) {
+            const int64_t c = vec * kVec<G>;
+            store_col<G>(row, zero, col_of<G>(cols, c));
+        }
     }
 }
 
 // The first `sum_blocks` workgroups sum pieces, the others write the empty rows.
-template <typename T, typename G, bool WAVE_ROW>
+template <typename T, typename G, bool WAVE_ROW, bool NT>
 __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(const T *__restrict__ grad_y, int64_t ld_grad_y,
                                                                   const uint32_t *__restrict__ keys,
                                                                   const uint32_t *__restrict__ order, Pieces pc,
                                                                   float scale, G *__restrict__ grad, int64_t ld_grad,
                                                                   int64_t num_ids, int64_t cols, int64_t cols_padded,
                                                                   float *__restrict__ partial, int accumulate,
-                                                                  uint32_t sum_blocks, Tiling tl)
+                                                                  uint32_t sum_blocks, Tiling tl, Tiling fill)
 {
     if (blockIdx.x < sum_blocks) {
         const int64_t units = tl.row_tiles * tl.col_tiles;
@@ -521,20 +629,22 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(const T *__res
             const int64_t piece = row_of<WAVE_ROW>(tl, unit / tl.col_tiles);
             const int64_t vec = ((unit % tl.col_tiles) << tl.tx_log2) + (threadIdx.x & ((1 << tl.tx_log2) - 1));
             if (piece < pc.count && vec < tl.vecs)
-                sum_piece<T, G, WAVE_ROW>(grad_y, ld_grad_y, keys, order, pc, scale, grad, ld_grad, cols, cols_padded,
+                sum_piece<T, G, NT>(grad_y, ld_grad_y, keys, order, pc, scale, grad, ld_grad, cols, cols_padded,
                                           partial, accumulate, piece, vec);
         }
     } else {
         const int64_t tiles = (num_ids + kFillRows - 1) / kFillRows;
         for (int64_t t = blockIdx.x - sum_blocks; t < tiles; t += gridDim.x - sum_blocks)
-            fill_rows<G>(keys, pc.n, grad, ld_grad, num_ids, cols, t);
+            fill_rows<G>(keys, pc.n, grad, ld_grad, num_ids, cols, t, fill);
     }
 }
 
-// Adds the partial sums of each run that crosses pieces: the workgroup of the piece
-// in which the run begins takes that piece's partial and those of the pieces after
-// it, four waves a quarter of them each, their sums joined in order.  64 vectors of
-// four columns per workgroup.
+// Adds the partial sums of each long run, in order: the one of the piece in which it
+// begins and those of the pieces after it.  A workgroup takes a run's 128 columns (32
+// lanes of four); eight slices of the workgroup add a contiguous part of the pieces
+// each, and their sums are joined in order.
+constexpr int kJoinLanes = 32;
+
 template <typename G>
 __global__ __launch_bounds__(kThreads) void embedding_join_kernel(const uint32_t *__restrict__ keys, Pieces pc,
                                                                   float scale, G *__restrict__ grad, int64_t ld_grad,
@@ -542,61 +652,54 @@ __global__ __launch_bounds__(kThreads) void embedding_join_kernel(const uint32_t
                                                                   const float *__restrict__ partial, int accumulate,
                                                                   int64_t col_tiles)
 {
-    constexpr int SLICES = kThreads / kWave;
-    __shared__ float s_sum[SLICES][kWave][4];
-    const int64_t units = (pc.count - 1) * col_tiles;
-    const int lane = threadIdx.x & (kWave - 1), slice = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    constexpr int LANES = kJoinLanes, SLICES = kThreads / LANES;
+    __shared__ float s_sum[SLICES][LANES][4];
+    __shared__ int64_t s_more;
+    const int lane = threadIdx.x & (LANES - 1), slice = threadIdx.x / LANES;
+    const int64_t units = (int64_t)pc.list[0] * col_tiles;
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const int64_t piece = unit / col_tiles;
-        const int64_t lo = piece * pc.piece, hi = lo + pc.piece;  // (the last piece is not among them)
-        const uint32_t run = keys[hi - 1];
-        if (run >= pc.groups || keys[hi] != run || (keys[lo] == run && lo > 0 && keys[lo - 1] == run)) continue;
-        // the run's last slot, then its last piece
-        int64_t a = hi, b = pc.n;  // keys[a] == run; b: past the end
-        while (b - a > 1) {
-            const int64_t mid = (a + b) >> 1;
-            if (keys[mid] == run)
-                a = mid;
-            else
-                b = mid;
+        const int64_t piece = pc.list[1 + unit / col_tiles];
+        const uint32_t run = keys[(piece + 1) * pc.piece];
+        if (threadIdx.x < kWave) {  // how many pieces after it begin with the run
+            int64_t more = 2;
+            for (;;) {
+                const int64_t q = piece + 1 + more + threadIdx.x;
+                const uint64_t same = __ballot(q < pc.count && keys[q * pc.piece] == run);
+                const int on = same == ~0ull ? kWave : __builtin_ctzll(~same);
+                more += on;
+                if (on < kWave) break;
+            }
+            if (threadIdx.x == 0) s_more = more;
         }
-        const int64_t last = a / pc.piece, more = last - piece;  // pieces after the first
-        const int64_t per = (more + SLICES - 1) / SLICES;
-        const int64_t from = piece + 1 + slice * per, to = from + per < last + 1 ? from + per : last + 1;
-        const int64_t c = ((unit % col_tiles) * kWave + lane) * 4;
+        __syncthreads();
+        const int64_t c = ((unit % col_tiles) * LANES + lane) * 4;
+        // parts 0 .. s_more: the first piece's slot 1, then slot 0 of those after it
+        const int64_t parts = s_more + 1, per = (parts + SLICES - 1) / SLICES;
+        const int64_t from = slice * per, to = from + per < parts ? from + per : parts;
         float sum[4] = {};
         if (c < cols) {
-            if (slice == 0) {
-                const u32x4 r = load_raw<float>(partial + (piece * 2 + 1) * cols_padded + c, 4);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sum[e] = element<float>(r, e);
-            }
 #pragma unroll 8
-            for (int64_t p = from; p < to; ++p) {
-                const u32x4 r = load_raw<float>(partial + p * 2 * cols_padded + c, 4);
+            for (int64_t q = from; q < to; ++q) {
+                const u32x4 r = *reinterpret_cast<const u32x4 *>(partial + ((piece + q) * 2 + (q == 0)) * cols_padded + c);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sum[e] += element<float>(r, e);
             }
         }
-        if (more > 1) {  // else the first wave has it all
-            __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s_sum[slice][lane][e] = sum[e];
-            __syncthreads();
-            if (slice == 0) {
-                for (int w = 1; w < SLICES; ++w)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sum[e] += s_sum[w][lane][e];
-            }
-        }
+        for (int e = 0; e < 4; ++e) s_sum[slice][lane][e] = sum[e];
+        __syncthreads();
         if (slice == 0 && c < cols) {
-            const int valid = valid_of(cols, c, 4);
-            G *p = grad + (int64_t)run * ld_grad + c;
+            const int64_t used = (parts + per - 1) / per;
+            for (int64_t w = 1; w < used; ++w)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] += s_sum[w][lane][e];
             // (four columns are half a vector of 16-bit elements: element by element)
+            G *p = grad + (int64_t)run * ld_grad + c;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (e < valid) p[e] = (G)(accumulate ? __builtin_fmaf(scale, sum[e], (float)p[e]) : scale * sum[e]);
+                if (c + e < cols) p[e] = (G)(accumulate ? __builtin_fmaf(scale, sum[e], (float)p[e]) : scale * sum[e]);
         }
+        __syncthreads();
     }
 }
 

@@ -113,6 +113,10 @@ constexpr int64_t kFewTiles = 2048;
 // of 33 and 65 instead of 70; 512 tokens (38 MB) the same either way.
 bool streams(int64_t bytes) { return bytes > ((int64_t)32 << 20); }
 
+// A gradient of more bytes than the last-level cache is read past the L2s; a smaller
+// one may still be there from the kernel that wrote it.
+constexpr int64_t kLastCacheBytes = (int64_t)256 << 20;
+
 // LDS that a dispatch asks for and does not use, so that six workgroups fit a CU
 // and not eight: fewer rows are being written at once.  16,384 tokens x 8 x 4096
 // bf16 in 226 us instead of 245, 4,096 x 8 x 8192 in 115 instead of 128; rows of
@@ -155,53 +159,142 @@ lrs_status guarded(F &&f)
 
 // ------------------------------------------------------------------ grouping
 
-// Temp storage of a grouping: keys and indices before and after the sort, and the
-// sort's own.
+// Few ids are ordered by counting passes of this file's own: a grouping of up to 2048
+// groups in one, an embedding's ids in passes of up to nine bits.  The others take the
+// library's sort.
+constexpr int kFewBins = 513, kManyBins = 2049;
+constexpr int64_t kDirectGroups = kManyBins - 1, kDirectSlots = 1 << 20;
+
+// Blocks of 1024 slots, or 4096 from 32K slots (a block reads every block's counts,
+// so few blocks; a wave's ranking is what they share, so not too few).  Up to 4096
+// slots one block does without the count launch.
+constexpr int64_t kOneBlockSlots = 4 * kPlaceThreads, kSmallBlockSlots = 128 * kPlaceThreads;
+
+int place_items(int64_t n) { return n <= kPlaceThreads || (n > kOneBlockSlots && n <= kSmallBlockSlots) ? 1 : 4; }
+int place_blocks(int64_t n)
+{
+    const int64_t slots = (int64_t)kPlaceThreads * place_items(n);
+    return (int)std::max<int64_t>(1, (n + slots - 1) / slots);
+}
+
+template <int MAX_BINS, int ITEMS, typename SRC>
+lrs_status run_pass(const SRC &src, const Pass &ps, uint32_t *counts, const PlaceOut &out, uint32_t *clear,
+                    hipStream_t stream)
+{
+    const int blocks = place_blocks(ps.n);
+    if (blocks > 1) {
+        count_kernel<SRC, MAX_BINS, ITEMS><<<blocks, kPlaceThreads, 0, stream>>>(src, ps, counts, clear);
+        const lrs_status st = launched();
+        if (st != LRS_OK) return st;
+    }
+    place_kernel<SRC, MAX_BINS, ITEMS><<<blocks, kPlaceThreads, 0, stream>>>(src, ps, blocks > 1 ? counts : nullptr,
+                                                                             blocks, out);
+    return launched();
+}
+
+template <typename SRC>
+lrs_status run_pass(const SRC &src, const Pass &ps, uint32_t *counts, const PlaceOut &out, uint32_t *clear,
+                    hipStream_t stream)
+{
+    const bool one = place_items(ps.n) == 1;
+    if (ps.bins <= kFewBins)
+        return one ? run_pass<kFewBins, 1>(src, ps, counts, out, clear, stream)
+                   : run_pass<kFewBins, 4>(src, ps, counts, out, clear, stream);
+    return one ? run_pass<kManyBins, 1>(src, ps, counts, out, clear, stream)
+               : run_pass<kManyBins, 4>(src, ps, counts, out, clear, stream);
+}
+
+int bits_of(int64_t values)  // bits that hold 0..values - 1
+{
+    int bits = 0;
+    while (((int64_t)1 << bits) < values) ++bits;
+    return bits;
+}
+
+// Temp storage of an order of ids: keys and indices before and after sorting, and the
+// sort's own or the passes' counts.
 struct GroupLayout {
     size_t off_keys = 0, off_index = 0, off_sorted = 0, off_order = 0, off_sort = 0, sort_bytes = 0, total = 0;
     int bits = 0;
 };
 
+constexpr int64_t kDirectIds = 1 << 17;
+constexpr int kDigitBits = 9;
+
 lrs_status group_layout(int64_t n, int64_t groups, GroupLayout *L)
 {
-    L->bits = 0;
-    while (((int64_t)1 << L->bits) <= groups) ++L->bits;  // keys are 0..groups
-    const size_t words = align_up((size_t)n * 4);
+    L->bits = bits_of(groups + 1);  // keys are 0..groups
+    const size_t words = align_up((size_t)(n + kKeyPad) * 4);  // (the sums read some words past the end)
     size_t off = 0;
     L->off_keys = off, off += words;
     L->off_index = off, off += words;
     L->off_sorted = off, off += words;
     L->off_order = off, off += words;
     L->off_sort = off;
-    // the size depends on n and the bit range alone: any distinct pointers will do
-    const uintptr_t some = (uintptr_t)1 << 40;
-    const lrs_status st = lrs_sort_digits(LRS_KEY_U32, 8, nullptr, &L->sort_bytes, (const void *)some,
-                                          (const uint32_t *)(2 * some), (void *)(3 * some), (uint32_t *)(4 * some), n,
-                                          0, L->bits, nullptr);
+    lrs_status st = LRS_OK;
+    if (n <= kDirectIds) {
+        L->sort_bytes = (size_t)place_blocks(n) * ((size_t)1 << kDigitBits) * 4;
+    } else {
+        // the size depends on n and the bit range alone: any distinct pointers will do
+        const uintptr_t some = (uintptr_t)1 << 40;
+        st = lrs_sort_digits(LRS_KEY_U32, 8, nullptr, &L->sort_bytes, (const void *)some, (const uint32_t *)(2 * some),
+                             (void *)(3 * some), (uint32_t *)(4 * some), n, 0, L->bits, nullptr);
+    }
     L->total = off + L->sort_bytes;
     return st;
 }
 
-// The sorted keys and their indices in temp storage (indices also in `order` if it
-// is not NULL: it is then where they are).
-lrs_status sort_ids(const GroupLayout &L, char *temp, lrs_id_type id_type, const void *ids, int64_t n, int64_t first,
-                    int64_t groups, int32_t *order, const uint32_t **sorted, const uint32_t **index, hipStream_t stream)
+// The sorted keys and their indices (in `order` if that is not NULL, else in temp
+// storage).  The first kernel sets *clear to zero, where it is given.
+template <typename ID>
+lrs_status sort_ids(const GroupLayout &L, char *temp, const void *ids, int64_t n, int64_t first, int64_t groups,
+                    int32_t *order, const uint32_t **sorted, const uint32_t **index, uint32_t *clear, hipStream_t stream)
 {
     uint32_t *keys = (uint32_t *)(temp + L.off_keys), *at = (uint32_t *)(temp + L.off_index);
     uint32_t *out = (uint32_t *)(temp + L.off_sorted);
     uint32_t *ord = order != nullptr ? (uint32_t *)order : (uint32_t *)(temp + L.off_order);
     *sorted = out, *index = ord;
     if (n == 0) return LRS_OK;
-    if (id_type == LRS_ID_I32)
-        group_keys_kernel<int32_t><<<flat_grid(n), kThreads, 0, stream>>>((const int32_t *)ids, n, first, (uint32_t)groups,
-                                                                         keys, at);
-    else
-        group_keys_kernel<int64_t><<<flat_grid(n), kThreads, 0, stream>>>((const int64_t *)ids, n, first, (uint32_t)groups,
-                                                                         keys, at);
+    const IdSource<ID> src{(const ID *)ids, first, (uint32_t)groups};
+    if (n <= kDirectIds) {
+        const int passes = (std::max(L.bits, 1) + kDigitBits - 1) / kDigitBits;
+        const int width = (std::max(L.bits, 1) + passes - 1) / passes;
+        if (place_blocks(n) == 1) {
+            if (n <= kPlaceThreads)
+                order_kernel<ID, kFewBins, 1><<<1, kPlaceThreads, 0, stream>>>(src, (int)n, L.bits, width, out, ord, clear);
+            else
+                order_kernel<ID, kFewBins, 4><<<1, kPlaceThreads, 0, stream>>>(src, (int)n, L.bits, width, out, ord, clear);
+            return launched();
+        }
+        uint32_t *counts = (uint32_t *)(temp + L.off_sort);
+        for (int p = 0; p < passes; ++p) {
+            const int shift = p * width, bits = std::min(width, std::max(L.bits, 1) - shift);
+            const Pass ps{n, shift, bits, (1u << bits) - 1u, 1u << bits};
+            // the passes alternate between the two pairs of arrays so that the last
+            // one writes the sorted ones
+            const bool to_out = (passes - 1 - p) % 2 == 0;
+            const PlaceOut dst = to_out ? PlaceOut{out, ord, nullptr, nullptr} : PlaceOut{keys, at, nullptr, nullptr};
+            const PairSource from = to_out ? PairSource{keys, at} : PairSource{out, ord};
+            const lrs_status st = p == 0 ? run_pass(src, ps, counts, dst, clear, stream)
+                                         : run_pass(from, ps, counts, dst, nullptr, stream);
+            if (st != LRS_OK) return st;
+        }
+        return LRS_OK;
+    }
+    group_keys_kernel<ID><<<flat_grid(n), kThreads, 0, stream>>>((const ID *)ids, n, first, (uint32_t)groups, keys, at,
+                                                                clear);
     const lrs_status st = launched();
     if (st != LRS_OK) return st;
     size_t bytes = L.sort_bytes;
     return lrs_sort_digits(LRS_KEY_U32, 8, temp + L.off_sort, &bytes, keys, at, out, ord, n, 0, L.bits, stream);
+}
+
+lrs_status sort_ids(const GroupLayout &L, char *temp, lrs_id_type id_type, const void *ids, int64_t n, int64_t first,
+                    int64_t groups, int32_t *order, const uint32_t **sorted, const uint32_t **index, uint32_t *clear, hipStream_t stream)
+{
+    return id_type == LRS_ID_I32
+               ? sort_ids<int32_t>(L, temp, ids, n, first, groups, order, sorted, index, clear, stream)
+               : sort_ids<int64_t>(L, temp, ids, n, first, groups, order, sorted, index, clear, stream);
 }
 
 // The two-phase temp storage convention: LRS_OK with *temp NULL after a query.
@@ -218,62 +311,13 @@ lrs_status take_temp(void *d_temp, size_t *temp_bytes, size_t total, char **temp
     return LRS_OK;
 }
 
-// Groupings of few groups and slots take one counting pass of their own; the others
-// the sort (several passes, and a kernel before and after them).
-constexpr int kFewBins = 513, kManyBins = 2049;
-constexpr int64_t kDirectGroups = kManyBins - 1, kDirectSlots = 1 << 20;
-
-// Blocks of 1024 slots, or 4096 from 32K slots (a block reads every block's counts,
-// so few blocks; a wave's ranking is what they share, so not too few).  Up to 4096
-// slots one block does without the count launch.
-constexpr int64_t kOneBlockSlots = 4 * kPlaceThreads, kSmallBlockSlots = 32 * kPlaceThreads;
-
-int place_items(int64_t n) { return n <= kPlaceThreads || (n > kOneBlockSlots && n <= kSmallBlockSlots) ? 1 : 4; }
-int place_blocks(int64_t n)
-{
-    const int64_t slots = (int64_t)kPlaceThreads * place_items(n);
-    return (int)std::max<int64_t>(1, (n + slots - 1) / slots);
-}
-
-template <int MAX_BINS, int ITEMS, typename SRC>
-lrs_status run_pass(const SRC &src, const Pass &ps, uint32_t *counts, const PlaceOut &out, hipStream_t stream)
-{
-    const int blocks = place_blocks(ps.n);
-    if (blocks > 1) {
-        count_kernel<SRC, MAX_BINS, ITEMS><<<blocks, kPlaceThreads, 0, stream>>>(src, ps, counts);
-        const lrs_status st = launched();
-        if (st != LRS_OK) return st;
-    }
-    place_kernel<SRC, MAX_BINS, ITEMS><<<blocks, kPlaceThreads, 0, stream>>>(src, ps, blocks > 1 ? counts : nullptr,
-                                                                             blocks, out);
-    return launched();
-}
-
-template <typename SRC>
-lrs_status run_pass(const SRC &src, const Pass &ps, uint32_t *counts, const PlaceOut &out, hipStream_t stream)
-{
-    const bool one = place_items(ps.n) == 1;
-    if (ps.bins <= kFewBins)
-        return one ? run_pass<kFewBins, 1>(src, ps, counts, out, stream)
-                   : run_pass<kFewBins, 4>(src, ps, counts, out, stream);
-    return one ? run_pass<kManyBins, 1>(src, ps, counts, out, stream)
-               : run_pass<kManyBins, 4>(src, ps, counts, out, stream);
-}
-
-int bits_of(int64_t values)  // bits that hold 0..values - 1
-{
-    int bits = 0;
-    while (((int64_t)1 << bits) < values) ++bits;
-    return bits;
-}
-
 template <typename ID>
 lrs_status group_direct(const void *ids, int64_t n, int64_t first, int64_t groups, uint32_t *counts, int32_t *order,
                         int32_t *position, int32_t *offsets, hipStream_t stream)
 {
     const IdSource<ID> src{(const ID *)ids, first, (uint32_t)groups};
     const Pass ps{n, 0, bits_of(groups + 1), ~0u, (uint32_t)groups + 1};
-    return run_pass(src, ps, counts, PlaceOut{nullptr, (uint32_t *)order, position, offsets}, stream);
+    return run_pass(src, ps, counts, PlaceOut{nullptr, (uint32_t *)order, position, offsets}, nullptr, stream);
 }
 
 lrs_status group_entry(void *d_temp, size_t *temp_bytes, lrs_id_type id_type, const void *d_ids, int64_t n,
@@ -309,7 +353,7 @@ lrs_status group_entry(void *d_temp, size_t *temp_bytes, lrs_id_type id_type, co
         return group_direct<int64_t>(d_ids, n, first, groups, (uint32_t *)temp, order, position, offsets, stream);
     }
     const uint32_t *sorted, *index;
-    st = sort_ids(L, temp, id_type, d_ids, n, first, groups, order, &sorted, &index, stream);
+    st = sort_ids(L, temp, id_type, d_ids, n, first, groups, order, &sorted, &index, nullptr, stream);
     if (st != LRS_OK || (position == nullptr && offsets == nullptr)) return st;
     group_finish_kernel<<<flat_grid(std::max(n, groups + 1)), kThreads, 0, stream>>>(sorted, index, n, (uint32_t)groups,
                                                                                      position, offsets);
@@ -474,22 +518,30 @@ LRS_API lrs_status lrs_embedding(lrs_row_type type, const void *d_table, int64_t
 namespace {
 
 // How an embedding's gradient cuts the sorted ids: pieces of 16 to 512 slots, so
-// many that the chip has some 8192 waves of 64 vectors (a part of the rows in a
-// piece, twice as many partial sums at most), and the partial sums' place.
+// many that the chip has some 16384 waves of 64 vectors (more than it holds, so that
+// they even out: 65,536 x 4096 added in 220 us, 225 with half as many, 223 with
+// twice), and shorter ones where even so a SIMD has no wave (777 x 515 in 17 us
+// instead of 25; of 16,384 x 2048 with one id they would make 89 us of 49).  And the
+// place of the long runs' partial sums and list.
 struct SumLayout {
     int piece = 16;
     int64_t count = 0, cols_padded = 0;
-    size_t bytes = 0;
+    size_t partial_bytes = 0, list_bytes = 0;
+    bool joins() const { return count > 2; }  // a run can go on beyond a piece's next
 };
 
 SumLayout sum_layout(int64_t n, int64_t cols, int vec)
 {
     SumLayout S;
     const int64_t waves = std::max<int64_t>(1, ((cols + vec - 1) / vec + kWave - 1) / kWave);
-    while (S.piece < 512 && n / S.piece > 8192 / waves) S.piece *= 2;
+    while (S.piece < 512 && n / S.piece > 16384 / waves) S.piece *= 2;
+    while (S.piece > 2 && n / S.piece < 1024 / waves) S.piece /= 2;
     S.count = (n + S.piece - 1) / S.piece;
     S.cols_padded = (cols + vec - 1) / vec * vec;
-    S.bytes = S.count > 1 ? (size_t)S.count * 2 * (size_t)S.cols_padded * 4 : 0;
+    if (S.joins()) {
+        S.partial_bytes = align_up((size_t)S.count * 2 * (size_t)S.cols_padded * 4);
+        S.list_bytes = (size_t)(S.count + 1) * 4;
+    }
     return S;
 }
 
@@ -512,30 +564,36 @@ lrs_status embedding_grad_entry(void *d_temp, size_t *temp_bytes, lrs_row_type t
     if (st != LRS_OK) return st;
     const SumLayout S = sum_layout(n, cols, (int)(16 / b));
     char *temp;
-    st = take_temp(d_temp, temp_bytes, align_up(L.total) + S.bytes, &temp);
+    st = take_temp(d_temp, temp_bytes, align_up(L.total) + S.partial_bytes + S.list_bytes, &temp);
     if (st != LRS_OK || temp == nullptr) return st;
     if (num_ids == 0 || cols == 0 || (n == 0 && accumulate)) return LRS_OK;
     const uint32_t *sorted, *index;
-    st = sort_ids(L, temp, id_type, d_ids, n, first, num_ids, nullptr, &sorted, &index, stream);
-    if (st != LRS_OK) return st;
     float *partial = (float *)(temp + align_up(L.total));
-    const Pieces pc{n, S.piece, S.count, (uint32_t)num_ids};
+    uint32_t *list = (uint32_t *)(temp + align_up(L.total) + S.partial_bytes);
+    st = sort_ids(L, temp, id_type, d_ids, n, first, num_ids, nullptr, &sorted, &index, S.joins() ? list : nullptr, stream);
+    if (st != LRS_OK) return st;
+    const Pieces pc{n, S.piece, S.count, (uint32_t)num_ids, list};
     return with_type(type, [&](auto elem) {
         using T = decltype(elem);
         auto run = [&](auto gelem) {
             using G = decltype(gelem);
             const Tiling t = tiling_of(S.count, cols, kVec<T>);
+            Tiling fill = tiling_of(num_ids, cols, kVec<G>);
+            fill.tx_log2 = std::min(fill.tx_log2, 6);  // a wave per row
             const unsigned sums = (unsigned)std::min(t.row_tiles * t.col_tiles, kMaxGridX);
             const unsigned fills =
                 accumulate ? 0u : (unsigned)std::min((num_ids + kFillRows - 1) / kFillRows, kMaxGridX);
-            auto *k = wave_row(t) ? embedding_grad_kernel<T, G, true> : embedding_grad_kernel<T, G, false>;
-            k<<<sums + fills, kThreads, 0, stream>>>((const T *)d_grad_y, ld_grad_y, sorted, index, pc, scale,
-                                                     (G *)d_grad, ld_grad, num_ids, cols, S.cols_padded, partial,
-                                                     accumulate, sums, t);
+            with_bool(wave_row(t), [&](auto wave) {
+                with_bool(n * cols * b > kLastCacheBytes, [&](auto nt) {
+                    embedding_grad_kernel<T, G, wave.value, nt.value><<<sums + fills, kThreads, 0, stream>>>(
+                        (const T *)d_grad_y, ld_grad_y, sorted, index, pc, scale, (G *)d_grad, ld_grad, num_ids, cols,
+                        S.cols_padded, partial, accumulate, sums, t, fill);
+                });
+            });
             const lrs_status st = launched();
-            if (st != LRS_OK || S.count < 2) return st;
-            const int64_t join_tiles = (cols + 4 * kWave - 1) / (4 * kWave);
-            const unsigned joins = (unsigned)std::min((S.count - 1) * join_tiles, kMaxGridX);
+            if (st != LRS_OK || !S.joins()) return st;
+            const int64_t join_tiles = (cols + 4 * kJoinLanes - 1) / (4 * kJoinLanes);
+            const unsigned joins = (unsigned)std::min<int64_t>((S.count + 1) / 2 * join_tiles, 4096);
             embedding_join_kernel<G><<<joins, kThreads, 0, stream>>>(sorted, pc, scale, (G *)d_grad, ld_grad, cols,
                                                                      S.cols_padded, partial, accumulate, join_tiles);
             return launched();

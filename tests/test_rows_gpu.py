@@ -471,6 +471,30 @@ def test_embedding_grad_of_long_runs(share):
     assert np.array_equal(got.cpu().numpy().astype(np.int64), want)
 
 
+@pytest.mark.parametrize("n", [1, 2, 3, 5, 31, 33, 63, 65, 127, 1023, 1024, 1025, 4096, 4097, 5000, 131072, 131073,
+                               200001])
+def test_embedding_grad_lengths(n):
+    """Whole numbers again: both sides of every length at which the ids are ordered
+    another way, ids of one to four digits, spread, in long runs, and of no row."""
+    torch = torch_()
+    rng = np.random.default_rng(n)
+    for vocab, cols, first in ((1, 8, 0), (300, 33, -7), (3000, 64, 5), (600000, 4, 0)):
+        announce("embedding grad of %d ids, vocab %d" % (n, vocab))
+        for kind in ("spread", "runs", "outside"):
+            ids = rng.integers(0, vocab, n)
+            if kind == "runs":
+                ids = ids // max(1, vocab // 5) * max(1, vocab // 5)
+            if kind == "outside":
+                ids = np.where(rng.random(n) < 0.9, rng.choice([-1, vocab, 2**40, -2**40], n), ids)
+            gy = rng.integers(-8, 9, (n, cols))
+            inside = (ids >= 0) & (ids < vocab)
+            want = np.zeros((vocab, cols), dtype=np.int64)
+            np.add.at(want, ids[inside], gy[inside])
+            got = lrs.embedding_grad(torch.from_numpy(gy).float().cuda(), torch.from_numpy(ids + first).cuda(), vocab,
+                                     first_id=first)
+            assert np.array_equal(got.cpu().numpy().astype(np.int64), want), kind
+
+
 # -------------------------------------------------------------------- together
 
 
