@@ -109,6 +109,19 @@ __device__ __forceinline__ uint32_t wave_rank(uint32_t digit, bool valid, int bi
     return rank;
 }
 
+// Adds the active lanes' digits to the counts in LDS.  A wave of one digit adds once:
+// 64 adds to one word would queue.
+__device__ __forceinline__ void count_digit(uint32_t *count, uint32_t digit)
+{
+    const uint32_t f = __builtin_amdgcn_readfirstlane(digit);
+    const uint64_t on = __ballot(1);
+    if (__ballot(digit != f) == 0) {
+        if (lanes_below(on) == 0) atomicAdd(&count[f], (uint32_t)__popcll(on));
+    } else {
+        atomicAdd(&count[digit], 1u);
+    }
+}
+
 // Digit counts of block b = slots [b * 1024 * ITEMS, ...), one row of `bins` each.
 // `clear`, where given, is a word set to zero for a later kernel.
 template <typename SRC, int MAX_BINS, int ITEMS>
@@ -126,16 +139,7 @@ __global__ __launch_bounds__(kPlaceThreads) void count_kernel(SRC src, Pass ps, 
         if (first + i * kPlaceThreads < ps.n) d[i] = digit_in(ps, src.key(first + i * kPlaceThreads));
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-        if (first + i * kPlaceThreads < ps.n) {
-            // a wave of one digit adds once: 64 adds to one word would queue
-            const uint32_t f = __builtin_amdgcn_readfirstlane(d[i]);
-            const uint64_t on = __ballot(1);
-            if (__ballot(d[i] != f) == 0) {
-                if (lanes_below(on) == 0) atomicAdd(&s_count[f], (uint32_t)__popcll(on));
-            } else {
-                atomicAdd(&s_count[d[i]], 1u);
-            }
-        }
+        if (first + i * kPlaceThreads < ps.n) count_digit(s_count, d[i]);
     }
     __syncthreads();
     for (uint32_t b = threadIdx.x; b < ps.bins; b += kPlaceThreads) counts[(int64_t)blockIdx.x * ps.bins + b] = s_count[b];
@@ -152,11 +156,12 @@ struct PlaceSmem {
 // Places of a block's slots, slot i of lane l of wave w being the block's
 // w * 64 * ITEMS + i * 64 + l, `valid` or not: a slot's place is its bin's start, plus
 // the bin's slots in earlier blocks, in earlier waves of the block and before it in
-// its wave.  `counts` holds every block's digit counts, or is NULL for a pass of one
-// block, which counts as it ranks.  Every thread calls it.
-template <int MAX_BINS, int ITEMS>
+// its wave.  `counts` holds every block's digit counts; where it is NULL, a block
+// counts the other blocks' slots itself (`other` gives a slot's key).  Every thread
+// calls it.
+template <int MAX_BINS, int ITEMS, typename KEY>
 __device__ __forceinline__ void place_slots(const Pass &ps, const uint32_t (&key)[ITEMS], const bool (&valid)[ITEMS],
-                                            const uint32_t *__restrict__ counts, int block, int blocks,
+                                            const uint32_t *__restrict__ counts, int block, int blocks, KEY other,
                                             int32_t *offsets, PlaceSmem<MAX_BINS> &s, uint32_t (&to)[ITEMS])
 {
     constexpr int PER = (MAX_BINS + kPlaceThreads - 1) / kPlaceThreads;
@@ -181,6 +186,21 @@ __device__ __forceinline__ void place_slots(const Pass &ps, const uint32_t (&key
             atomicAdd(&s.all[b], all);
             atomicAdd(&s.start[b], before);
         }
+    } else if (blocks > 1) {
+        constexpr int AHEAD = 4;
+        const int64_t mine = (int64_t)block * kPlaceThreads * ITEMS, after = mine + kPlaceThreads * ITEMS;
+        for (int64_t at = tid; at < ps.n; at += AHEAD * kPlaceThreads) {
+            uint32_t d[AHEAD];
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                if (at + u * kPlaceThreads < ps.n) d[u] = digit_in(ps, other(at + u * kPlaceThreads));
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                // (a wave's 64 slots are all before this block's, in it, or after)
+                const int64_t i = at + u * kPlaceThreads;
+                if (i < ps.n && (i < mine || i >= after)) count_digit(i < mine ? s.start : s.all, d[u]);
+            }
+        }
     }
     uint32_t rank[ITEMS];
 #pragma unroll
@@ -195,7 +215,8 @@ __device__ __forceinline__ void place_slots(const Pass &ps, const uint32_t (&key
             s.wave[w * ps.bins + b] = sum;
             sum += c;
         }
-        if (counts == nullptr) s.all[b] = sum;
+        // (counted here: the bin's slots before this block, in it, and after it)
+        if (counts == nullptr) s.all[b] += s.start[b] + sum;
     }
     __syncthreads();
     uint32_t mine[PER], total = 0;
@@ -227,8 +248,9 @@ __device__ __forceinline__ void place_slots(const Pass &ps, const uint32_t (&key
 // One block's share of a pass: slots [block * 1024 * ITEMS, ...).
 template <typename SRC, int MAX_BINS, int ITEMS>
 __global__ __launch_bounds__(kPlaceThreads) void place_kernel(SRC src, Pass ps, const uint32_t *__restrict__ counts,
-                                                              int blocks, PlaceOut out)
+                                                              int blocks, PlaceOut out, uint32_t *clear)
 {
+    if (clear != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *clear = 0;
     __shared__ PlaceSmem<MAX_BINS> s;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t first = (int64_t)blockIdx.x * kPlaceThreads * ITEMS + wave * 64 * ITEMS + lane;
@@ -239,7 +261,8 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(SRC src, Pass ps, 
         valid[i] = first + i * 64 < ps.n;
         if (valid[i]) key[i] = src.key(first + i * 64);
     }
-    place_slots<MAX_BINS, ITEMS>(ps, key, valid, counts, blockIdx.x, blocks, out.offsets, s, to);
+    place_slots<MAX_BINS, ITEMS>(ps, key, valid, counts, blockIdx.x, blocks, [&](int64_t i) { return src.key(i); },
+                                 out.offsets, s, to);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
         if (!valid[i]) continue;
@@ -272,7 +295,7 @@ __global__ __launch_bounds__(kPlaceThreads) void order_kernel(IdSource<ID> src, 
     for (int shift = 0; shift < bits; shift += digit_bits) {
         const int width = digit_bits < bits - shift ? digit_bits : bits - shift;
         const Pass ps{n, shift, width, (1u << width) - 1u, 1u << width};
-        place_slots<MAX_BINS, ITEMS>(ps, key, valid, nullptr, 0, 1, nullptr, s, to);
+        place_slots<MAX_BINS, ITEMS>(ps, key, valid, nullptr, 0, 1, [](int64_t) { return 0u; }, nullptr, s, to);
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i)
             if (valid[i]) s_key[to[i]] = key[i], s_value[to[i]] = value[i];

@@ -118,11 +118,13 @@ def lrs_embedding_grad(d_temp, temp_bytes, row_type, d_grad_y, ld_grad_y, id_typ
 # ------------------------------------------------------------- conveniences
 #
 # A decode step's calls take a few microseconds on the GPU, so what the host does for
-# each is kept short: type codes are looked up by the dtype itself, the C functions
-# are called with plain addresses, and the temp bytes of a size are asked for once.
+# each is kept short: type codes are looked up by the dtype itself, devices compared
+# by their index, the C functions called with plain addresses, and the temp bytes of
+# a size asked for once.
 
-_types = None  # {torch dtype: code}: (ids, rows)
+_types = None  # ({torch dtype: code} of ids, of rows, torch.int32)
 _needs: dict = {}  # temp bytes by sizes and types, which alone decide them
+_functions: dict = {}  # C functions of the loaded library
 
 
 def _type_codes():
@@ -146,9 +148,8 @@ def _row_code(name, dtype) -> int:
     return code
 
 
-def _same_device(device, name, t):
-    if t is not None and t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+def _elsewhere(name, t, other):
+    return ValueError("%s is on %s, expected %s" % (name, t.device, other.device))
 
 
 def _matrix(name, t):
@@ -158,10 +159,11 @@ def _matrix(name, t):
     return t.shape
 
 
-def _row_stride(t):
+def _row_stride(t, rows, cols):
     """Elements from one row to the next, or None if a row's elements are not next to
     each other or rows share memory."""
-    rows, cols = t.shape
+    if t.is_contiguous():
+        return cols
     step, one = t.stride()
     if cols > 1 and one != 1:
         return None
@@ -170,38 +172,37 @@ def _row_stride(t):
     return cols
 
 
-def _rows_in(t):
+def _rows_in(t, rows, cols):
     """A matrix argument as the library reads it, and its row stride: a copy where a
     row's elements are not next to each other."""
-    ld = _row_stride(t)
-    if ld is None:
-        t = t.contiguous()
-        ld = t.shape[1]
-    return t, ld
+    ld = _row_stride(t, rows, cols)
+    return (t, ld) if ld is not None else (t.contiguous(), cols)
 
 
-def _out_matrix(name, t, rows, cols, dtype, device):
-    """Row stride of an output matrix, which must have that shape (rows None: any
-    number), type and device."""
-    if t.dtype != dtype:
-        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+def _rows_out(name, t, rows, cols, like):
+    """(rows, row stride) of an output matrix, which must have that shape (rows None:
+    any number) and the type and device of `like`."""
+    if t.dtype is not like.dtype:
+        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, like.dtype))
     r, c = _matrix(name, t)
     if c != cols or (rows is not None and r != rows):
         raise ValueError("%s has shape %s, expected (%s, %d)" % (name, tuple(t.shape), "any" if rows is None else rows,
                                                                  cols))
-    ld = _row_stride(t)
+    ld = _row_stride(t, r, c)
     if ld is None:
         raise ValueError("%s must be contiguous within each row" % name)
-    _same_device(device, name, t)
-    return ld
+    if t.get_device() != like.get_device():
+        raise _elsewhere(name, t, like)
+    return r, ld
 
 
-def _position(position, device):
+def _position(position, like):
     if position.dtype is not (_types or _type_codes())[2]:
         raise TypeError("position must be int32, not %s" % position.dtype)
     if position.dim() != 2:
         raise ValueError("position must have the shape (tokens, slots), not %s" % (tuple(position.shape),))
-    _same_device(device, "position", position)
+    if position.get_device() != like.get_device():
+        raise _elsewhere("position", position, like)
     return position.contiguous()
 
 
@@ -210,71 +211,9 @@ def _weights(weights, position):
         return None, 0
     if weights.shape != position.shape:
         raise ValueError("weights have shape %s, position %s" % (tuple(weights.shape), tuple(position.shape)))
-    _same_device(position.device, "weights", weights)
+    if weights.get_device() != position.get_device():
+        raise _elsewhere("weights", weights, position)
     return weights.contiguous(), _row_code("weights", weights.dtype)
-
-
-class _On:
-    """Where a call runs if that is not simply the current stream of the current
-    device: the tensors' device is made current, and on another stream than the
-    current one the work waits for what the current one holds (inputs copied and
-    outputs allocated there), and the tensors are recorded on it, so that the caching
-    allocator does not hand their memory on while it is in use there."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.device, self.side = device, None
-        self.current = torch.cuda.current_stream(device)
-        self.handle = self.current.cuda_stream
-        if stream is not None:
-            handle = stream if isinstance(stream, int) else stream.cuda_stream
-            if handle != self.handle:
-                self.side = torch.cuda.ExternalStream(handle, device) if isinstance(stream, int) else stream
-                if self.side.device != device:
-                    raise ValueError("stream is on %s, the tensors on %s" % (self.side.device, device))
-                self.handle = handle
-
-    def call(self, fn, tensors, args) -> int:
-        import torch
-        if self.side is not None:
-            self.side.wait_stream(self.current)
-        with torch.cuda.device(self.device):
-            status = fn(*args, self.handle or None)
-        if self.side is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.side)
-        return status
-
-
-def _on(device, stream):
-    """None for the current stream of the current device, else an _On."""
-    import torch
-    if device.type != "cuda":
-        raise ValueError("lrsort needs device tensors, got a tensor on %s" % device)
-    if stream is None and torch.cuda.current_device() == device.index:
-        return None
-    return _On(device, stream)
-
-
-def _current_handle(device) -> int:
-    """Handle of the device's current stream: torch's own shortcut to it where there
-    is one (the Stream object that the public call builds takes 2 us)."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
-
-
-def _run(on, device, name, tensors, args) -> None:
-    """Calls the C function `name` with `args` and the stream; `tensors` are in use
-    until the stream has done it."""
-    fn = getattr(load_library(), name)
-    if on is None:
-        status = fn(*args, _current_handle(device) or None)
-    else:
-        status = on.call(fn, tensors, args)
-    if status:
-        _check(status, name)
 
 
 def _at(t):
@@ -282,23 +221,78 @@ def _at(t):
     return None if t is None else t.data_ptr() or None
 
 
-def _temp(name, sizes, args, device, temp):
+def _function(name):
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(load_library(), name)
+    return fn
+
+
+def _current_handle(index) -> int:
+    """Handle of a device's current stream: torch's own shortcut to it where there is
+    one (the Stream object that the public call builds takes 2 us)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _on_device(t) -> None:
+    if not t.is_cuda:
+        raise ValueError("lrsort needs device tensors, got a tensor on %s" % t.device)
+
+
+def _run(name, stream, tensors, args) -> None:
+    """Calls the C function `name` with `args` and the stream's handle, with the
+    device of the first of `tensors` current.  None is that device's current stream.
+    On another stream the work waits for what the current one holds (inputs copied
+    and outputs allocated there), and the tensors are recorded on it, so that the
+    caching allocator does not hand their memory on while it is in use there."""
+    import torch
+    fn = _function(name)
+    index = tensors[0].get_device()
+    if stream is None and torch.cuda.current_device() == index:
+        status = fn(*args, _current_handle(index) or None)
+        if status:
+            _check(status, name)
+        return
+    current = torch.cuda.current_stream(index)
+    handle = current.cuda_stream if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+    side = None
+    if handle != current.cuda_stream:
+        side = torch.cuda.ExternalStream(handle, index) if isinstance(stream, int) else stream
+        if side.device.index != index:
+            raise ValueError("stream is on %s, the tensors on %s" % (side.device, tensors[0].device))
+        side.wait_stream(current)
+    with torch.cuda.device(index):
+        _check(fn(*args, handle or None), name)
+    if side is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(side)
+
+
+def _temp(name, sizes, args, like, temp):
     """Temp storage for the C call `name` (args: what follows temp_bytes, without the
-    stream), and its size.  `sizes`: what the size depends on."""
+    stream), and its size.  `sizes`: what the size depends on.  255 bytes are the
+    alignment's alone: the call then needs no storage, and any address will do."""
     import torch
     key = (name,) + sizes
     need = _needs.get(key)
     if need is None:
         tb = ctypes.c_size_t(0)
-        _check(getattr(load_library(), name)(None, ctypes.byref(tb), *args, None), name)
+        _check(_function(name)(None, ctypes.byref(tb), *args, None), name)
         if len(_needs) >= 4096:
             _needs.clear()
         need = _needs[key] = tb.value
     if temp is not None:
+        if temp.get_device() != like.get_device():
+            raise _elsewhere("temp", temp, like)
         size = temp.numel() * temp.element_size()
         if size >= need:
             return temp, size
-    return torch.empty(need, dtype=torch.uint8, device=device), need
+    if need <= 255:
+        return like, need
+    return torch.empty(need, dtype=torch.uint8, device=like.device), need
 
 
 def group_tokens(ids, num_groups: int, first_id: int = 0, temp=None, stream=None):
@@ -309,17 +303,16 @@ def group_tokens(ids, num_groups: int, first_id: int = 0, temp=None, stream=None
     (num_groups + 1), where each group begins and the last ends."""
     import torch
     code = _id_code(ids)
-    device = ids.device
-    _same_device(device, "temp", temp)
-    on = _on(device, stream)
-    shape, n, num_groups = ids.shape, ids.numel(), int(num_groups)
+    _on_device(ids)
     ids = ids.contiguous()
-    order = torch.empty(n, dtype=torch.int32, device=device)
-    position = torch.empty(shape, dtype=torch.int32, device=device)
-    offsets = torch.empty(max(num_groups, 0) + 1, dtype=torch.int32, device=device)
+    n, num_groups, int32 = ids.numel(), int(num_groups), _types[2]
+    position = torch.empty_like(ids, dtype=int32)
+    order = position.new_empty(n)
+    offsets = position.new_empty(num_groups + 1 if num_groups > 0 else 1)
     args = (code, _at(ids), n, int(first_id), num_groups, _at(order), _at(position), _at(offsets))
-    t, size = _temp("lrs_group_tokens", (code, n, num_groups), args, device, temp)
-    _run(on, device, "lrs_group_tokens", (ids, t, order, position, offsets), (_at(t), ctypes.byref(ctypes.c_size_t(size))) + args)
+    t, size = _temp("lrs_group_tokens", (code, n, num_groups), args, offsets, temp)
+    _run("lrs_group_tokens", stream, (offsets, ids, t, order, position),
+         (t.data_ptr(), ctypes.byref(ctypes.c_size_t(size))) + args)
     return order, position, offsets
 
 
@@ -329,20 +322,21 @@ def dispatch_rows(x, position, num_rows: int | None = None, out=None, stream=Non
     rows: `out`, or a new matrix of num_rows rows (tokens * slots by default).  Rows
     that no position names are left as they were: unset in a new matrix.
     The gradient with respect to x is combine_rows(grad_rows, position)."""
-    import torch
     code = _row_code("x", x.dtype)
-    device = x.device
     tokens, cols = _matrix("x", x)
-    pos = _position(position, device)
-    if pos.shape[0] != tokens:
-        raise ValueError("position is for %d tokens, x has %d" % (pos.shape[0], tokens))
-    ld_out = cols if out is None else _out_matrix("out", out, num_rows, cols, x.dtype, device)
-    on = _on(device, stream)
+    pos = _position(position, x)
+    t, slots = pos.shape
+    if t != tokens:
+        raise ValueError("position is for %d tokens, x has %d" % (t, tokens))
+    if out is not None:
+        num_rows, ld_out = _rows_out("out", out, num_rows, cols, x)
+    _on_device(x)
     if out is None:
-        out = torch.empty(pos.numel() if num_rows is None else int(num_rows), cols, dtype=x.dtype, device=device)
-    x, ld = _rows_in(x)
-    _run(on, device, "lrs_dispatch_rows", (x, pos, out),
-           (code, _at(x), ld, _at(pos), tokens, pos.shape[1], cols, _at(out), ld_out, out.shape[0]))
+        num_rows, ld_out = t * slots if num_rows is None else int(num_rows), cols
+        out = x.new_empty(num_rows, cols)
+    x, ld = _rows_in(x, tokens, cols)
+    _run("lrs_dispatch_rows", stream, (x, pos, out),
+         (code, _at(x), ld, _at(pos), tokens, slots, cols, _at(out), ld_out, num_rows))
     return out
 
 
@@ -350,20 +344,18 @@ def combine_rows(rows, position, weights=None, out=None, stream=None):
     """y[t] = sum over k of weights[t, k] * rows[position[t, k]] (weights None:
     ones; float32, bfloat16 or float16, of the shape of position).  Slots of
     position -1 add nothing.  Returns y, of the type of rows."""
-    import torch
     code = _row_code("rows", rows.dtype)
-    device = rows.device
     num_rows, cols = _matrix("rows", rows)
-    pos = _position(position, device)
+    pos = _position(position, rows)
     w, wcode = _weights(weights, pos)
     tokens, slots = pos.shape
-    ld_out = cols if out is None else _out_matrix("out", out, tokens, cols, rows.dtype, device)
-    on = _on(device, stream)
+    ld_out = cols if out is None else _rows_out("out", out, tokens, cols, rows)[1]
+    _on_device(rows)
     if out is None:
-        out = torch.empty(tokens, cols, dtype=rows.dtype, device=device)
-    rows, ld = _rows_in(rows)
-    _run(on, device, "lrs_combine_rows", (rows, pos, w, out),
-           (code, _at(rows), ld, num_rows, _at(pos), wcode, _at(w), tokens, slots, cols, _at(out), ld_out))
+        out = rows.new_empty(tokens, cols)
+    rows, ld = _rows_in(rows, num_rows, cols)
+    _run("lrs_combine_rows", stream, (rows, pos, w, out),
+         (code, _at(rows), ld, num_rows, _at(pos), wcode, _at(w), tokens, slots, cols, _at(out), ld_out))
     return out
 
 
@@ -374,27 +366,26 @@ def combine_rows_grad(grad_y, rows, position, weights, grad_rows=None, stream=No
     is then replaced) or a new one, rows that no position names left as they were
     (zeros in a new one); grad_weights of the type of weights, zero where position
     is -1, None where weights is None."""
-    import torch
     code = _row_code("rows", rows.dtype)
-    device = rows.device
     num_rows, cols = _matrix("rows", rows)
-    pos = _position(position, device)
+    pos = _position(position, rows)
     w, wcode = _weights(weights, pos)
     tokens, slots = pos.shape
-    if grad_y.dtype != rows.dtype or _matrix("grad_y", grad_y) != (tokens, cols):
+    if grad_y.dtype is not rows.dtype or _matrix("grad_y", grad_y) != (tokens, cols):
         raise ValueError("grad_y is %s %s, expected %s %s" % (grad_y.dtype, tuple(grad_y.shape), rows.dtype,
                                                               (tokens, cols)))
-    _same_device(device, "grad_y", grad_y)
-    ld_out = cols if grad_rows is None else _out_matrix("grad_rows", grad_rows, num_rows, cols, rows.dtype, device)
-    on = _on(device, stream)
+    if grad_y.get_device() != rows.get_device():
+        raise _elsewhere("grad_y", grad_y, rows)
+    ld_out = cols if grad_rows is None else _rows_out("grad_rows", grad_rows, num_rows, cols, rows)[1]
+    _on_device(rows)
     if grad_rows is None:
-        grad_rows = torch.zeros(num_rows, cols, dtype=rows.dtype, device=device)
-    grad_w = None if w is None else torch.empty_like(w)
-    grad_y, ld_y = _rows_in(grad_y)
-    rows, ld = _rows_in(rows)
-    _run(on, device, "lrs_combine_rows_grad", (grad_y, rows, pos, w, grad_rows, grad_w),
-           (code, _at(grad_y), ld_y, _at(rows), ld, num_rows, _at(pos), wcode, _at(w), tokens, slots, cols,
-            _at(grad_rows), ld_out, _at(grad_w)))
+        grad_rows = rows.new_zeros(num_rows, cols)
+    grad_w = None if w is None else w.new_empty(tokens, slots)
+    grad_y, ld_y = _rows_in(grad_y, tokens, cols)
+    rows, ld = _rows_in(rows, num_rows, cols)
+    _run("lrs_combine_rows_grad", stream, (rows, grad_y, pos, w, grad_rows, grad_w),
+         (code, _at(grad_y), ld_y, _at(rows), ld, num_rows, _at(pos), wcode, _at(w), tokens, slots, cols,
+          _at(grad_rows), ld_out, _at(grad_w)))
     return grad_rows, grad_w
 
 
@@ -402,11 +393,10 @@ def embedding(table, ids, scale: float = 1.0, first_id: int = 0, out=None, strea
     """y[...] = scale * table[ids[...] - first_id], zeros for ids outside
     [first_id, first_id + number of rows).  ids: int32 or int64, any shape; y has
     that shape with the row length appended."""
-    import torch
     code, id_code = _row_code("table", table.dtype), _id_code(ids)
-    device = table.device
     num_ids, cols = _matrix("table", table)
-    _same_device(device, "ids", ids)
+    if ids.get_device() != table.get_device():
+        raise _elsewhere("ids", ids, table)
     n, shape = ids.numel(), (*ids.shape, cols)
     y, ld_y = out, cols
     if out is not None:
@@ -416,14 +406,14 @@ def embedding(table, ids, scale: float = 1.0, first_id: int = 0, out=None, strea
             if not out.is_contiguous():
                 raise ValueError("out must be contiguous")
             y = out.view(n, cols)
-        ld_y = _out_matrix("out", y, n, cols, table.dtype, device)
-    on = _on(device, stream)
+        ld_y = _rows_out("out", y, n, cols, table)[1]
+    _on_device(table)
     if out is None:
-        y = out = torch.empty(shape, dtype=table.dtype, device=device)
-    table, ld = _rows_in(table)
+        y = out = table.new_empty(shape)
+    table, ld = _rows_in(table, num_ids, cols)
     ids = ids.contiguous()
-    _run(on, device, "lrs_embedding", (table, ids, y),
-           (code, _at(table), ld, num_ids, id_code, _at(ids), n, int(first_id), float(scale), cols, _at(y), ld_y))
+    _run("lrs_embedding", stream, (table, ids, y),
+         (code, _at(table), ld, num_ids, id_code, _at(ids), n, int(first_id), float(scale), cols, _at(y), ld_y))
     return out
 
 
@@ -436,29 +426,33 @@ def embedding_grad(grad_y, ids, num_ids: int, scale: float = 1.0, first_id: int 
     `grad`, and rows that no id names are not touched; otherwise every row is
     written."""
     import torch
-    code, id_code = _row_code("grad_y", grad_y.dtype), _id_code(ids)
-    device, num_ids = grad_y.device, int(num_ids)
-    _same_device(device, "ids", ids)
-    _same_device(device, "temp", temp)
+    code, id_code, num_ids = _row_code("grad_y", grad_y.dtype), _id_code(ids), int(num_ids)
+    if ids.get_device() != grad_y.get_device():
+        raise _elsewhere("ids", ids, grad_y)
     if grad_y.dim() < 1 or grad_y.shape[:-1] != ids.shape:
         raise ValueError("grad_y has shape %s for ids of shape %s" % (tuple(grad_y.shape), tuple(ids.shape)))
     n, cols = ids.numel(), grad_y.shape[-1]
     if dtype is None:
         dtype = grad.dtype if grad is not None else grad_y.dtype
-    if dtype not in (grad_y.dtype, torch.float32):
+    if dtype is not grad_y.dtype and dtype is not torch.float32:
         raise TypeError("the gradient must be %s or float32, not %s" % (grad_y.dtype, dtype))
+    ld_grad = cols
     if grad is not None:
-        ld_grad = _out_matrix("grad", grad, num_ids, cols, dtype, device)
+        if grad.dtype is not dtype:
+            raise ValueError("grad has dtype %s, expected %s" % (grad.dtype, dtype))
+        if grad.get_device() != grad_y.get_device():
+            raise _elsewhere("grad", grad, grad_y)
+        ld_grad = _rows_out("grad", grad, num_ids, cols, grad)[1]
     elif accumulate:
         raise ValueError("accumulate needs the gradient to add to")
-    on = _on(device, stream)
+    _on_device(grad_y)
     if grad is None:
-        grad, ld_grad = torch.empty(max(num_ids, 0), cols, dtype=dtype, device=device), cols
-    g2, ld = _rows_in(grad_y if grad_y.dim() == 2 else grad_y.reshape(n, cols))
+        grad = torch.empty(num_ids if num_ids > 0 else 0, cols, dtype=dtype, device=grad_y.device)
+    g2, ld = _rows_in(grad_y if grad_y.dim() == 2 else grad_y.reshape(n, cols), n, cols)
     ids = ids.contiguous()
-    grad_code = _row_code("grad", dtype)
+    grad_code = _types[1][dtype]
     args = (code, _at(g2), ld, id_code, _at(ids), n, int(first_id), float(scale), grad_code, _at(grad), ld_grad, num_ids,
             cols, 1 if accumulate else 0)
-    t, size = _temp("lrs_embedding_grad", (code, id_code, n, grad_code, num_ids, cols), args, device, temp)
-    _run(on, device, "lrs_embedding_grad", (g2, ids, t, grad), (_at(t), ctypes.byref(ctypes.c_size_t(size))) + args)
+    t, size = _temp("lrs_embedding_grad", (code, id_code, n, grad_code, num_ids, cols), args, grad, temp)
+    _run("lrs_embedding_grad", stream, (g2, ids, t, grad), (t.data_ptr(), ctypes.byref(ctypes.c_size_t(size))) + args)
     return grad

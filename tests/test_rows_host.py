@@ -37,9 +37,10 @@ def test_group_queries_and_refusals():
         assert ei.value.status == lrs.LRS_ERR_INVALID_ARG, kw
     group(first=2**63 - 9, groups=8)
     group(first=-2**63, groups=8)
+    need = group(n=500000)
     for temp, nbytes in ((T, need - 256), (T + 1, need - 1)):
         with pytest.raises(lrs.LrsError) as ei:
-            group(temp=temp, nbytes=nbytes)
+            group(temp=temp, nbytes=nbytes, n=500000)
         assert ei.value.status == lrs.LRS_ERR_TEMP_TOO_SMALL
     lib = lrs.load_library()
     assert lib.lrs_group_tokens(None, None, 0, A, 10, 0, 4, B, C, D, None) == lrs.LRS_ERR_INVALID_ARG
