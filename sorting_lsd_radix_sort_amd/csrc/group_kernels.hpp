@@ -109,16 +109,22 @@ __device__ __forceinline__ uint32_t wave_rank(uint32_t digit, bool valid, int bi
     return rank;
 }
 
-// Adds the active lanes' digits to the counts in LDS.  A wave of one digit adds once:
-// 64 adds to one word would queue.
-__device__ __forceinline__ void count_digit(uint32_t *count, uint32_t digit)
+// Adds the active lanes' digits to the counts in LDS.  Lanes of the last bin (of no
+// group: most of them, for a rank's share of the experts) add once together, and so
+// does a wave whose others are all of one bin: 64 adds to one word would queue.
+__device__ __forceinline__ void count_digit(uint32_t *count, uint32_t digit, uint32_t last)
 {
-    const uint32_t f = __builtin_amdgcn_readfirstlane(digit);
-    const uint64_t on = __ballot(1);
-    if (__ballot(digit != f) == 0) {
-        if (lanes_below(on) == 0) atomicAdd(&count[f], (uint32_t)__popcll(on));
+    if (digit == last) {
+        const uint64_t on = __ballot(1);
+        if (lanes_below(on) == 0) atomicAdd(&count[last], (uint32_t)__popcll(on));
     } else {
-        atomicAdd(&count[digit], 1u);
+        const uint32_t f = __builtin_amdgcn_readfirstlane(digit);
+        if (__ballot(digit != f) == 0) {
+            const uint64_t on = __ballot(1);
+            if (lanes_below(on) == 0) atomicAdd(&count[f], (uint32_t)__popcll(on));
+        } else {
+            atomicAdd(&count[digit], 1u);
+        }
     }
 }
 
@@ -139,7 +145,7 @@ __global__ __launch_bounds__(kPlaceThreads) void count_kernel(SRC src, Pass ps, 
         if (first + i * kPlaceThreads < ps.n) d[i] = digit_in(ps, src.key(first + i * kPlaceThreads));
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-        if (first + i * kPlaceThreads < ps.n) count_digit(s_count, d[i]);
+        if (first + i * kPlaceThreads < ps.n) count_digit(s_count, d[i], ps.bins - 1);
     }
     __syncthreads();
     for (uint32_t b = threadIdx.x; b < ps.bins; b += kPlaceThreads) counts[(int64_t)blockIdx.x * ps.bins + b] = s_count[b];
@@ -198,7 +204,7 @@ __device__ __forceinline__ void place_slots(const Pass &ps, const uint32_t (&key
             for (int u = 0; u < AHEAD; ++u) {
                 // (a wave's 64 slots are all before this block's, in it, or after)
                 const int64_t i = at + u * kPlaceThreads;
-                if (i < ps.n && (i < mine || i >= after)) count_digit(i < mine ? s.start : s.all, d[u]);
+                if (i < ps.n && (i < mine || i >= after)) count_digit(i < mine ? s.start : s.all, d[u], ps.bins - 1);
             }
         }
     }

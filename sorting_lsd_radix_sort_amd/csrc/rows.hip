@@ -160,22 +160,25 @@ lrs_status guarded(F &&f)
 // ------------------------------------------------------------------ grouping
 
 // Few ids are ordered by counting passes of this file's own: a grouping of up to 2048
-// groups in one, an embedding's ids in passes of up to nine bits.  The others take the
+// groups and a million ids in one (262,144 ids of 256 groups in 13.8 us; by the sort
+// 31.4), an embedding's ids in passes of up to nine bits.  The others take the
 // library's sort.
 constexpr int kFewBins = 513, kManyBins = 2049;
 constexpr int64_t kDirectGroups = kManyBins - 1, kDirectSlots = 1 << 20;
 
-// Blocks of 1024 slots, or of 4096 from 128K slots on (a block reads every block's
-// counts, so not too many; a wave's ranking is what they share, so not too few).  Up
-// to 12K slots the blocks count one another's slots and need no count launch: 6,000
-// ids of 256 groups in 6.2 us instead of 7.8, 12,282 in 7.7 instead of 8.7, 16,384 in
-// 8.7 instead of 7.7 (kernels alone; a launch is 3 us of the host's).
-constexpr int64_t kSmallBlockSlots = 128 * kPlaceThreads, kSelfCountSlots = 12 * kPlaceThreads;
+// Blocks of 1024 slots, or of 4096 where those would be many (a block reads every
+// block's counts; a wave's ranking is what they share): 131,072 ids of 256 groups in
+// 11.5 us with 128 blocks, 15 with 32; of 2048 groups 28.5 with 128, and 262,144 ids
+// 24.5 with 64.  Up to 12K slots the blocks count one another's slots and need no
+// count launch: 6,000 ids of 256 groups in 6.4 us instead of 7.8, 12,282 in 8.2
+// instead of 8.7, 16,384 in 9.3 instead of 7.7 (kernels alone; a launch is 3 us of
+// the host's).
+constexpr int64_t kSelfCountSlots = 12 * kPlaceThreads;
 
-int place_items(int64_t n) { return n <= kSmallBlockSlots ? 1 : 4; }
-int place_blocks(int64_t n)
+int place_items(int64_t n, int64_t bins) { return n <= (bins <= kFewBins ? 128 : 32) * kPlaceThreads ? 1 : 4; }
+int place_blocks(int64_t n, int64_t bins)
 {
-    const int64_t slots = (int64_t)kPlaceThreads * place_items(n);
+    const int64_t slots = (int64_t)kPlaceThreads * place_items(n, bins);
     return (int)std::max<int64_t>(1, (n + slots - 1) / slots);
 }
 
@@ -183,7 +186,7 @@ template <int MAX_BINS, int ITEMS, typename SRC>
 lrs_status run_pass(const SRC &src, const Pass &ps, uint32_t *counts, const PlaceOut &out, uint32_t *clear,
                     hipStream_t stream)
 {
-    const int blocks = place_blocks(ps.n);
+    const int blocks = place_blocks(ps.n, ps.bins);
     const bool count = blocks > 1 && ps.n > kSelfCountSlots;
     if (count) {
         count_kernel<SRC, MAX_BINS, ITEMS><<<blocks, kPlaceThreads, 0, stream>>>(src, ps, counts, clear);
@@ -199,7 +202,7 @@ template <typename SRC>
 lrs_status run_pass(const SRC &src, const Pass &ps, uint32_t *counts, const PlaceOut &out, uint32_t *clear,
                     hipStream_t stream)
 {
-    const bool one = place_items(ps.n) == 1;
+    const bool one = place_items(ps.n, ps.bins) == 1;
     if (ps.bins <= kFewBins)
         return one ? run_pass<kFewBins, 1>(src, ps, counts, out, clear, stream)
                    : run_pass<kFewBins, 4>(src, ps, counts, out, clear, stream);
@@ -236,7 +239,7 @@ lrs_status group_layout(int64_t n, int64_t groups, GroupLayout *L)
     L->off_sort = off;
     lrs_status st = LRS_OK;
     if (n <= kDirectIds) {
-        L->sort_bytes = (size_t)place_blocks(n) * ((size_t)1 << kDigitBits) * 4;
+        L->sort_bytes = (size_t)place_blocks(n, kFewBins) * ((size_t)1 << kDigitBits) * 4;
     } else {
         // the size depends on n and the bit range alone: any distinct pointers will do
         const uintptr_t some = (uintptr_t)1 << 40;
@@ -342,7 +345,7 @@ lrs_status group_entry(void *d_temp, size_t *temp_bytes, lrs_id_type id_type, co
     GroupLayout L;
     lrs_status st = LRS_OK;
     if (direct)
-        L.total = n > kSelfCountSlots ? (size_t)place_blocks(n) * (size_t)(groups + 1) * 4 : 0;
+        L.total = n > kSelfCountSlots ? (size_t)place_blocks(n, groups + 1) * (size_t)(groups + 1) * 4 : 0;
     else
         st = group_layout(n, groups, &L);
     if (st != LRS_OK) return st;

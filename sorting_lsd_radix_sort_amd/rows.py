@@ -6,7 +6,8 @@ bindings do.  ``group_tokens``, ``dispatch_rows``, ``combine_rows`` and
 ``combine_rows_grad`` (tokens sorted by expert and back), ``embedding`` and
 ``embedding_grad`` are conveniences over them on torch tensors: they allocate
 outputs and temp storage, and refuse tensors of the wrong shape, type or device
-with ValueError or TypeError before any work.
+with ValueError or TypeError before any work.  Gradients are calls of their own, as
+in the C interface; nothing is recorded for torch's autograd.
 
 Matrices may have any row stride; their elements must be contiguous within a row
 (inputs that are not are copied first, outputs are refused).  ``stream`` is as for
@@ -216,6 +217,13 @@ def _weights(weights, position):
     return weights.contiguous(), _row_code("weights", weights.dtype)
 
 
+def _int64(name, v) -> int:
+    v = int(v)
+    if not -2**63 <= v < 2**63:
+        raise ValueError("%s %d is no int64" % (name, v))
+    return v
+
+
 def _at(t):
     """Address of a tensor's first element (None for None and for empty tensors)."""
     return None if t is None else t.data_ptr() or None
@@ -309,7 +317,7 @@ def group_tokens(ids, num_groups: int, first_id: int = 0, temp=None, stream=None
     position = torch.empty_like(ids, dtype=int32)
     order = position.new_empty(n)
     offsets = position.new_empty(num_groups + 1 if num_groups > 0 else 1)
-    args = (code, _at(ids), n, int(first_id), num_groups, _at(order), _at(position), _at(offsets))
+    args = (code, _at(ids), n, _int64("first_id", first_id), num_groups, _at(order), _at(position), _at(offsets))
     t, size = _temp("lrs_group_tokens", (code, n, num_groups), args, offsets, temp)
     _run("lrs_group_tokens", stream, (offsets, ids, t, order, position),
          (t.data_ptr(), ctypes.byref(ctypes.c_size_t(size))) + args)
@@ -365,7 +373,8 @@ def combine_rows_grad(grad_y, rows, position, weights, grad_rows=None, stream=No
     weights[t, k] * grad_y[t], in the given matrix (which may be `rows` itself: it
     is then replaced) or a new one, rows that no position names left as they were
     (zeros in a new one); grad_weights of the type of weights, zero where position
-    is -1, None where weights is None."""
+    is -1, None where weights is None.  No two slots may have the same position
+    (group_tokens gives none such)."""
     code = _row_code("rows", rows.dtype)
     num_rows, cols = _matrix("rows", rows)
     pos = _position(position, rows)
@@ -413,7 +422,7 @@ def embedding(table, ids, scale: float = 1.0, first_id: int = 0, out=None, strea
     table, ld = _rows_in(table, num_ids, cols)
     ids = ids.contiguous()
     _run("lrs_embedding", stream, (table, ids, y),
-         (code, _at(table), ld, num_ids, id_code, _at(ids), n, int(first_id), float(scale), cols, _at(y), ld_y))
+         (code, _at(table), ld, num_ids, id_code, _at(ids), n, _int64("first_id", first_id), float(scale), cols, _at(y), ld_y))
     return out
 
 
@@ -451,7 +460,7 @@ def embedding_grad(grad_y, ids, num_ids: int, scale: float = 1.0, first_id: int 
     g2, ld = _rows_in(grad_y if grad_y.dim() == 2 else grad_y.reshape(n, cols), n, cols)
     ids = ids.contiguous()
     grad_code = _types[1][dtype]
-    args = (code, _at(g2), ld, id_code, _at(ids), n, int(first_id), float(scale), grad_code, _at(grad), ld_grad, num_ids,
+    args = (code, _at(g2), ld, id_code, _at(ids), n, _int64("first_id", first_id), float(scale), grad_code, _at(grad), ld_grad, num_ids,
             cols, 1 if accumulate else 0)
     t, size = _temp("lrs_embedding_grad", (code, id_code, n, grad_code, num_ids, cols), args, grad, temp)
     _run("lrs_embedding_grad", stream, (g2, ids, t, grad), (t.data_ptr(), ctypes.byref(ctypes.c_size_t(size))) + args)

@@ -145,6 +145,32 @@ def test_group_tokens_edges():
     check_group(torch.tensor([70000, 3, 3], device="cuda"), 70001, 0, lrs.group_tokens(torch.tensor([70000, 3, 3], device="cuda"), 70001))
 
 
+@pytest.mark.parametrize("groups", [5, 300, 512, 513, 2048])
+def test_group_many(groups):
+    """Around the sizes where blocks become larger and where the sort takes over."""
+    for n in (12288, 12289, 32768, 32769, 131073, 2**20, 2**20 + 1):
+        announce("group n=%d groups=%d" % (n, groups))
+        for kind in ("skewed", "far"):
+            ids = routing(n, 1, groups, n + groups, kind).reshape(-1)
+            check_group(ids, groups, 0, lrs.group_tokens(ids, groups))
+
+
+def test_first_id_beyond_int64_is_refused():
+    torch = torch_()
+    announce("first id beyond int64")
+    ids, x = torch.zeros(4, dtype=torch.int64, device="cuda"), torch.zeros(4, 8, device="cuda")
+    for first in (2**63, -2**63 - 1, 2**64):
+        with pytest.raises(ValueError, match="int64"):
+            lrs.group_tokens(ids, 4, first_id=first)
+        with pytest.raises(ValueError, match="int64"):
+            lrs.embedding(x, ids, first_id=first)
+        with pytest.raises(ValueError, match="int64"):
+            lrs.embedding_grad(x, ids, 4, first_id=first)
+    for groups in (-1, 2**31):
+        with pytest.raises((lrs.LrsError, RuntimeError)):
+            lrs.group_tokens(ids, groups)
+
+
 def test_group_outputs_are_optional_and_temp_is_reused():
     torch = torch_()
     for n, groups in ((500, 8), (30000, 100), (30000, 30000)):
@@ -590,6 +616,48 @@ def test_gradients_against_differences():
     diff = inner(gz, lrs.embedding(up, ids, scale=1.7)) - inner(gz, lrs.embedding(down, ids, scale=1.7))
     bound = (400 + 2) * 2.0**-24 * 4 * size(gz.abs(), lrs.embedding(up.abs() + down.abs(), ids, scale=1.7))
     assert abs(diff - inner(grad, up.double() - down.double())) <= bound
+
+
+def test_infinities_nan_and_subnormals():
+    """What the values of real slots and rows hold reaches the results as in IEEE
+    arithmetic, results below the normal range keep their bits (half the smallest
+    subnormal is allowed), and a sum beyond float16 rounds to infinity."""
+    torch = torch_()
+    announce("special values")
+    inf, nan = float("inf"), float("nan")
+    for name, cols in (("f32", 5), ("bf16", 11), ("f16", 11)):
+        dt = dtype_of(name)
+        rows = torch.ones(4, cols, dtype=dt, device="cuda")
+        rows[0, 0], rows[1, 1], rows[2, 2], rows[3, 2] = inf, nan, inf, -inf
+        position = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device="cuda")
+        y = lrs.combine_rows(rows, position)
+        want = torch.full((2, cols), 2.0, dtype=dt, device="cuda")
+        want[0, 0], want[0, 1], want[1, 2] = inf, nan, nan
+        assert torch.equal(y.isnan(), want.isnan()) and torch.equal(y.nan_to_num(7.0), want.nan_to_num(7.0))
+        grad = lrs.embedding_grad(rows, torch.tensor([3, 3, 1, 1], device="cuda"), 5)
+        want = torch.zeros(5, cols, dtype=dt, device="cuda")
+        want[3], want[1] = 2.0, 2.0
+        want[3, 0], want[3, 1], want[1, 2] = inf, nan, nan
+        assert torch.equal(grad.isnan(), want.isnan()) and torch.equal(grad.nan_to_num(7.0), want.nan_to_num(7.0))
+    big = torch.full((2, 3), 60000.0, dtype=torch.float16, device="cuda")
+    assert bool((lrs.combine_rows(big, torch.tensor([[0, 1]], dtype=torch.int32, device="cuda")) == inf).all())
+    for name, scale, step in (("f32", 2.0**-140, 2.0**-149), ("bf16", 2.0**-128, 2.0**-133), ("f16", 2.0**-20, 2.0**-24)):
+        table = randn((50, 40), name, 151)
+        ids = torch.arange(50, device="cuda")
+        want = as64(table) * scale
+        assert (np.abs(as64(lrs.embedding(table, ids, scale=scale)) - want) <= step / 2).all(), name
+        assert (np.abs(as64(lrs.embedding_grad(table, ids, 50, scale=scale)) - want) <= step / 2).all(), name
+
+
+def test_rows_named_by_several_tokens():
+    """The way back may read a row more than once, also within a token."""
+    torch = torch_()
+    announce("rows named twice")
+    rows = randn((6, 77), "f32", 161)
+    position = torch.tensor([[0, 0, 5], [5, 0, 2]], dtype=torch.int32, device="cuda")
+    want = torch.stack([rows[0].double() * 2 + rows[5].double(), rows[5].double() + rows[0].double() + rows[2].double()])
+    mag = torch.stack([rows[0].abs() * 2 + rows[5].abs(), rows[5].abs() + rows[0].abs() + rows[2].abs()])
+    within(lrs.combine_rows(rows, position), as64(want), as64(mag), 3)
 
 
 # --------------------------------------------- streams, graphs, large offsets
