@@ -126,6 +126,7 @@ def lrs_embedding_grad(d_temp, temp_bytes, row_type, d_grad_y, ld_grad_y, id_typ
 _types = None  # ({torch dtype: code} of ids, of rows, torch.int32)
 _needs: dict = {}  # temp bytes by sizes and types, which alone decide them
 _functions: dict = {}  # C functions of the loaded library
+_current_handle = None  # device index -> handle of its current stream, once looked for
 
 
 def _type_codes():
@@ -225,8 +226,8 @@ def _int64(name, v) -> int:
 
 
 def _at(t):
-    """Address of a tensor's first element (None for None and for empty tensors)."""
-    return None if t is None else t.data_ptr() or None
+    """Address of an optional tensor's first element."""
+    return None if t is None else t.data_ptr()
 
 
 def _function(name):
@@ -236,12 +237,14 @@ def _function(name):
     return fn
 
 
-def _current_handle(index) -> int:
-    """Handle of a device's current stream: torch's own shortcut to it where there is
-    one (the Stream object that the public call builds takes 2 us)."""
+def _handle_lookup():
+    """Finds how a device's current stream handle is had: by torch's own shortcut to it
+    where there is one (the Stream object that the public call builds takes 2 us)."""
+    global _current_handle
     import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+    _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _current_handle
 
 
 def _on_device(t) -> None:
@@ -259,7 +262,7 @@ def _run(name, stream, tensors, args) -> None:
     fn = _function(name)
     index = tensors[0].get_device()
     if stream is None and torch.cuda.current_device() == index:
-        status = fn(*args, _current_handle(index) or None)
+        status = fn(*args, (_current_handle or _handle_lookup())(index) or None)
         if status:
             _check(status, name)
         return
@@ -317,7 +320,7 @@ def group_tokens(ids, num_groups: int, first_id: int = 0, temp=None, stream=None
     position = torch.empty_like(ids, dtype=int32)
     order = position.new_empty(n)
     offsets = position.new_empty(num_groups + 1 if num_groups > 0 else 1)
-    args = (code, _at(ids), n, _int64("first_id", first_id), num_groups, _at(order), _at(position), _at(offsets))
+    args = (code, ids.data_ptr(), n, _int64("first_id", first_id), num_groups, order.data_ptr(), position.data_ptr(), offsets.data_ptr())
     t, size = _temp("lrs_group_tokens", (code, n, num_groups), args, offsets, temp)
     _run("lrs_group_tokens", stream, (offsets, ids, t, order, position),
          (t.data_ptr(), ctypes.byref(ctypes.c_size_t(size))) + args)
@@ -344,7 +347,7 @@ def dispatch_rows(x, position, num_rows: int | None = None, out=None, stream=Non
         out = x.new_empty(num_rows, cols)
     x, ld = _rows_in(x, tokens, cols)
     _run("lrs_dispatch_rows", stream, (x, pos, out),
-         (code, _at(x), ld, _at(pos), tokens, slots, cols, _at(out), ld_out, num_rows))
+         (code, x.data_ptr(), ld, pos.data_ptr(), tokens, slots, cols, out.data_ptr(), ld_out, num_rows))
     return out
 
 
@@ -363,7 +366,7 @@ def combine_rows(rows, position, weights=None, out=None, stream=None):
         out = rows.new_empty(tokens, cols)
     rows, ld = _rows_in(rows, num_rows, cols)
     _run("lrs_combine_rows", stream, (rows, pos, w, out),
-         (code, _at(rows), ld, num_rows, _at(pos), wcode, _at(w), tokens, slots, cols, _at(out), ld_out))
+         (code, rows.data_ptr(), ld, num_rows, pos.data_ptr(), wcode, _at(w), tokens, slots, cols, out.data_ptr(), ld_out))
     return out
 
 
@@ -393,8 +396,8 @@ def combine_rows_grad(grad_y, rows, position, weights, grad_rows=None, stream=No
     grad_y, ld_y = _rows_in(grad_y, tokens, cols)
     rows, ld = _rows_in(rows, num_rows, cols)
     _run("lrs_combine_rows_grad", stream, (rows, grad_y, pos, w, grad_rows, grad_w),
-         (code, _at(grad_y), ld_y, _at(rows), ld, num_rows, _at(pos), wcode, _at(w), tokens, slots, cols,
-          _at(grad_rows), ld_out, _at(grad_w)))
+         (code, grad_y.data_ptr(), ld_y, rows.data_ptr(), ld, num_rows, pos.data_ptr(), wcode, _at(w), tokens, slots, cols,
+          grad_rows.data_ptr(), ld_out, _at(grad_w)))
     return grad_rows, grad_w
 
 
@@ -422,7 +425,7 @@ def embedding(table, ids, scale: float = 1.0, first_id: int = 0, out=None, strea
     table, ld = _rows_in(table, num_ids, cols)
     ids = ids.contiguous()
     _run("lrs_embedding", stream, (table, ids, y),
-         (code, _at(table), ld, num_ids, id_code, _at(ids), n, _int64("first_id", first_id), float(scale), cols, _at(y), ld_y))
+         (code, table.data_ptr(), ld, num_ids, id_code, ids.data_ptr(), n, _int64("first_id", first_id), float(scale), cols, y.data_ptr(), ld_y))
     return out
 
 
@@ -460,7 +463,7 @@ def embedding_grad(grad_y, ids, num_ids: int, scale: float = 1.0, first_id: int 
     g2, ld = _rows_in(grad_y if grad_y.dim() == 2 else grad_y.reshape(n, cols), n, cols)
     ids = ids.contiguous()
     grad_code = _types[1][dtype]
-    args = (code, _at(g2), ld, id_code, _at(ids), n, _int64("first_id", first_id), float(scale), grad_code, _at(grad), ld_grad, num_ids,
+    args = (code, g2.data_ptr(), ld, id_code, ids.data_ptr(), n, _int64("first_id", first_id), float(scale), grad_code, grad.data_ptr(), ld_grad, num_ids,
             cols, 1 if accumulate else 0)
     t, size = _temp("lrs_embedding_grad", (code, id_code, n, grad_code, num_ids, cols), args, grad, temp)
     _run("lrs_embedding_grad", stream, (g2, ids, t, grad), (t.data_ptr(), ctypes.byref(ctypes.c_size_t(size))) + args)
