@@ -36,14 +36,16 @@
  *  - Device pointers, streams, asynchrony and graph capture as in lrsort.h: the
  *    library allocates nothing, each call only enqueues kernels on `stream`.
  *    Calls with d_temp follow the two-phase temp storage convention there (the
- *    query with d_temp == NULL checks the arguments too); the query depends on
- *    the sizes and types alone, not on the pointers' values.
+ *    query with d_temp == NULL checks the arguments too); the size depends on the
+ *    sizes and types alone, not on the pointers' values, and a size of 255 (what
+ *    alignment may take) means that nothing is stored there.
  *  - Outputs must not overlap inputs or other outputs (columns of one buffer that
  *    are interleaved with equal row strides may), except where a call allows it;
  *    an overlap that the library sees gives LRS_ERR_INVALID_ARG.
  *  - Sizes may be zero.  tokens * slots and the number of ids are at most
- *    2^31 - 1 (positions are int32), counts of groups, rows and ids likewise;
- *    row lengths and strides are 64-bit.  Negative sizes, NULL pointers to
+ *    2^31 - 1 (positions are int32), rows and columns likewise, the counts of
+ *    groups and of a gradient's ids at most 2^31 - 2; strides are 64-bit.  Negative
+ *    sizes, NULL pointers to
  *    arrays that are not empty, misaligned pointers, unknown types and
  *    first_id + count beyond int64 give LRS_ERR_INVALID_ARG.  Every check is
  *    made before any work is enqueued.
@@ -120,7 +122,8 @@ lrs_status lrs_embedding(lrs_row_type type, const void *d_table, int64_t ld_tabl
  * output, d_grad_y (n x cols, of `type`):
  *    g[v] = scale * (sum of d_grad_y[i] over the i with d_ids[i] = first_id + v)
  * The ids are sorted (with their indices) and each id's rows summed in the order
- * of their indices, in pieces of a length that depends on n and cols alone.
+ * of their indices, in pieces of a length that depends on n, cols and the type
+ * alone; the pieces' sums are kept in float32 until they are added up.
  *  - accumulate == 0: every row of d_grad (num_ids x cols, of grad_type) is
  *    written, zeros where no id names it.
  *  - accumulate != 0: g is added to d_grad, in float32, rounded once; rows that no

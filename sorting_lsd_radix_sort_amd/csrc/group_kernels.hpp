@@ -1,10 +1,14 @@
 // group_kernels.hpp -- gfx950 (CDNA4, wave64) kernels that order ids stably: one
 // counting pass for a grouping by expert, two or three for an embedding's ids.
 //
-// Few ids are ordered here, up to some hundred thousand: their bytes are nothing, so
-// launches and dependent steps bound them, and each pass runs in one launch of one
-// workgroup or in two launches (count, place) of a few.  Larger orders take the
-// library's sort.
+// Few ids are ordered here, up to a million: their bytes are nothing (12 to 20 per
+// id), so launches and dependent steps bound them.  A pass is one launch (a block
+// counts and places, and counts the other blocks' ids too) or two (count, place), and
+// an embedding's few thousand ids take all their passes in one launch of one block.
+// 1024 threads a block: 16 waves rank 64 ids each by ballots, and the counts of the
+// waves before are summed bin by bin.  32 ids of 256 groups take 3.6 us, 4,096 5.6,
+// 131,072 11.5 (kernels back to back); the launch itself is some 2 us of each.
+// Larger orders take the library's sort.
 #pragma once
 
 #include <hip/hip_runtime.h>

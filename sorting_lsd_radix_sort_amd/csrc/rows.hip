@@ -296,7 +296,8 @@ lrs_status sort_ids(const GroupLayout &L, char *temp, const void *ids, int64_t n
 }
 
 lrs_status sort_ids(const GroupLayout &L, char *temp, lrs_id_type id_type, const void *ids, int64_t n, int64_t first,
-                    int64_t groups, int32_t *order, const uint32_t **sorted, const uint32_t **index, uint32_t *clear, hipStream_t stream)
+                    int64_t groups, int32_t *order, const uint32_t **sorted, const uint32_t **index, uint32_t *clear,
+                    hipStream_t stream)
 {
     return id_type == LRS_ID_I32
                ? sort_ids<int32_t>(L, temp, ids, n, first, groups, order, sorted, index, clear, stream)
@@ -403,8 +404,8 @@ LRS_API lrs_status lrs_dispatch_rows(lrs_row_type type, const void *d_x, int64_t
         using W = decltype(word);
         const Tiling t = tiling_of(tokens, cols, kVec<W>);
         auto *k = wave_row(t) ? dispatch_kernel<W, true> : dispatch_kernel<W, false>;
-        k<<<grid_of(t), kThreads, kDispatchLds, stream>>>((const W *)d_x, ld_x, d_position, tokens, (int)slots, cols, (W *)d_rows,
-                                               ld_rows, (uint32_t)num_rows, t);
+        k<<<grid_of(t), kThreads, kDispatchLds, stream>>>((const W *)d_x, ld_x, d_position, tokens, (int)slots, cols,
+                                                          (W *)d_rows, ld_rows, (uint32_t)num_rows, t);
         return launched();
     };
     return b == 4 ? run(uint32_t{}) : run(uint16_t{});

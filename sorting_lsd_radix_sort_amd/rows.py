@@ -320,7 +320,8 @@ def group_tokens(ids, num_groups: int, first_id: int = 0, temp=None, stream=None
     position = torch.empty_like(ids, dtype=int32)
     order = position.new_empty(n)
     offsets = position.new_empty(num_groups + 1 if num_groups > 0 else 1)
-    args = (code, ids.data_ptr(), n, _int64("first_id", first_id), num_groups, order.data_ptr(), position.data_ptr(), offsets.data_ptr())
+    args = (code, ids.data_ptr(), n, _int64("first_id", first_id), num_groups, order.data_ptr(), position.data_ptr(),
+            offsets.data_ptr())
     t, size = _temp("lrs_group_tokens", (code, n, num_groups), args, offsets, temp)
     _run("lrs_group_tokens", stream, (offsets, ids, t, order, position),
          (t.data_ptr(), ctypes.byref(ctypes.c_size_t(size))) + args)
@@ -425,7 +426,8 @@ def embedding(table, ids, scale: float = 1.0, first_id: int = 0, out=None, strea
     table, ld = _rows_in(table, num_ids, cols)
     ids = ids.contiguous()
     _run("lrs_embedding", stream, (table, ids, y),
-         (code, table.data_ptr(), ld, num_ids, id_code, ids.data_ptr(), n, _int64("first_id", first_id), float(scale), cols, y.data_ptr(), ld_y))
+         (code, table.data_ptr(), ld, num_ids, id_code, ids.data_ptr(), n, _int64("first_id", first_id), float(scale),
+          cols, y.data_ptr(), ld_y))
     return out
 
 
@@ -463,8 +465,8 @@ def embedding_grad(grad_y, ids, num_ids: int, scale: float = 1.0, first_id: int 
     g2, ld = _rows_in(grad_y if grad_y.dim() == 2 else grad_y.reshape(n, cols), n, cols)
     ids = ids.contiguous()
     grad_code = _types[1][dtype]
-    args = (code, g2.data_ptr(), ld, id_code, ids.data_ptr(), n, _int64("first_id", first_id), float(scale), grad_code, grad.data_ptr(), ld_grad, num_ids,
-            cols, 1 if accumulate else 0)
+    args = (code, g2.data_ptr(), ld, id_code, ids.data_ptr(), n, _int64("first_id", first_id), float(scale), grad_code,
+            grad.data_ptr(), ld_grad, num_ids, cols, 1 if accumulate else 0)
     t, size = _temp("lrs_embedding_grad", (code, id_code, n, grad_code, num_ids, cols), args, grad, temp)
     _run("lrs_embedding_grad", stream, (g2, ids, t, grad), (t.data_ptr(), ctypes.byref(ctypes.c_size_t(size))) + args)
     return grad
