@@ -47,9 +47,10 @@ struct PairSource {
 // A pass: its digit is (key >> shift) & mask, below `bins`, which is at most 2^bits
 // and a kernel's MAX_BINS.  (A grouping's last bin holds the ids of no group.)
 struct Pass {
-    int64_t n;
-    int shift, bits;
-    uint32_t mask, bins;
+    int n;
+    uint32_t mask;
+    uint16_t bins;
+    uint8_t shift, bits;
 };
 
 __device__ __forceinline__ uint32_t digit_in(const Pass &ps, uint32_t key) { return (key >> ps.shift) & ps.mask; }
@@ -304,7 +305,7 @@ __global__ __launch_bounds__(kPlaceThreads) void order_kernel(IdSource<ID> src, 
     }
     for (int shift = 0; shift < bits; shift += digit_bits) {
         const int width = digit_bits < bits - shift ? digit_bits : bits - shift;
-        const Pass ps{n, shift, width, (1u << width) - 1u, 1u << width};
+        const Pass ps{n, (1u << width) - 1u, (uint16_t)(1u << width), (uint8_t)shift, (uint8_t)width};
         place_slots<MAX_BINS, ITEMS>(ps, key, valid, nullptr, 0, 1, [](int64_t) { return 0u; }, nullptr, s, to);
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i)

@@ -186,33 +186,57 @@ __device__ __forceinline__ void store_scalar(void *p, int type, int64_t i, float
 
 // ---------------------------------------------------------------------- grid
 //
-// A workgroup serves kThreads / tx rows, tx lanes each (a power of two), and tx
-// vectors of each row; grid.x runs over a row's pieces and grid.y over the rows,
-// both in strides where there are more than the grid holds.
-struct Tiling {
-    int tx_log2;
-    int64_t vecs;  // vectors per row, the last perhaps short
-    int64_t row_tiles;
-    int64_t col_tiles;
-};
+// A workgroup serves kThreads / tx rows, tx = 2^tx_log2 lanes each, and tx vectors of
+// each row; grid.x runs over a row's pieces and grid.y over the rows, both in strides
+// where there are more than kMaxGridX and kMaxGridY.
+//
+// Kernels take their counts as 32-bit words, work out what follows from them (vectors,
+// tiles, the grid itself) and ask for nothing that the runtime passes beside their own
+// arguments: a launch with up to 96 bytes of arguments takes 2.8 us of the host's time,
+// one with 128 or more 3.5 to 3.9, and a use of gridDim adds 66 bytes and more.
+constexpr int64_t kMaxGridX = 1 << 20, kMaxGridY = 65535;
 
 // The row that this thread serves in row tile `tile`; the same for a whole wave
 // where a wave serves one row, which the compiler is told.
 template <bool WAVE_ROW>
-__device__ __forceinline__ int64_t row_of(const Tiling &tl, int64_t tile)
+__device__ __forceinline__ int64_t row_of(int tx_log2, int64_t tile)
 {
-    const int ty = kThreads >> tl.tx_log2;
-    int r = (int)(threadIdx.x >> tl.tx_log2);
+    int r = (int)(threadIdx.x >> tx_log2);
     if constexpr (WAVE_ROW) r = __builtin_amdgcn_readfirstlane(r);
-    return tile * ty + r;
+    return tile * (kThreads >> tx_log2) + r;
 }
 
-#define LRS_FOR_TILES(tl, rows, row, vec)                                                              \
-    for (int64_t tile_ = blockIdx.y; tile_ < (tl).row_tiles; tile_ += gridDim.y)                       \
-        if (const int64_t row = row_of<WAVE_ROW>(tl, tile_); row < (rows))                             \
-            for (int64_t ct_ = blockIdx.x; ct_ < (tl).col_tiles; ct_ += gridDim.x)                     \
-                if (const int64_t vec = (ct_ << (tl).tx_log2) + (threadIdx.x & ((1 << (tl).tx_log2) - 1)); \
-                    vec < (tl).vecs)
+template <typename T>
+__device__ __forceinline__ int vecs_of(int cols)
+{
+    return (int)(((uint32_t)cols + kVec<T> - 1) / (uint32_t)kVec<T>);
+}
+
+__device__ __forceinline__ int64_t tiles_of(int64_t count, int log2) { return (count + (1 << log2) - 1) >> log2; }
+
+constexpr int kThreadsLog2 = 8;
+static_assert(kThreads == 1 << kThreadsLog2, "rows of a tile are found by shifts");
+
+// Calls f(row, vector) for each that this thread serves.  The grid is the number of
+// tiles, up to the two limits: so a step of a limit leaves it at once where there are
+// no more, and nothing has to be worked out before the first loads.
+template <bool WAVE_ROW, typename F>
+__device__ __forceinline__ void for_tiles(int tx_log2, int rows, int vecs, F &&f)
+{
+    int64_t tile = blockIdx.y;
+    do {
+        const int64_t row = row_of<WAVE_ROW>(tx_log2, tile);
+        if (row < rows) {
+            int64_t piece = blockIdx.x;
+            do {
+                const int64_t vec = (piece << tx_log2) + (threadIdx.x & ((1 << tx_log2) - 1));
+                if (vec < vecs) f(row, vec);
+                piece += kMaxGridX;
+            } while (piece << tx_log2 < vecs);
+        }
+        tile += kMaxGridY;
+    } while (tile << (kThreadsLog2 - tx_log2) < rows);
+}
 
 // ------------------------------------------------------------------ grouping
 
@@ -220,7 +244,7 @@ __device__ __forceinline__ int64_t row_of(const Tiling &tl, int64_t tile)
 // `groups` (sorted last), and the indices that travel with them.  `clear`, where
 // given, is a word that the first kernel of an order sets to zero for a later one.
 template <typename ID>
-__global__ __launch_bounds__(kThreads) void group_keys_kernel(const ID *__restrict__ ids, int64_t n, int64_t first,
+__global__ __launch_bounds__(kThreads) void group_keys_kernel(const ID *__restrict__ ids, int n, int64_t first,
                                                               uint32_t groups, uint32_t *__restrict__ keys,
                                                               uint32_t *__restrict__ index, uint32_t *clear)
 {
@@ -270,19 +294,18 @@ __global__ __launch_bounds__(kThreads) void group_finish_kernel(const uint32_t *
 // of the same bytes 157.  T: an unsigned word of the element's size.
 template <typename T, bool WAVE_ROW>
 __global__ __launch_bounds__(kThreads) void dispatch_kernel(const T *__restrict__ x, int64_t ld_x,
-                                                            const int32_t *__restrict__ position, int64_t tokens,
-                                                            int slots, int64_t cols, T *__restrict__ rows,
-                                                            int64_t ld_rows, uint32_t num_rows, Tiling tl)
+                                                            const int32_t *__restrict__ position, int tokens,
+                                                            int slots, int cols, uint32_t num_rows,
+                                                            T *__restrict__ rows, int64_t ld_rows, int tx_log2)
 {
-    LRS_FOR_TILES(tl, tokens, t, vec)
-    {
+    for_tiles<WAVE_ROW>(tx_log2, tokens, vecs_of<T>(cols), [&](int64_t t, int64_t vec) {
         const Col col = col_of<T>(cols, vec * kVec<T>);
         const u32x4 v = load_col<T>(x + t * ld_x, col);
         for (int k = 0; k < slots; ++k) {
             const uint32_t p = (uint32_t)position[t * slots + k];
             if (p < num_rows) store_col<T>(rows + (int64_t)p * ld_rows, v, col);
         }
-    }
+    });
 }
 
 // A token's rows are summed in the order of its slots, in float32, SLOTS of them in
@@ -291,13 +314,12 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(const T *__restrict_
 // eight 217.
 template <typename T, bool WAVE_ROW, int SLOTS, bool NT>
 __global__ __launch_bounds__(kThreads) void combine_kernel(const T *__restrict__ rows, int64_t ld_rows,
-                                                           uint32_t num_rows, const int32_t *__restrict__ position,
-                                                           int weight_type, const void *__restrict__ weights,
-                                                           int64_t tokens, int slots, int64_t cols,
-                                                           T *__restrict__ y, int64_t ld_y, Tiling tl)
+                                                           uint32_t num_rows, int weight_type,
+                                                           const int32_t *__restrict__ position,
+                                                           const void *__restrict__ weights, int tokens, int slots,
+                                                           int cols, int tx_log2, T *__restrict__ y, int64_t ld_y)
 {
-    LRS_FOR_TILES(tl, tokens, t, vec)
-    {
+    for_tiles<WAVE_ROW>(tx_log2, tokens, vecs_of<T>(cols), [&](int64_t t, int64_t vec) {
         const Col col = col_of<T>(cols, vec * kVec<T>);
         float sum[kVec<T>] = {};
         for (int k0 = 0; k0 < slots; k0 += SLOTS) {
@@ -321,7 +343,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const T *__restrict__
                 }
         }
         store_col<T, NT>(y + t * ld_y, pack<T>(sum), col);
-    }
+    });
 }
 
 // Sum over the lanes of a row: a whole wave (WAVE_ROW) or 2^tx_log2 lanes of it, in
@@ -348,7 +370,7 @@ __device__ __forceinline__ float lanes_sum(float v, int tx_log2)
     }
 }
 
-// A row tile serves whole tokens, slot by slot (grid.x of their slots at once): a
+// A row tile serves whole tokens, slot by slot (or, where tokens are `few`, every slot by a workgroup of its own): a
 // slot's row is read, its inner product with the token's grad_y formed, and its
 // gradient stored; grad_y comes from cache after the first slot.  rows and grad_rows
 // may be the same memory: a thread reads each element before it stores there.  Bound
@@ -357,24 +379,26 @@ __device__ __forceinline__ float lanes_sum(float v, int tx_log2)
 // 447 and 469, a wave per token (no barrier) 478, a workgroup per slot 468.
 template <typename T, bool WAVE_ROW, bool NT>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(const T *__restrict__ grad_y, int64_t ld_grad_y,
-                                                                const T *rows, int64_t ld_rows, uint32_t num_rows,
-                                                                const int32_t *__restrict__ position, int weight_type,
-                                                                const void *__restrict__ weights, int64_t tokens,
-                                                                int slots, int64_t cols, T *grad_rows,
+                                                                const T *rows, int64_t ld_rows,
+                                                                const int32_t *__restrict__ position,
+                                                                const void *__restrict__ weights, T *grad_rows,
                                                                 int64_t ld_grad_rows, void *__restrict__ grad_weights,
-                                                                Tiling tl)
+                                                                uint32_t num_rows, int tokens, int slots, int cols,
+                                                                int8_t weight_type, int8_t tx_log2, int16_t few)
 {
     __shared__ float s_part[kThreads / kWave];
-    const int lane = threadIdx.x & ((1 << tl.tx_log2) - 1);
-    const int waves = 1 << tl.tx_log2 >> 6;  // per token; 0 where a wave serves several
-    for (int64_t tile = blockIdx.y; tile < tl.row_tiles; tile += gridDim.y) {
-        const int64_t t = row_of<WAVE_ROW>(tl, tile);
-        for (int64_t k = blockIdx.x; k < slots; k += gridDim.x) {
+    const int lane = threadIdx.x & ((1 << tx_log2) - 1);
+    const int waves = 1 << tx_log2 >> 6;  // per token; 0 where a wave serves several
+    const int vecs = vecs_of<T>(cols);
+    const int64_t tiles = tiles_of(tokens, kThreadsLog2 - tx_log2), at_once = few ? kMaxGridX : 1;
+    for (int64_t tile = blockIdx.y; tile < tiles; tile += kMaxGridY) {
+        const int64_t t = row_of<WAVE_ROW>(tx_log2, tile);
+        for (int64_t k = blockIdx.x; k < slots; k += at_once) {
             const uint32_t p = t < tokens ? (uint32_t)position[t * slots + k] : ~0u;
             float dot = 0.0f;
             if (p < num_rows) {
                 const float w = weights != nullptr ? load_scalar(weights, weight_type, t * slots + k) : 1.0f;
-                for (int64_t vec = lane; vec < tl.vecs; vec += 1 << tl.tx_log2) {
+                for (int64_t vec = lane; vec < vecs; vec += 1 << tx_log2) {
                     const Col col = col_of<T>(cols, vec * kVec<T>);
                     u32x4 g = issue<T>(grad_y + t * ld_grad_y, col);
                     u32x4 r = {0u, 0u, 0u, 0u};
@@ -391,7 +415,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(const T *__restr
                 }
             }
             if (grad_weights == nullptr) continue;
-            dot = lanes_sum<WAVE_ROW>(dot, tl.tx_log2);
+            dot = lanes_sum<WAVE_ROW>(dot, tx_log2);
             if (waves > 1) {
                 __syncthreads();  // (the last slot's parts have been read)
                 if ((threadIdx.x & (kWave - 1)) == 0) s_part[threadIdx.x / kWave] = dot;
@@ -413,12 +437,11 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(const T *__restr
 // instead of 110 (the table's rows that occur are read once, 0.4 GB in all).
 template <typename T, typename ID, bool WAVE_ROW, bool NT>
 __global__ __launch_bounds__(kThreads) void embedding_kernel(const T *__restrict__ table, int64_t ld_table,
-                                                             uint32_t num_ids, const ID *__restrict__ ids, int64_t n,
-                                                             int64_t first, float scale, int64_t cols,
-                                                             T *__restrict__ y, int64_t ld_y, Tiling tl)
+                                                             const ID *__restrict__ ids, int64_t first,
+                                                             uint32_t num_ids, int n, int cols, float scale,
+                                                             T *__restrict__ y, int64_t ld_y, int tx_log2)
 {
-    LRS_FOR_TILES(tl, n, i, vec)
-    {
+    for_tiles<WAVE_ROW>(tx_log2, n, vecs_of<T>(cols), [&](int64_t i, int64_t vec) {
         const Col col = col_of<T>(cols, vec * kVec<T>);
         const uint64_t v = (uint64_t)ids[i] - (uint64_t)first;
         u32x4 r = {0u, 0u, 0u, 0u};
@@ -432,7 +455,7 @@ __global__ __launch_bounds__(kThreads) void embedding_kernel(const T *__restrict
             }
         }
         store_col<T, NT>(y + i * ld_y, r, col);
-    }
+    });
 }
 
 // The gradient's sums, bound by HBM: 65,536 ids x 4096 bf16 of 131,072 rows take 302 us
@@ -451,11 +474,23 @@ __global__ __launch_bounds__(kThreads) void embedding_kernel(const T *__restrict
 constexpr int kKeyPad = 16;
 
 struct Pieces {
-    int64_t n;        // sorted slots
-    int piece;        // slots per piece
-    int64_t count;    // pieces
-    uint32_t groups;  // ids at or above it are of no row (sorted last)
-    uint32_t *list;   // its length (0 before), then the pieces in which a long run begins
+    const uint32_t *__restrict__ keys;   // sorted, and the indices that travelled with them
+    const uint32_t *__restrict__ order;
+    float *__restrict__ partial;  // two rows of whole vectors per piece
+    uint32_t *list;               // its length (0 before), then the pieces in which a long run begins
+    int n, piece;                 // sorted slots, and slots per piece
+    uint32_t groups;              // ids at or above it are of no row (sorted last)
+    int cols;
+    __device__ __forceinline__ int64_t count() const { return ((int64_t)n + piece - 1) / piece; }
+};
+
+// Where the sums go: scale * sum, added to what is there if `accumulate`, rounded once.
+template <typename G>
+struct GradOut {
+    G *grad;
+    int64_t ld;
+    float scale;
+    int accumulate;
 };
 
 template <typename G, int E>
@@ -470,14 +505,15 @@ __device__ __forceinline__ void store_values(G *p, const float (&v)[E], int vali
     }
 }
 
-// scale * sum, added to what is there if `accumulate`, rounded once.  The columns are
-// those of a vector of E elements, one vector of G or two.
+// A vector of a run's sums to its row: one vector of G, or two.
 template <typename G, int E>
-__device__ __forceinline__ void store_grad(G *row, const float (&sum)[E], float scale, int accumulate, int64_t cols,
+__device__ __forceinline__ void store_grad(const GradOut<G> &out, uint32_t run, const float (&sum)[E], int cols,
                                            const Col &col)
 {
+    G *row = out.grad + (int64_t)run * out.ld;
+    const float scale = out.scale;
     float v[E];
-    if (accumulate) {
+    if (out.accumulate) {
         u32x4 old[E / kVec<G>];
 #pragma unroll
         for (int q = 0; q < E / kVec<G>; ++q) old[q] = issue<G>(row, col_of<G>(cols, col.c + q * kVec<G>));
@@ -496,13 +532,14 @@ __device__ __forceinline__ void store_grad(G *row, const float (&sum)[E], float 
 }
 
 template <typename T, typename G, bool NT>
-__device__ __forceinline__ void sum_piece(const T *__restrict__ grad_y, int64_t ld_grad_y, const uint32_t *__restrict__ keys,
-                          const uint32_t *__restrict__ order, Pieces pc, float scale, G *__restrict__ grad,
-                          int64_t ld_grad, int64_t cols, int64_t cols_padded, float *__restrict__ partial,
-                          int accumulate, int64_t piece, int64_t vec)
+__device__ __forceinline__ void sum_piece(const T *__restrict__ grad_y, int64_t ld_grad_y, const Pieces &pc,
+                                          const GradOut<G> &out, int64_t piece, int64_t vec)
 {
     constexpr int E = kVec<T>;
-        constexpr int UNROLL = 8;  // rows in flight per lane (4: 16,384 x 2048 added in 75 us instead of 69)
+    constexpr int UNROLL = 8;  // rows in flight per lane (4: 16,384 x 2048 added in 75 us instead of 69)
+    const uint32_t *__restrict__ keys = pc.keys, *__restrict__ order = pc.order;
+    const int cols = pc.cols;
+    const int64_t cols_padded = (int64_t)vecs_of<T>(cols) * E;
     const Col col = col_of<T>(cols, vec * E);
     const int64_t lo = piece * pc.piece;
     const int64_t hi = lo + pc.piece < pc.n ? lo + pc.piece : pc.n;
@@ -523,9 +560,9 @@ __device__ __forceinline__ void sum_piece(const T *__restrict__ grad_y, int64_t 
     auto leave = [&](bool partly) {
         if (run >= pc.groups || passed) return;
         if (here && !partly)
-            store_grad<G, E>(grad + (int64_t)run * ld_grad, sum, scale, accumulate, cols, col);
+            store_grad<G, E>(out, run, sum, cols, col);
         else  // (padded rows of whole vectors: no partial store)
-            store_values<float, E>(partial + (piece * 2 + (here ? 1 : 0)) * cols_padded + col.c, sum, E);
+            store_values<float, E>(pc.partial + (piece * 2 + (here ? 1 : 0)) * cols_padded + col.c, sum, E);
     };
     bool on = true;
     for (int64_t j = lo; on; j += UNROLL) {
@@ -586,9 +623,10 @@ __device__ __forceinline__ int64_t wave_lower_bound(const uint32_t *__restrict__
 constexpr int kFillRows = 16;
 
 template <typename G>
-__device__ __forceinline__ void fill_rows(const uint32_t *__restrict__ keys, int64_t n, G *__restrict__ grad, int64_t ld_grad,
-                          int64_t num_ids, int64_t cols, int64_t tile, const Tiling &tl)
+__device__ __forceinline__ void fill_rows(const Pieces &pc, const GradOut<G> &out, int64_t tile, int tx_log2)
 {
+    const uint32_t *__restrict__ keys = pc.keys;
+    const int64_t n = pc.n, num_ids = pc.groups;
     __shared__ int64_t s_range[2];
     __shared__ int s_named[kFillRows];
     __syncthreads();
@@ -618,40 +656,35 @@ __device__ __forceinline__ void fill_rows(const uint32_t *__restrict__ keys, int
     }
     __syncthreads();
     const u32x4 zero = {0u, 0u, 0u, 0u};
-    const int rows_at_once = kThreads >> tl.tx_log2, lane = threadIdx.x & ((1 << tl.tx_log2) - 1);
-    for (int q = threadIdx.x >> tl.tx_log2; q < kFillRows; q += rows_at_once) {
+    const int rows_at_once = kThreads >> tx_log2, lane = threadIdx.x & ((1 << tx_log2) - 1);
+    const int vecs = vecs_of<G>(pc.cols);
+    for (int q = threadIdx.x >> tx_log2; q < kFillRows; q += rows_at_once) {
         if (s_named[q]) continue;
-        G *row = grad + (tile * kFillRows + q) * ld_grad;
-        for (int64_t vec = lane; vec < tl.vecs; vec += 1 << tl.tx_log2) {
-            const int64_t c = vec * kVec<G>;
-            store_col<G>(row, zero, col_of<G>(cols, c));
-        }
+        G *row = out.grad + (tile * kFillRows + q) * out.ld;
+        for (int64_t vec = lane; vec < vecs; vec += 1 << tx_log2)
+            store_col<G>(row, zero, col_of<G>(pc.cols, vec * kVec<G>));
     }
 }
 
 // The first `sum_blocks` workgroups sum pieces, the others write the empty rows.
 template <typename T, typename G, bool WAVE_ROW, bool NT>
 __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(const T *__restrict__ grad_y, int64_t ld_grad_y,
-                                                                  const uint32_t *__restrict__ keys,
-                                                                  const uint32_t *__restrict__ order, Pieces pc,
-                                                                  float scale, G *__restrict__ grad, int64_t ld_grad,
-                                                                  int64_t num_ids, int64_t cols, int64_t cols_padded,
-                                                                  float *__restrict__ partial, int accumulate,
-                                                                  uint32_t sum_blocks, Tiling tl, Tiling fill)
+                                                                  Pieces pc, GradOut<G> out, uint32_t sum_blocks,
+                                                                  int16_t tx_log2, int16_t fill_tx_log2)
 {
     if (blockIdx.x < sum_blocks) {
-        const int64_t units = tl.row_tiles * tl.col_tiles;
+        const int vecs = vecs_of<T>(pc.cols);
+        const int64_t count = pc.count(), col_tiles = tiles_of(vecs, tx_log2);
+        const int64_t units = tiles_of(count, kThreadsLog2 - tx_log2) * col_tiles;
         for (int64_t unit = blockIdx.x; unit < units; unit += sum_blocks) {
-            const int64_t piece = row_of<WAVE_ROW>(tl, unit / tl.col_tiles);
-            const int64_t vec = ((unit % tl.col_tiles) << tl.tx_log2) + (threadIdx.x & ((1 << tl.tx_log2) - 1));
-            if (piece < pc.count && vec < tl.vecs)
-                sum_piece<T, G, NT>(grad_y, ld_grad_y, keys, order, pc, scale, grad, ld_grad, cols, cols_padded, partial,
-                                    accumulate, piece, vec);
+            const int64_t piece = row_of<WAVE_ROW>(tx_log2, unit / col_tiles);
+            const int64_t vec = ((unit % col_tiles) << tx_log2) + (threadIdx.x & ((1 << tx_log2) - 1));
+            if (piece < count && vec < vecs) sum_piece<T, G, NT>(grad_y, ld_grad_y, pc, out, piece, vec);
         }
     } else {
-        const int64_t tiles = (num_ids + kFillRows - 1) / kFillRows;
-        for (int64_t t = blockIdx.x - sum_blocks; t < tiles; t += gridDim.x - sum_blocks)
-            fill_rows<G>(keys, pc.n, grad, ld_grad, num_ids, cols, t, fill);
+        const int64_t tiles = ((int64_t)pc.groups + kFillRows - 1) / kFillRows;
+        for (int64_t t = blockIdx.x - sum_blocks; t < tiles; t += kMaxGridX)
+            fill_rows<G>(pc, out, t, fill_tx_log2);
     }
 }
 
@@ -660,27 +693,27 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(const T *__res
 // lanes of four); eight slices of the workgroup add a contiguous part of the pieces
 // each, and their sums are joined in order.
 constexpr int kJoinLanes = 32;
+constexpr int64_t kMaxJoins = 4096;
 
 template <typename G>
-__global__ __launch_bounds__(kThreads) void embedding_join_kernel(const uint32_t *__restrict__ keys, Pieces pc,
-                                                                  float scale, G *__restrict__ grad, int64_t ld_grad,
-                                                                  int64_t cols, int64_t cols_padded,
-                                                                  const float *__restrict__ partial, int accumulate,
-                                                                  int64_t col_tiles)
+__global__ __launch_bounds__(kThreads) void embedding_join_kernel(Pieces pc, GradOut<G> out, int cols_padded)
 {
+    const uint32_t *__restrict__ keys = pc.keys;
+    const int cols = pc.cols;
+    const int64_t count = pc.count(), col_tiles = (cols + 4 * kJoinLanes - 1) / (4 * kJoinLanes);
     constexpr int LANES = kJoinLanes, SLICES = kThreads / LANES;
     __shared__ float s_sum[SLICES][LANES][4];
     __shared__ int64_t s_more;
     const int lane = threadIdx.x & (LANES - 1), slice = threadIdx.x / LANES;
     const int64_t units = (int64_t)pc.list[0] * col_tiles;
-    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    for (int64_t unit = blockIdx.x; unit < units; unit += kMaxJoins) {
         const int64_t piece = pc.list[1 + unit / col_tiles];
         const uint32_t run = keys[(piece + 1) * pc.piece];
         if (threadIdx.x < kWave) {  // how many pieces after it begin with the run
             int64_t more = 2;
             for (;;) {
                 const int64_t q = piece + 1 + more + threadIdx.x;
-                const uint64_t same = __ballot(q < pc.count && keys[q * pc.piece] == run);
+                const uint64_t same = __ballot(q < count && keys[q * pc.piece] == run);
                 const int on = same == ~0ull ? kWave : __builtin_ctzll(~same);
                 more += on;
                 if (on < kWave) break;
@@ -696,7 +729,8 @@ __global__ __launch_bounds__(kThreads) void embedding_join_kernel(const uint32_t
         if (c < cols) {
 #pragma unroll 8
             for (int64_t q = from; q < to; ++q) {
-                const u32x4 r = *reinterpret_cast<const u32x4 *>(partial + ((piece + q) * 2 + (q == 0)) * cols_padded + c);
+                const u32x4 r = *reinterpret_cast<const u32x4 *>(pc.partial +
+                                                                       ((piece + q) * 2 + (q == 0)) * cols_padded + c);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sum[e] += element<float>(r, e);
             }
@@ -710,10 +744,11 @@ __global__ __launch_bounds__(kThreads) void embedding_join_kernel(const uint32_t
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sum[e] += s_sum[w][lane][e];
             // (four columns are half a vector of 16-bit elements: element by element)
-            G *p = grad + (int64_t)run * ld_grad + c;
+            G *p = out.grad + (int64_t)run * out.ld + c;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (c + e < cols) p[e] = (G)(accumulate ? __builtin_fmaf(scale, sum[e], (float)p[e]) : scale * sum[e]);
+                if (c + e < cols)
+                    p[e] = (G)(out.accumulate ? __builtin_fmaf(out.scale, sum[e], (float)p[e]) : out.scale * sum[e]);
         }
         __syncthreads();
     }

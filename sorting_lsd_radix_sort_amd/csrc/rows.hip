@@ -20,7 +20,6 @@ using namespace lrs_rows;
 
 constexpr size_t kAlign = 256;
 constexpr int64_t kMaxCount = 0x7FFFFFFFll;  // positions and offsets are int32
-constexpr int64_t kMaxGridX = 1 << 20, kMaxGridY = 65535;
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
@@ -81,6 +80,11 @@ bool overlap(const Span &a, const Span &b)
 lrs_status launched() { return hipGetLastError() == hipSuccess ? LRS_OK : LRS_ERR_HIP; }
 
 // Lanes per row: as many as its vectors, a power of two up to a workgroup.
+struct Tiling {
+    int tx_log2;
+    int64_t vecs, row_tiles, col_tiles;
+};
+
 Tiling tiling_of(int64_t rows, int64_t cols, int vec)
 {
     Tiling t;
@@ -275,7 +279,7 @@ lrs_status sort_ids(const GroupLayout &L, char *temp, const void *ids, int64_t n
         uint32_t *counts = (uint32_t *)(temp + L.off_sort);
         for (int p = 0; p < passes; ++p) {
             const int shift = p * width, bits = std::min(width, std::max(L.bits, 1) - shift);
-            const Pass ps{n, shift, bits, (1u << bits) - 1u, 1u << bits};
+            const Pass ps{(int)n, (1u << bits) - 1u, (uint16_t)(1u << bits), (uint8_t)shift, (uint8_t)bits};
             // the passes alternate between the two pairs of arrays so that the last
             // one writes the sorted ones
             const bool to_out = (passes - 1 - p) % 2 == 0;
@@ -287,7 +291,7 @@ lrs_status sort_ids(const GroupLayout &L, char *temp, const void *ids, int64_t n
         }
         return LRS_OK;
     }
-    group_keys_kernel<ID><<<flat_grid(n), kThreads, 0, stream>>>((const ID *)ids, n, first, (uint32_t)groups, keys, at,
+    group_keys_kernel<ID><<<flat_grid(n), kThreads, 0, stream>>>((const ID *)ids, (int)n, first, (uint32_t)groups, keys, at,
                                                                 clear);
     const lrs_status st = launched();
     if (st != LRS_OK) return st;
@@ -323,7 +327,7 @@ lrs_status group_direct(const void *ids, int64_t n, int64_t first, int64_t group
                         int32_t *position, int32_t *offsets, hipStream_t stream)
 {
     const IdSource<ID> src{(const ID *)ids, first, (uint32_t)groups};
-    const Pass ps{n, 0, bits_of(groups + 1), ~0u, (uint32_t)groups + 1};
+    const Pass ps{(int)n, ~0u, (uint16_t)(groups + 1), 0, (uint8_t)bits_of(groups + 1)};
     return run_pass(src, ps, counts, PlaceOut{nullptr, (uint32_t *)order, position, offsets}, nullptr, stream);
 }
 
@@ -404,8 +408,8 @@ LRS_API lrs_status lrs_dispatch_rows(lrs_row_type type, const void *d_x, int64_t
         using W = decltype(word);
         const Tiling t = tiling_of(tokens, cols, kVec<W>);
         auto *k = wave_row(t) ? dispatch_kernel<W, true> : dispatch_kernel<W, false>;
-        k<<<grid_of(t), kThreads, kDispatchLds, stream>>>((const W *)d_x, ld_x, d_position, tokens, (int)slots, cols,
-                                                          (W *)d_rows, ld_rows, (uint32_t)num_rows, t);
+        k<<<grid_of(t), kThreads, kDispatchLds, stream>>>((const W *)d_x, ld_x, d_position, (int)tokens, (int)slots,
+                                                          (int)cols, (uint32_t)num_rows, (W *)d_rows, ld_rows, t.tx_log2);
         return launched();
     };
     return b == 4 ? run(uint32_t{}) : run(uint16_t{});
@@ -432,8 +436,8 @@ LRS_API lrs_status lrs_combine_rows(lrs_row_type type, const void *d_rows, int64
         const Tiling t = tiling_of(tokens, cols, kVec<T>);
         auto pick = [&](auto wave, auto slots_at_once, auto nt) {
             combine_kernel<T, wave.value, slots_at_once.value, nt.value><<<grid_of(t), kThreads, 0, stream>>>(
-                (const T *)d_rows, ld_rows, (uint32_t)num_rows, d_position, (int)weight_type, d_weights, tokens,
-                (int)slots, cols, (T *)d_y, ld_y, t);
+                (const T *)d_rows, ld_rows, (uint32_t)num_rows, (int)weight_type, d_position, d_weights, (int)tokens,
+                (int)slots, (int)cols, t.tx_log2, (T *)d_y, ld_y);
         };
         const bool few = t.row_tiles * t.col_tiles < kFewTiles;
         with_bool(wave_row(t), [&](auto wave) {
@@ -477,14 +481,15 @@ LRS_API lrs_status lrs_combine_rows_grad(lrs_row_type type, const void *d_grad_y
         Tiling t = tiling_of(tokens, cols, kVec<T>);
         // Few tokens: a workgroup per slot, so that more of the chip works (grad_y
         // is then read once per slot, from cache).
-        const int64_t at_once = t.row_tiles < kFewTiles ? slots : 1;
+        const bool few = t.row_tiles < kFewTiles;
+        const int64_t at_once = few ? slots : 1;
         const dim3 grid((unsigned)std::min(at_once, kMaxGridX), (unsigned)std::min(t.row_tiles, kMaxGridY));
         with_bool(wave_row(t), [&](auto wave) {
             with_bool(streams((2 * n + tokens) * cols * b), [&](auto nt) {
                 combine_grad_kernel<T, wave.value, nt.value><<<grid, kThreads, 0, stream>>>(
-                    (const T *)d_grad_y, ld_grad_y, (const T *)d_rows, ld_rows, (uint32_t)num_rows, d_position,
-                    (int)weight_type, d_weights, tokens, (int)slots, cols, (T *)d_grad_rows, ld_grad_rows,
-                    d_grad_weights, t);
+                    (const T *)d_grad_y, ld_grad_y, (const T *)d_rows, ld_rows, d_position, d_weights,
+                    (T *)d_grad_rows, ld_grad_rows, d_grad_weights, (uint32_t)num_rows, (int)tokens, (int)slots,
+                    (int)cols, (int8_t)weight_type, (int8_t)t.tx_log2, few);
             });
         });
         return launched();
@@ -512,8 +517,8 @@ LRS_API lrs_status lrs_embedding(lrs_row_type type, const void *d_table, int64_t
             with_bool(wave_row(t), [&](auto wave) {
                 with_bool(streams(2 * n * cols * b), [&](auto nt) {
                     embedding_kernel<T, ID, wave.value, nt.value><<<grid_of(t), kThreads, 0, stream>>>(
-                        (const T *)d_table, ld_table, (uint32_t)num_ids, (const ID *)d_ids, n, first_id, scale, cols,
-                        (T *)d_y, ld_y, t);
+                        (const T *)d_table, ld_table, (const ID *)d_ids, first_id, (uint32_t)num_ids, (int)n,
+                        (int)cols, scale, (T *)d_y, ld_y, t.tx_log2);
                 });
             });
             return launched();
@@ -579,11 +584,12 @@ lrs_status embedding_grad_entry(void *d_temp, size_t *temp_bytes, lrs_row_type t
     uint32_t *list = (uint32_t *)(temp + align_up(L.total) + S.partial_bytes);
     st = sort_ids(L, temp, id_type, d_ids, n, first, num_ids, nullptr, &sorted, &index, S.joins() ? list : nullptr, stream);
     if (st != LRS_OK) return st;
-    const Pieces pc{n, S.piece, S.count, (uint32_t)num_ids, list};
+    const Pieces pc{sorted, index, partial, list, (int)n, S.piece, (uint32_t)num_ids, (int)cols};
     return with_type(type, [&](auto elem) {
         using T = decltype(elem);
         auto run = [&](auto gelem) {
             using G = decltype(gelem);
+            const GradOut<G> out{(G *)d_grad, ld_grad, scale, accumulate ? 1 : 0};
             const Tiling t = tiling_of(S.count, cols, kVec<T>);
             Tiling fill = tiling_of(num_ids, cols, kVec<G>);
             fill.tx_log2 = std::min(fill.tx_log2, 6);  // a wave per row
@@ -593,16 +599,14 @@ lrs_status embedding_grad_entry(void *d_temp, size_t *temp_bytes, lrs_row_type t
             with_bool(wave_row(t), [&](auto wave) {
                 with_bool(n * cols * b > kLastCacheBytes, [&](auto nt) {
                     embedding_grad_kernel<T, G, wave.value, nt.value><<<sums + fills, kThreads, 0, stream>>>(
-                        (const T *)d_grad_y, ld_grad_y, sorted, index, pc, scale, (G *)d_grad, ld_grad, num_ids, cols,
-                        S.cols_padded, partial, accumulate, sums, t, fill);
+                        (const T *)d_grad_y, ld_grad_y, pc, out, sums, (int16_t)t.tx_log2, (int16_t)fill.tx_log2);
                 });
             });
             const lrs_status st = launched();
             if (st != LRS_OK || !S.joins()) return st;
             const int64_t join_tiles = (cols + 4 * kJoinLanes - 1) / (4 * kJoinLanes);
-            const unsigned joins = (unsigned)std::min<int64_t>((S.count + 1) / 2 * join_tiles, 4096);
-            embedding_join_kernel<G><<<joins, kThreads, 0, stream>>>(sorted, pc, scale, (G *)d_grad, ld_grad, cols,
-                                                                     S.cols_padded, partial, accumulate, join_tiles);
+            const unsigned joins = (unsigned)std::min((S.count + 1) / 2 * join_tiles, kMaxJoins);
+            embedding_join_kernel<G><<<joins, kThreads, 0, stream>>>(pc, out, (int)S.cols_padded);
             return launched();
         };
         return grad_type == LRS_ROW_F32 ? run(float{}) : run(elem);
