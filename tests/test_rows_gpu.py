@@ -796,6 +796,71 @@ def test_conveniences_on_a_side_stream(as_int):
             assert torch.equal(got, want)
 
 
+def test_calls_from_several_threads():
+    """Host threads, each on a stream of its own, through the conveniences at once."""
+    import threading
+    torch = torch_()
+    announce("several threads")
+    chosen, w = [routing(1500 + 100 * i, 3, 12, 170 + i) for i in range(4)], [torch.rand(1500 + 100 * i, 3, device="cuda")
+                                                                              for i in range(4)]
+    x = [randn((1500 + 100 * i, 264), "bf16", 180 + i) for i in range(4)]
+
+    def work(i):
+        order, position, offsets = lrs.group_tokens(chosen[i], 12)
+        rows = lrs.dispatch_rows(x[i], position)
+        y = lrs.combine_rows(rows, position, w[i])
+        grad_rows, grad_w = lrs.combine_rows_grad(y, rows, position, w[i])
+        ids = chosen[i][:, 0].contiguous()
+        return [order, position, offsets, rows, y, grad_rows, grad_w, lrs.embedding_grad(y, ids, 700 + i)]
+
+    want = [work(i) for i in range(4)]
+    torch.cuda.synchronize()
+    got = [[] for _ in range(4)]
+
+    def thread(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(5):
+                got[i].append(work(i))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(4):
+        assert len(got[i]) == 5
+        for answers in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(answers, want[i]))
+
+
+def test_tensors_of_two_devices_and_given_temp():
+    torch = torch_()
+    announce("two devices, given temp")
+    ids, x = routing(300, 2, 9, 190), randn((300, 40), "f32", 191)
+    order, position, offsets = lrs.group_tokens(ids, 9)
+    rows, w = lrs.dispatch_rows(x, position), torch.rand(300, 2, device="cuda")
+    flat = ids[:, 0].contiguous()
+    for call in (lambda: lrs.dispatch_rows(x, position.cpu()), lambda: lrs.dispatch_rows(x.cpu(), position),
+                 lambda: lrs.dispatch_rows(x, position, out=torch.zeros(600, 40)),
+                 lambda: lrs.combine_rows(rows, position, w.cpu()), lambda: lrs.combine_rows(rows.cpu(), position),
+                 lambda: lrs.combine_rows_grad(x.cpu(), rows, position, w), lambda: lrs.embedding(x, flat.cpu()),
+                 lambda: lrs.embedding(x.cpu(), flat), lambda: lrs.embedding_grad(x, flat.cpu(), 9),
+                 lambda: lrs.embedding_grad(x, flat, 9, grad=torch.zeros(9, 40)),
+                 lambda: lrs.group_tokens(ids, 9, temp=torch.zeros(1 << 20)),
+                 lambda: lrs.embedding_grad(x, flat, 9, temp=torch.zeros(1 << 20))):
+        with pytest.raises(ValueError, match="is on|device tensors"):
+            call()
+    for temp in (torch.empty(1 << 22, dtype=torch.uint8, device="cuda"), torch.empty(1, device="cuda")):
+        assert all(torch.equal(a, b) for a, b in zip(lrs.group_tokens(ids, 9, temp=temp), (order, position, offsets)))
+        assert torch.equal(lrs.embedding_grad(x, flat, 9, temp=temp), lrs.embedding_grad(x, flat, 9))
+    big = routing(20000, 2, 9, 192)
+    temp = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    assert all(torch.equal(a, b) for a, b in zip(lrs.group_tokens(big, 9, temp=temp), lrs.group_tokens(big, 9)))
+
+
 def test_results_are_the_same_on_every_run():
     torch = torch_()
     announce("same on every run")
