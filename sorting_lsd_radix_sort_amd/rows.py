@@ -123,15 +123,17 @@ def lrs_embedding_grad(d_temp, temp_bytes, row_type, d_grad_y, ld_grad_y, id_typ
 # by their index, the C functions called with plain addresses, and the temp bytes of
 # a size asked for once.
 
-_types = None  # ({torch dtype: code} of ids, of rows, torch.int32)
+_types = None  # ({torch dtype: code} of ids, of rows, torch.int32), once torch is there
+_torch = None
 _needs: dict = {}  # temp bytes by sizes and types, which alone decide them
 _functions: dict = {}  # C functions of the loaded library
 _current_handle = None  # device index -> handle of its current stream, once looked for
 
 
 def _type_codes():
-    global _types
+    global _types, _torch
     import torch
+    _torch = torch
     _types = ({torch.int32: 0, torch.int64: 1}, {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}, torch.int32)
     return _types
 
@@ -219,6 +221,8 @@ def _weights(weights, position):
 
 
 def _int64(name, v) -> int:
+    if v == 0:
+        return 0
     v = int(v)
     if not -2**63 <= v < 2**63:
         raise ValueError("%s %d is no int64" % (name, v))
@@ -230,10 +234,8 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _function(name):
-    fn = _functions.get(name)
-    if fn is None:
-        fn = _functions[name] = getattr(load_library(), name)
+def _load(name):
+    fn = _functions[name] = getattr(load_library(), name)
     return fn
 
 
@@ -247,9 +249,8 @@ def _handle_lookup():
     return _current_handle
 
 
-def _on_device(t) -> None:
-    if not t.is_cuda:
-        raise ValueError("lrsort needs device tensors, got a tensor on %s" % t.device)
+def _host_tensor(t):
+    return ValueError("lrsort needs device tensors, got a tensor on %s" % t.device)
 
 
 def _run(name, stream, tensors, args) -> None:
@@ -258,14 +259,14 @@ def _run(name, stream, tensors, args) -> None:
     On another stream the work waits for what the current one holds (inputs copied
     and outputs allocated there), and the tensors are recorded on it, so that the
     caching allocator does not hand their memory on while it is in use there."""
-    import torch
-    fn = _function(name)
+    fn = _functions.get(name) or _load(name)
     index = tensors[0].get_device()
-    if stream is None and torch.cuda.current_device() == index:
+    if stream is None and _torch.cuda.current_device() == index:
         status = fn(*args, (_current_handle or _handle_lookup())(index) or None)
         if status:
             _check(status, name)
         return
+    torch = _torch
     current = torch.cuda.current_stream(index)
     handle = current.cuda_stream if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
     side = None
@@ -286,12 +287,11 @@ def _temp(name, sizes, args, like, temp):
     """Temp storage for the C call `name` (args: what follows temp_bytes, without the
     stream), and its size.  `sizes`: what the size depends on.  255 bytes are the
     alignment's alone: the call then needs no storage, and any address will do."""
-    import torch
     key = (name,) + sizes
     need = _needs.get(key)
     if need is None:
         tb = ctypes.c_size_t(0)
-        _check(_function(name)(None, ctypes.byref(tb), *args, None), name)
+        _check((_functions.get(name) or _load(name))(None, ctypes.byref(tb), *args, None), name)
         if len(_needs) >= 4096:
             _needs.clear()
         need = _needs[key] = tb.value
@@ -303,7 +303,7 @@ def _temp(name, sizes, args, like, temp):
             return temp, size
     if need <= 255:
         return like, need
-    return torch.empty(need, dtype=torch.uint8, device=like.device), need
+    return _torch.empty(need, dtype=_torch.uint8, device=like.device), need
 
 
 def group_tokens(ids, num_groups: int, first_id: int = 0, temp=None, stream=None):
@@ -312,12 +312,12 @@ def group_tokens(ids, num_groups: int, first_id: int = 0, temp=None, stream=None
     order, the flat indices sorted by group, those of no group last; position, of
     the shape of ids, where each stands in that order, or -1; offsets
     (num_groups + 1), where each group begins and the last ends."""
-    import torch
     code = _id_code(ids)
-    _on_device(ids)
+    if not ids.is_cuda:
+        raise _host_tensor(ids)
     ids = ids.contiguous()
     n, num_groups, int32 = ids.numel(), int(num_groups), _types[2]
-    position = torch.empty_like(ids, dtype=int32)
+    position = _torch.empty_like(ids, dtype=int32)
     order = position.new_empty(n)
     offsets = position.new_empty(num_groups + 1 if num_groups > 0 else 1)
     args = (code, ids.data_ptr(), n, _int64("first_id", first_id), num_groups, order.data_ptr(), position.data_ptr(),
@@ -342,7 +342,8 @@ def dispatch_rows(x, position, num_rows: int | None = None, out=None, stream=Non
         raise ValueError("position is for %d tokens, x has %d" % (t, tokens))
     if out is not None:
         num_rows, ld_out = _rows_out("out", out, num_rows, cols, x)
-    _on_device(x)
+    if not x.is_cuda:
+        raise _host_tensor(x)
     if out is None:
         num_rows, ld_out = t * slots if num_rows is None else int(num_rows), cols
         out = x.new_empty(num_rows, cols)
@@ -362,7 +363,8 @@ def combine_rows(rows, position, weights=None, out=None, stream=None):
     w, wcode = _weights(weights, pos)
     tokens, slots = pos.shape
     ld_out = cols if out is None else _rows_out("out", out, tokens, cols, rows)[1]
-    _on_device(rows)
+    if not rows.is_cuda:
+        raise _host_tensor(rows)
     if out is None:
         out = rows.new_empty(tokens, cols)
     rows, ld = _rows_in(rows, num_rows, cols)
@@ -390,7 +392,8 @@ def combine_rows_grad(grad_y, rows, position, weights, grad_rows=None, stream=No
     if grad_y.get_device() != rows.get_device():
         raise _elsewhere("grad_y", grad_y, rows)
     ld_out = cols if grad_rows is None else _rows_out("grad_rows", grad_rows, num_rows, cols, rows)[1]
-    _on_device(rows)
+    if not rows.is_cuda:
+        raise _host_tensor(rows)
     if grad_rows is None:
         grad_rows = rows.new_zeros(num_rows, cols)
     grad_w = None if w is None else w.new_empty(tokens, slots)
@@ -420,7 +423,8 @@ def embedding(table, ids, scale: float = 1.0, first_id: int = 0, out=None, strea
                 raise ValueError("out must be contiguous")
             y = out.view(n, cols)
         ld_y = _rows_out("out", y, n, cols, table)[1]
-    _on_device(table)
+    if not table.is_cuda:
+        raise _host_tensor(table)
     if out is None:
         y = out = table.new_empty(shape)
     table, ld = _rows_in(table, num_ids, cols)
@@ -439,7 +443,6 @@ def embedding_grad(grad_y, ids, num_ids: int, scale: float = 1.0, first_id: int 
     default, or float32): `grad` if given.  accumulate: the gradient is added to
     `grad`, and rows that no id names are not touched; otherwise every row is
     written."""
-    import torch
     code, id_code, num_ids = _row_code("grad_y", grad_y.dtype), _id_code(ids), int(num_ids)
     if ids.get_device() != grad_y.get_device():
         raise _elsewhere("ids", ids, grad_y)
@@ -448,7 +451,7 @@ def embedding_grad(grad_y, ids, num_ids: int, scale: float = 1.0, first_id: int 
     n, cols = ids.numel(), grad_y.shape[-1]
     if dtype is None:
         dtype = grad.dtype if grad is not None else grad_y.dtype
-    if dtype is not grad_y.dtype and dtype is not torch.float32:
+    if dtype is not grad_y.dtype and dtype is not _torch.float32:
         raise TypeError("the gradient must be %s or float32, not %s" % (grad_y.dtype, dtype))
     ld_grad = cols
     if grad is not None:
@@ -459,9 +462,10 @@ def embedding_grad(grad_y, ids, num_ids: int, scale: float = 1.0, first_id: int 
         ld_grad = _rows_out("grad", grad, num_ids, cols, grad)[1]
     elif accumulate:
         raise ValueError("accumulate needs the gradient to add to")
-    _on_device(grad_y)
+    if not grad_y.is_cuda:
+        raise _host_tensor(grad_y)
     if grad is None:
-        grad = torch.empty(num_ids if num_ids > 0 else 0, cols, dtype=dtype, device=grad_y.device)
+        grad = _torch.empty(num_ids if num_ids > 0 else 0, cols, dtype=dtype, device=grad_y.device)
     g2, ld = _rows_in(grad_y if grad_y.dim() == 2 else grad_y.reshape(n, cols), n, cols)
     ids = ids.contiguous()
     grad_code = _types[1][dtype]
