@@ -370,10 +370,12 @@ __device__ __forceinline__ float lanes_sum(float v, int tx_log2)
     }
 }
 
-// A row tile serves whole tokens, slot by slot (or, where tokens are `few`, every slot by a workgroup of its own): a
-// slot's row is read, its inner product with the token's grad_y formed, and its
-// gradient stored; grad_y comes from cache after the first slot.  rows and grad_rows
-// may be the same memory: a thread reads each element before it stores there.  Bound
+// A row tile serves whole tokens, slot by slot (or, where tokens are `few`, every slot
+// by a workgroup of its own): a slot's row is read, its inner product with the token's
+// grad_y formed, and its gradient stored; grad_y comes from cache after the first
+// slot.  rows and grad_rows may be the same memory: a thread reads each element before
+// it stores there (a row's last vector also loads elements of the one before it, which
+// may be stored meanwhile, and shifts them out).  Bound
 // by HBM: 16,384 tokens x 8 x 4096 bf16 in 443 us, 2.28 GB at 5.15 TB/s; a copy reaches
 // 5.9, and the same rows in sequence 395 to 413.  Slots two or eight at a time took
 // 447 and 469, a wave per token (no barrier) 478, a workgroup per slot 468.
@@ -462,10 +464,9 @@ __global__ __launch_bounds__(kThreads) void embedding_kernel(const T *__restrict
 // here for 1.6 GB (5.3 TB/s), after 26 us of ordering and before 12 of joining.  Sums
 // and empty rows in separate phases of one launch: mixed evenly they took 25 us more.
 //
-// The sorted ids are cut into pieces of `piece` slots, one
-// piece of a column tile per unit of work, whatever the ids: a run of equal ids may
-// be one slot or all of them, and no unit sums more than two pieces' slots.  A run is
-// summed in registers and stored at once by the piece in which it begins, also where
+// The sorted ids are cut into pieces of `piece` slots, one piece of a column tile per
+// unit of work, whatever the ids: a run of equal ids may be one slot or all of them,
+// and no unit sums more than two pieces' slots.  A run is summed in registers and stored at once by the piece in which it begins, also where
 // it goes on into the next one (which passes over it).  Only a run that goes on
 // beyond that is left as float32 partial sums, one for each piece that it touches:
 // slot 1 of the piece in which it begins, slot 0 of those after it.  The piece in
