@@ -165,7 +165,7 @@ lrs_status guarded(F &&f)
 
 // Few ids are ordered by counting passes of this file's own: a grouping of up to 2048
 // groups and a million ids in one (262,144 ids of 256 groups in 13.8 us; by the sort
-// 31.4), an embedding's ids in passes of up to nine bits.  The others take the
+// 31.4), an embedding's ids in passes of up to eleven bits.  The others take the
 // library's sort.
 constexpr int kFewBins = 513, kManyBins = 2049;
 constexpr int64_t kDirectGroups = kManyBins - 1, kDirectSlots = 1 << 20;
@@ -229,7 +229,18 @@ struct GroupLayout {
 };
 
 constexpr int64_t kDirectIds = 1 << 17, kOrderSlots = 4 * kPlaceThreads;  // (one block has all passes up to here)
-constexpr int kDigitBits = 9;
+int passes_of(int bits, int digit) { return (std::max(bits, 1) + digit - 1) / digit; }
+
+// Bits of a pass's digit.  Digits of eleven bits save a launch or two in some orders,
+// and the more slots, the more their counts cost: 12,000 keys of 11 bits added up in
+// 31.6 us with one pass, 38.4 with two; of 19 bits 36 with two, 43.5 with three; 32,768
+// of 10 bits 28.5 and 31.3, but of 22 bits (digits of eleven) 56 and 50.5; 65,536 keys
+// of 10 bits 33.5 and 32.  (Up to kOrderSlots the passes share a launch.)
+int digit_bits(int64_t n, int bits)
+{
+    const int most = n <= kOrderSlots ? 9 : n <= 16 * kPlaceThreads ? 11 : n <= 32 * kPlaceThreads ? 10 : 9;
+    return passes_of(bits, passes_of(bits, most));
+}
 
 lrs_status group_layout(int64_t n, int64_t groups, GroupLayout *L)
 {
@@ -243,7 +254,8 @@ lrs_status group_layout(int64_t n, int64_t groups, GroupLayout *L)
     L->off_sort = off;
     lrs_status st = LRS_OK;
     if (n <= kDirectIds) {
-        L->sort_bytes = (size_t)place_blocks(n, kFewBins) * ((size_t)1 << kDigitBits) * 4;
+        const int64_t bins = (int64_t)1 << digit_bits(n, L->bits);
+        L->sort_bytes = (size_t)place_blocks(n, bins) * (size_t)bins * 4;
     } else {
         // the size depends on n and the bit range alone: any distinct pointers will do
         const uintptr_t some = (uintptr_t)1 << 40;
@@ -267,8 +279,7 @@ lrs_status sort_ids(const GroupLayout &L, char *temp, const void *ids, int64_t n
     if (n == 0) return LRS_OK;
     const IdSource<ID> src{(const ID *)ids, first, (uint32_t)groups};
     if (n <= kDirectIds) {
-        const int passes = (std::max(L.bits, 1) + kDigitBits - 1) / kDigitBits;
-        const int width = (std::max(L.bits, 1) + passes - 1) / passes;
+        const int width = digit_bits(n, L.bits), passes = passes_of(L.bits, width);
         if (n <= kOrderSlots) {
             if (n <= kPlaceThreads)
                 order_kernel<ID, kFewBins, 1><<<1, kPlaceThreads, 0, stream>>>(src, (int)n, L.bits, width, out, ord, clear);

@@ -521,6 +521,28 @@ def test_embedding_grad_lengths(n):
             assert np.array_equal(got.cpu().numpy().astype(np.int64), want), kind
 
 
+@pytest.mark.parametrize("vocab", [511, 512, 1023, 1024, 2047, 2048, 2**18 - 1, 2**18, 2**20, 2**22 - 1, 2**22])
+def test_embedding_grad_digits(vocab):
+    """Whole numbers again: keys of every number of digits, of each width, on both
+    sides of the lengths at which the digits become narrower."""
+    torch = torch_()
+    rng = np.random.default_rng(vocab)
+    for n in (4097, 12289, 16384, 16385, 32768, 32769):
+        announce("embedding grad of %d ids, vocab %d" % (n, vocab))
+        for kind in ("spread", "one digit", "last"):
+            ids = rng.integers(-1, vocab + 1, n)
+            if kind == "one digit":
+                ids = ids & ~0x3FF
+            if kind == "last":
+                ids = vocab - rng.integers(0, 3, n)
+            gy = rng.integers(-8, 9, (n, 3))
+            inside = (ids >= 0) & (ids < vocab)
+            want = np.zeros((vocab, 3), dtype=np.int64)
+            np.add.at(want, ids[inside], gy[inside])
+            got = lrs.embedding_grad(torch.from_numpy(gy).float().cuda(), torch.from_numpy(ids).cuda(), vocab)
+            assert np.array_equal(got.cpu().numpy().astype(np.int64), want), kind
+
+
 # -------------------------------------------------------------------- together
 
 
