@@ -257,10 +257,19 @@ def key_suffix(dtype) -> str:
                         "float64, not %s" % dtype) from None
 
 
+def _check_temp(temp):
+    """Temp storage must be one block: a call writes the bytes that follow its first
+    element, which of a strided tensor are not all its own."""
+    if not temp.is_contiguous():
+        raise ValueError("temp must be contiguous")
+
+
 def _temp_tensor(nbytes, device, temp):
     import torch
-    if temp is not None and temp.numel() * temp.element_size() >= nbytes:
-        return temp
+    if temp is not None:
+        _check_temp(temp)
+        if temp.numel() * temp.element_size() >= nbytes:
+            return temp
     return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
 
 
@@ -308,7 +317,8 @@ def sort_keys(keys, begin_bit: int = 0, end_bit: int | None = None, out=None, te
     order code, in passes of `digit_bits` (8 or 11) bits; returns the output
     tensor.  A tensor of any shape is sorted as the flat array of its elements;
     `out`, when given, must be contiguous with as many elements, of the same
-    dtype, on the same device (ValueError otherwise, before any work)."""
+    dtype, on the same device (ValueError otherwise, before any work).  `temp`,
+    when given, must be contiguous (ValueError); one that is too small is not used."""
     import torch
     sfx = key_suffix(keys.dtype)
     end_bit = KEY_BITS[sfx] if end_bit is None else end_bit
@@ -340,7 +350,7 @@ def sort_pairs(keys, values, begin_bit: int = 0, end_bit: int | None = None, key
     or 11) bits; returns (keys_out, values_out).  `values` must hold as many
     elements as `keys`, and the outputs, when given, must be contiguous with
     that many elements of the inputs' dtypes on the same device (ValueError
-    otherwise, before any work)."""
+    otherwise, before any work); `temp` as for sort_keys."""
     import torch
     sfx = key_suffix(keys.dtype)
     if str(values.dtype) != "torch.uint32":

@@ -10,7 +10,8 @@ with ValueError or TypeError before any work.  Gradients are calls of their own,
 in the C interface; nothing is recorded for torch's autograd.
 
 Matrices may have any row stride; their elements must be contiguous within a row
-(inputs that are not are copied first, outputs are refused).  ``stream`` is as for
+(inputs that are not are copied first, outputs are refused).  ``temp``, where a call
+takes it, must be contiguous; one that is too small is not used.  ``stream`` is as for
 ``sort_keys``: None is the current stream of the tensors' device; on any other
 stream the work also waits for what the current one already holds, so that inputs
 just written there can be passed.
@@ -19,7 +20,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _check, _ptr, _stream, load_library
+from . import _check, _check_temp, _ptr, _stream, load_library
 
 ID_TYPE_CODES = {"i32": 0, "i64": 1}
 ROW_TYPE_CODES = {"f32": 0, "bf16": 1, "f16": 2}
@@ -296,6 +297,7 @@ def _temp(name, sizes, args, like, temp):
             _needs.clear()
         need = _needs[key] = tb.value
     if temp is not None:
+        _check_temp(temp)
         if temp.get_device() != like.get_device():
             raise _elsewhere("temp", temp, like)
         size = temp.numel() * temp.element_size()
