@@ -273,6 +273,13 @@ def _temp_tensor(nbytes, device, temp):
     return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
 
 
+def _stream_of(handle: int, device=None):
+    """torch's stream of a raw handle.  0 is the device's default stream: of it
+    ExternalStream would make a new stream, that nothing then waits for."""
+    import torch
+    return torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+
+
 def _side_stream(stream):
     """The torch stream a call is enqueued on when that is not torch's current
     stream (None otherwise): tensors the conveniences allocate, or copy into
@@ -286,7 +293,7 @@ def _side_stream(stream):
     handle = stream if isinstance(stream, int) else stream.cuda_stream
     if handle == cur.cuda_stream:
         return None
-    return stream if not isinstance(stream, int) else torch.cuda.ExternalStream(handle)
+    return stream if not isinstance(stream, int) else _stream_of(handle)
 
 
 def _keep_for(side, *tensors):

@@ -20,7 +20,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _check, _check_temp, _ptr, _stream, load_library
+from . import _check, _check_temp, _ptr, _stream, _stream_of, load_library
 
 ID_TYPE_CODES = {"i32": 0, "i64": 1}
 ROW_TYPE_CODES = {"f32": 0, "bf16": 1, "f16": 2}
@@ -272,7 +272,7 @@ def _run(name, stream, tensors, args) -> None:
     handle = current.cuda_stream if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
     side = None
     if handle != current.cuda_stream:
-        side = torch.cuda.ExternalStream(handle, index) if isinstance(stream, int) else stream
+        side = _stream_of(handle, index) if isinstance(stream, int) else stream
         if side.device.index != index:
             raise ValueError("stream is on %s, the tensors on %s" % (side.device, tensors[0].device))
         side.wait_stream(current)

@@ -1,0 +1,44 @@
+"""Calls on the default stream by its handle, with another stream current."""
+from __future__ import annotations
+
+import pytest
+
+import sorting_lsd_radix_sort_amd as lrs
+from gpu_util import announce
+
+pytestmark = pytest.mark.gpu
+
+
+def test_default_stream_by_handle_waits_for_the_current_one():
+    """Inputs written on a side stream behind long work there, the calls on handle 0:
+    their results are those of the finished inputs."""
+    import torch
+    announce("default stream by handle")
+    g = torch.Generator("cuda").manual_seed(1)
+    ids = torch.randint(0, 12, (4000, 2), generator=g, device="cuda")
+    x = torch.randn(4000, 520, generator=g, device="cuda")
+    w = torch.rand(4000, 2, generator=g, device="cuda")
+    want = lrs.group_tokens(ids, 12)
+    want_rows = lrs.dispatch_rows(x, want[1])
+    want_y = lrs.combine_rows(want_rows, want[1], w)
+    want_grad = lrs.embedding_grad(x, ids[:, 0], 12)
+    torch.cuda.synchronize()
+    side, default = torch.cuda.Stream(), torch.cuda.default_stream()
+    big = torch.ones(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for rep in range(3):
+        with torch.cuda.stream(side):
+            late_ids, late_x = torch.zeros_like(ids), torch.zeros_like(x)
+            for _ in range(4):
+                big @ big
+            late_ids.copy_(ids)
+            late_x.copy_(x)
+            got = lrs.group_tokens(late_ids, 12, stream=0)
+            side.wait_stream(default)
+            rows = lrs.dispatch_rows(late_x, got[1], stream=0)
+            side.wait_stream(default)
+            y = lrs.combine_rows(rows, got[1], w, stream=0)
+            grad = lrs.embedding_grad(late_x, late_ids[:, 0], 12, stream=0)
+        default.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), rep
+        assert torch.equal(rows, want_rows) and torch.equal(y, want_y) and torch.equal(grad, want_grad), rep

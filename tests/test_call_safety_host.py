@@ -41,3 +41,72 @@ def test_temp_that_is_not_one_block_is_refused(kind):
     whole = torch.zeros(1 << 20, dtype=torch.uint8)
     assert lrs._temp_tensor(need, whole.device, whole) is whole
     assert rows._temp("lrs_group_tokens", (1, 20000, 8), args, like, whole)[0] is whole
+
+
+# ---------------------------------------------------------------------- streams
+
+
+class FakeStream:
+    def __init__(self, handle, index=0):
+        self.cuda_stream = handle
+        self.device = torch.device("cuda", index)
+        self.waited = []
+
+    def wait_stream(self, other):
+        self.waited.append(other)
+
+
+class FakeTensor:
+    device = torch.device("cuda", 0)
+
+    def __init__(self):
+        self.recorded = []
+
+    def get_device(self):
+        return 0
+
+    def record_stream(self, stream):
+        self.recorded.append(stream)
+
+
+@pytest.fixture
+def fake_streams(monkeypatch):
+    """torch's streams replaced by objects that note what is asked of them: the current
+    one has the handle 5, and the default stream's handle is 0, as on a GPU.  torch's
+    ExternalStream takes the handle 0 for "a new stream"."""
+    import contextlib
+    import types
+
+    current, default, made = FakeStream(5), FakeStream(0), []
+
+    def external(handle, device=None):
+        made.append(FakeStream(handle if handle else 999))
+        return made[-1]
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: default)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", lambda index: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "ExternalStream", external)
+    rows._type_codes()
+    calls = []
+    monkeypatch.setitem(rows._functions, "a_call", lambda *args: calls.append(args) or 0)
+    return types.SimpleNamespace(current=current, default=default, made=made, calls=calls)
+
+
+def test_handle_zero_is_the_default_stream(fake_streams):
+    """With another stream current, work on handle 0 waits for the current stream, and
+    the tensors are recorded on the default one."""
+    f, t = fake_streams, FakeTensor()
+    rows._run("a_call", 0, (t,), (7,))
+    assert f.calls == [(7, None)]
+    assert f.default.waited == [f.current] and t.recorded == [f.default] and not f.made
+    assert lrs._side_stream(0) is f.default and not f.made
+    # any other handle is that stream, the current one's needs nothing
+    rows._run("a_call", 12, (t,), ())
+    assert f.calls[-1] == (12,) and f.made[-1].cuda_stream == 12 and f.made[-1].waited == [f.current]
+    assert t.recorded[-1] is f.made[-1]
+    assert lrs._side_stream(12).cuda_stream == 12
+    rows._run("a_call", 5, (t,), ())
+    assert f.calls[-1] == (5,) and len(t.recorded) == 2
+    assert lrs._side_stream(5) is None
