@@ -285,7 +285,8 @@ def _side_stream(stream):
     stream (None otherwise): tensors the conveniences allocate, or copy into
     contiguous form, on the current stream are then recorded on it, so that
     the caching allocator does not hand their memory to other work while the
-    sort still uses it."""
+    sort still uses it.  The side stream waits for what the current one holds:
+    the copies, and earlier work on the memory allocated."""
     import torch
     if stream is None:
         return None
@@ -293,7 +294,9 @@ def _side_stream(stream):
     handle = stream if isinstance(stream, int) else stream.cuda_stream
     if handle == cur.cuda_stream:
         return None
-    return stream if not isinstance(stream, int) else _stream_of(handle)
+    side = stream if not isinstance(stream, int) else _stream_of(handle)
+    side.wait_stream(cur)
+    return side
 
 
 def _keep_for(side, *tensors):
@@ -325,7 +328,8 @@ def sort_keys(keys, begin_bit: int = 0, end_bit: int | None = None, out=None, te
     tensor.  A tensor of any shape is sorted as the flat array of its elements;
     `out`, when given, must be contiguous with as many elements, of the same
     dtype, on the same device (ValueError otherwise, before any work).  `temp`,
-    when given, must be contiguous (ValueError); one that is too small is not used."""
+    when given, must be contiguous (ValueError); one that is too small is not used.
+    On a `stream` other than the current one the sort waits for what that one holds."""
     import torch
     sfx = key_suffix(keys.dtype)
     end_bit = KEY_BITS[sfx] if end_bit is None else end_bit
@@ -357,7 +361,7 @@ def sort_pairs(keys, values, begin_bit: int = 0, end_bit: int | None = None, key
     or 11) bits; returns (keys_out, values_out).  `values` must hold as many
     elements as `keys`, and the outputs, when given, must be contiguous with
     that many elements of the inputs' dtypes on the same device (ValueError
-    otherwise, before any work); `temp` as for sort_keys."""
+    otherwise, before any work); `temp` and `stream` as for sort_keys."""
     import torch
     sfx = key_suffix(keys.dtype)
     if str(values.dtype) != "torch.uint32":

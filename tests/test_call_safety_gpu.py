@@ -42,3 +42,30 @@ def test_default_stream_by_handle_waits_for_the_current_one():
         default.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)), rep
         assert torch.equal(rows, want_rows) and torch.equal(y, want_y) and torch.equal(grad, want_grad), rep
+
+
+@pytest.mark.parametrize("as_int", [False, True])
+def test_sorts_of_a_copy_made_on_the_current_stream(as_int):
+    """Strided keys and values, written behind long work on the current stream and
+    copied there, are sorted on a side stream."""
+    import torch
+    announce("sort of a copy, as int %s" % as_int)
+    g = torch.Generator("cuda").manual_seed(2)
+    keys = torch.randint(0, 2**31 - 1, (300001, 2), generator=g, device="cuda", dtype=torch.int32)
+    values = torch.arange(600002, device="cuda", dtype=torch.int32).view(300001, 2)
+    want_keys, order = torch.sort(keys[:, 1], stable=True)
+    side = torch.cuda.Stream()
+    big = torch.ones(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for rep in range(3):
+        late_keys, late_values = torch.zeros_like(keys), torch.zeros_like(values)
+        for _ in range(4):
+            big @ big
+        late_keys.copy_(keys)
+        late_values.copy_(values)
+        stream = side.cuda_stream if as_int else side
+        alone = lrs.sort_keys(late_keys[:, 1], stream=stream)
+        got_keys, got_values = lrs.sort_pairs(late_keys[:, 1], late_values.view(torch.uint32)[:, 1], stream=stream)
+        side.synchronize()
+        assert torch.equal(alone, want_keys) and torch.equal(got_keys, want_keys), rep
+        assert torch.equal(got_values.view(torch.int32), values[:, 1][order]), rep

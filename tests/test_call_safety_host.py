@@ -110,3 +110,13 @@ def test_handle_zero_is_the_default_stream(fake_streams):
     rows._run("a_call", 5, (t,), ())
     assert f.calls[-1] == (5,) and len(t.recorded) == 2
     assert lrs._side_stream(5) is None
+
+
+def test_sorts_on_a_side_stream_wait_for_the_current_one(fake_streams):
+    """Copies made and memory handed out on the current stream are ready there, and
+    free of earlier work, only behind what it holds."""
+    f, side = fake_streams, FakeStream(12)
+    assert lrs._side_stream(side) is side and side.waited == [f.current]
+    assert lrs._side_stream(13).waited == [f.current]
+    assert lrs._side_stream(f.current) is None and not f.current.waited
+    assert lrs._side_stream(None) is None
