@@ -268,13 +268,13 @@ def _run(name, stream, tensors, args) -> None:
             _check(status, name)
         return
     torch = _torch
+    if stream is not None and not isinstance(stream, int) and stream.device.index != index:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, tensors[0].device))
     current = torch.cuda.current_stream(index)
     handle = current.cuda_stream if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
     side = None
     if handle != current.cuda_stream:
         side = _stream_of(handle, index) if isinstance(stream, int) else stream
-        if side.device.index != index:
-            raise ValueError("stream is on %s, the tensors on %s" % (side.device, tensors[0].device))
         side.wait_stream(current)
     with torch.cuda.device(index):
         _check(fn(*args, handle or None), name)

@@ -120,3 +120,16 @@ def test_sorts_on_a_side_stream_wait_for_the_current_one(fake_streams):
     assert lrs._side_stream(13).waited == [f.current]
     assert lrs._side_stream(f.current) is None and not f.current.waited
     assert lrs._side_stream(None) is None
+
+
+def test_default_stream_of_another_device_is_refused(fake_streams):
+    """Every device's default stream has the handle 0: the device tells them apart."""
+    f, t = fake_streams, FakeTensor()
+    f.current.cuda_stream = 0
+    rows._run("a_call", FakeStream(0, 0), (t,), ())
+    assert f.calls == [(None,)]
+    for other in (FakeStream(0, 1), FakeStream(12, 1)):
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            rows._run("a_call", other, (t,), ())
+        assert not other.waited
+    assert len(f.calls) == 1 and not t.recorded
