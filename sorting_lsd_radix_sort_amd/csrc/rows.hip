@@ -61,18 +61,21 @@ bool shape_ok(int64_t rows, int64_t cols, int64_t ld)
 // The array is there and aligned, or empty.
 bool array_ok(const Span &s, int64_t bytes) { return s.empty() || (s.at != 0 && s.at % bytes == 0); }
 
-// Whether two arrays share memory.  Rows that are interleaved with equal strides
-// (columns of one buffer) share none if their columns are apart.
+// Whether two arrays share memory: exact where their rows are equally far apart or one
+// has a single row (columns of one buffer share none); matrices of other strides do if
+// their extents meet.  Row i of a and row j of b meet if the distance between them, d +
+// (j - i) * step, is above -b.row and below a.row: the first j - i above decides.
 bool overlap(const Span &a, const Span &b)
 {
     if (a.empty() || b.empty() || a.at == 0 || b.at == 0) return false;
-    if ((__int128)a.at + a.extent() <= (__int128)b.at || (__int128)b.at + b.extent() <= (__int128)a.at) return false;
-    if (a.rows > 1 && b.rows > 1 && a.step == b.step) {
-        const uintptr_t step = (uintptr_t)a.step;
-        const uintptr_t gap = a.at <= b.at ? (b.at - a.at) % step : (step - (a.at - b.at) % step) % step;
-        return gap < (uintptr_t)a.row || gap + (uintptr_t)b.row > step;
-    }
-    return true;
+    const __int128 d = (__int128)b.at - (__int128)a.at;
+    if (d >= a.extent() || -d >= b.extent()) return false;
+    if (a.rows > 1 && b.rows > 1 && a.step != b.step) return true;
+    const __int128 step = a.rows > 1 ? a.step : b.step;
+    const __int128 above = -b.row - d;  // (j - i) * step has to be more
+    __int128 by = above >= 0 ? above / step + 1 : -((-above - 1) / step);
+    by = std::max<__int128>(by, 1 - a.rows);
+    return by < b.rows && d + by * step < a.row;
 }
 
 // ------------------------------------------------------------------ launches

@@ -69,3 +69,22 @@ def test_sorts_of_a_copy_made_on_the_current_stream(as_int):
         side.synchronize()
         assert torch.equal(alone, want_keys) and torch.equal(got_keys, want_keys), rep
         assert torch.equal(got_values.view(torch.int32), values[:, 1][order]), rep
+
+
+def test_one_row_beside_the_rows_of_its_buffer():
+    """A single token's row in the columns beside those its copies go to, and the sum
+    of them back to another row's."""
+    import torch
+    announce("one row beside others")
+    wide = torch.arange(8 * 400, device="cuda", dtype=torch.float32).view(8, 400) % 97
+    before = wide.clone()
+    position = torch.tensor([[6, 0, 7]], dtype=torch.int32, device="cuda")
+    for row in (0, 3, 7):
+        wide.copy_(before)
+        lrs.dispatch_rows(wide[row:row + 1, 200:], position, out=wide[:, :200])
+        want = before.clone()
+        want[[6, 0, 7], :200] = before[row, 200:]
+        assert torch.equal(wide, want), row
+        lrs.combine_rows(wide[:, :200], position, out=wide[row:row + 1, 200:])
+        want[row, 200:] *= 3
+        assert torch.equal(wide, want), row
