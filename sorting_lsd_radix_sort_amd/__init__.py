@@ -307,6 +307,15 @@ def _keep_for(side, *tensors):
             t.record_stream(side)
 
 
+def _written(*tensors):
+    """Counts a write to each tensor that a caller gave as output, so that autograd
+    notices where one had been saved for a gradient."""
+    import torch
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 def _check_out(name, t, n, dtype, device):
     """An output tensor must be contiguous with n elements of `dtype` on the
     input's device (checked before anything is enqueued)."""
@@ -336,6 +345,7 @@ def sort_keys(keys, begin_bit: int = 0, end_bit: int | None = None, out=None, te
     src = keys
     keys = keys.contiguous()
     n = keys.numel()
+    given = out
     if out is None:
         out = torch.empty_like(keys)
     else:
@@ -352,6 +362,7 @@ def sort_keys(keys, begin_bit: int = 0, end_bit: int | None = None, out=None, te
         t = _temp_tensor(need, keys.device, temp)
         fn(t, t.numel() * t.element_size(), keys, out, n, begin_bit, end_bit, stream)
     _keep_for(side, t, out, keys if keys is not src else None)
+    _written(given)
     return out
 
 
@@ -375,6 +386,7 @@ def sort_pairs(keys, values, begin_bit: int = 0, end_bit: int | None = None, key
     keys = keys.contiguous()
     values = values.contiguous()
     n = keys.numel()
+    given = keys_out, values_out
     if keys_out is None:
         keys_out = torch.empty_like(keys)
     else:
@@ -397,6 +409,7 @@ def sort_pairs(keys, values, begin_bit: int = 0, end_bit: int | None = None, key
         fn(t, t.numel() * t.element_size(), keys, values, keys_out, values_out, n, begin_bit, end_bit, stream)
     _keep_for(side, t, keys_out, values_out, keys if keys is not ksrc else None,
               values if values is not vsrc else None)
+    _written(*given)
     return keys_out, values_out
 
 

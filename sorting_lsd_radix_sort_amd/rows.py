@@ -7,7 +7,9 @@ bindings do.  ``group_tokens``, ``dispatch_rows``, ``combine_rows`` and
 ``embedding_grad`` are conveniences over them on torch tensors: they allocate
 outputs and temp storage, and refuse tensors of the wrong shape, type or device
 with ValueError or TypeError before any work.  Gradients are calls of their own, as
-in the C interface; nothing is recorded for torch's autograd.
+in the C interface: nothing is recorded for torch's autograd, whatever the inputs
+require (as under ``torch.no_grad``), but a tensor given as output counts as changed
+in place, so a gradient that still needs its old values is refused by torch.
 
 Matrices may have any row stride; their elements must be contiguous within a row
 (inputs that are not are copied first, outputs are refused).  ``temp``, where a call
@@ -20,7 +22,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _check, _check_temp, _ptr, _stream, _stream_of, load_library
+from . import _check, _check_temp, _ptr, _stream, _stream_of, _written, load_library
 
 ID_TYPE_CODES = {"i32": 0, "i64": 1}
 ROW_TYPE_CODES = {"f32": 0, "bf16": 1, "f16": 2}
@@ -254,18 +256,21 @@ def _host_tensor(t):
     return ValueError("lrsort needs device tensors, got a tensor on %s" % t.device)
 
 
-def _run(name, stream, tensors, args) -> None:
+def _run(name, stream, tensors, args, written=None) -> None:
     """Calls the C function `name` with `args` and the stream's handle, with the
     device of the first of `tensors` current.  None is that device's current stream.
     On another stream the work waits for what the current one holds (inputs copied
     and outputs allocated there), and the tensors are recorded on it, so that the
-    caching allocator does not hand their memory on while it is in use there."""
+    caching allocator does not hand their memory on while it is in use there.
+    `written`: an output that the caller gave."""
     fn = _functions.get(name) or _load(name)
     index = tensors[0].get_device()
     if stream is None and _torch.cuda.current_device() == index:
         status = fn(*args, (_current_handle or _handle_lookup())(index) or None)
         if status:
             _check(status, name)
+        if written is not None:
+            _written(written)
         return
     torch = _torch
     if stream is not None and not isinstance(stream, int) and stream.device.index != index:
@@ -282,6 +287,7 @@ def _run(name, stream, tensors, args) -> None:
         for t in tensors:
             if t is not None:
                 t.record_stream(side)
+    _written(written)
 
 
 def _temp(name, sizes, args, like, temp):
@@ -346,12 +352,13 @@ def dispatch_rows(x, position, num_rows: int | None = None, out=None, stream=Non
         num_rows, ld_out = _rows_out("out", out, num_rows, cols, x)
     if not x.is_cuda:
         raise _host_tensor(x)
+    given = out
     if out is None:
         num_rows, ld_out = t * slots if num_rows is None else int(num_rows), cols
         out = x.new_empty(num_rows, cols)
     x, ld = _rows_in(x, tokens, cols)
     _run("lrs_dispatch_rows", stream, (x, pos, out),
-         (code, x.data_ptr(), ld, pos.data_ptr(), tokens, slots, cols, out.data_ptr(), ld_out, num_rows))
+         (code, x.data_ptr(), ld, pos.data_ptr(), tokens, slots, cols, out.data_ptr(), ld_out, num_rows), given)
     return out
 
 
@@ -367,11 +374,13 @@ def combine_rows(rows, position, weights=None, out=None, stream=None):
     ld_out = cols if out is None else _rows_out("out", out, tokens, cols, rows)[1]
     if not rows.is_cuda:
         raise _host_tensor(rows)
+    given = out
     if out is None:
         out = rows.new_empty(tokens, cols)
     rows, ld = _rows_in(rows, num_rows, cols)
     _run("lrs_combine_rows", stream, (rows, pos, w, out),
-         (code, rows.data_ptr(), ld, num_rows, pos.data_ptr(), wcode, _at(w), tokens, slots, cols, out.data_ptr(), ld_out))
+         (code, rows.data_ptr(), ld, num_rows, pos.data_ptr(), wcode, _at(w), tokens, slots, cols, out.data_ptr(),
+          ld_out), given)
     return out
 
 
@@ -396,6 +405,7 @@ def combine_rows_grad(grad_y, rows, position, weights, grad_rows=None, stream=No
     ld_out = cols if grad_rows is None else _rows_out("grad_rows", grad_rows, num_rows, cols, rows)[1]
     if not rows.is_cuda:
         raise _host_tensor(rows)
+    given = grad_rows
     if grad_rows is None:
         grad_rows = rows.new_zeros(num_rows, cols)
     grad_w = None if w is None else w.new_empty(tokens, slots)
@@ -403,7 +413,7 @@ def combine_rows_grad(grad_y, rows, position, weights, grad_rows=None, stream=No
     rows, ld = _rows_in(rows, num_rows, cols)
     _run("lrs_combine_rows_grad", stream, (rows, grad_y, pos, w, grad_rows, grad_w),
          (code, grad_y.data_ptr(), ld_y, rows.data_ptr(), ld, num_rows, pos.data_ptr(), wcode, _at(w), tokens, slots, cols,
-          grad_rows.data_ptr(), ld_out, _at(grad_w)))
+          grad_rows.data_ptr(), ld_out, _at(grad_w)), given)
     return grad_rows, grad_w
 
 
@@ -416,7 +426,7 @@ def embedding(table, ids, scale: float = 1.0, first_id: int = 0, out=None, strea
     if ids.get_device() != table.get_device():
         raise _elsewhere("ids", ids, table)
     n, shape = ids.numel(), (*ids.shape, cols)
-    y, ld_y = out, cols
+    given, y, ld_y = out, out, cols
     if out is not None:
         if out.shape != shape:
             raise ValueError("out has shape %s, expected %s" % (tuple(out.shape), shape))
@@ -433,7 +443,7 @@ def embedding(table, ids, scale: float = 1.0, first_id: int = 0, out=None, strea
     ids = ids.contiguous()
     _run("lrs_embedding", stream, (table, ids, y),
          (code, table.data_ptr(), ld, num_ids, id_code, ids.data_ptr(), n, _int64("first_id", first_id), float(scale),
-          cols, y.data_ptr(), ld_y))
+          cols, y.data_ptr(), ld_y), given)
     return out
 
 
@@ -466,6 +476,7 @@ def embedding_grad(grad_y, ids, num_ids: int, scale: float = 1.0, first_id: int 
         raise ValueError("accumulate needs the gradient to add to")
     if not grad_y.is_cuda:
         raise _host_tensor(grad_y)
+    given = grad
     if grad is None:
         grad = _torch.empty(num_ids if num_ids > 0 else 0, cols, dtype=dtype, device=grad_y.device)
     g2, ld = _rows_in(grad_y if grad_y.dim() == 2 else grad_y.reshape(n, cols), n, cols)
@@ -474,5 +485,6 @@ def embedding_grad(grad_y, ids, num_ids: int, scale: float = 1.0, first_id: int 
     args = (code, g2.data_ptr(), ld, id_code, ids.data_ptr(), n, _int64("first_id", first_id), float(scale), grad_code,
             grad.data_ptr(), ld_grad, num_ids, cols, 1 if accumulate else 0)
     t, size = _temp("lrs_embedding_grad", (code, id_code, n, grad_code, num_ids, cols), args, grad, temp)
-    _run("lrs_embedding_grad", stream, (g2, ids, t, grad), (t.data_ptr(), ctypes.byref(ctypes.c_size_t(size))) + args)
+    _run("lrs_embedding_grad", stream, (g2, ids, t, grad), (t.data_ptr(), ctypes.byref(ctypes.c_size_t(size))) + args,
+         given)
     return grad

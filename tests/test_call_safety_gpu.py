@@ -88,3 +88,40 @@ def test_one_row_beside_the_rows_of_its_buffer():
         lrs.combine_rows(wide[:, :200], position, out=wide[row:row + 1, 200:])
         want[row, 200:] *= 3
         assert torch.equal(wide, want), row
+
+
+def test_autograd_notices_what_the_calls_write():
+    """Every tensor given to be written, here one that another gradient still needs, has
+    a new version afterwards; what is only read keeps its own."""
+    import torch
+    announce("versions of written tensors")
+    ids = torch.arange(6, device="cuda").view(3, 2) % 2
+    x, w = torch.ones(3, 8, device="cuda"), torch.ones(3, 2, device="cuda")
+    _, position, _ = lrs.group_tokens(ids, 2)
+    rows, table = torch.ones(6, 8, device="cuda"), torch.ones(2, 8, device="cuda")
+    keys, values = torch.arange(8, device="cuda", dtype=torch.int32), torch.arange(8, device="cuda").to(torch.uint32)
+    read = [ids, x, w, position, rows, table, keys, values]
+    versions = [t._version for t in read]
+    calls = [((6, 8), lambda out: lrs.dispatch_rows(x, position, out=out)),
+             ((3, 8), lambda out: lrs.combine_rows(rows, position, w, out=out)),
+             ((6, 8), lambda out: lrs.combine_rows_grad(x, rows, position, w, grad_rows=out)),
+             ((6, 8), lambda out: lrs.combine_rows_grad(x, out, position, w, grad_rows=out)),
+             ((3, 8), lambda out: lrs.embedding(table, ids[:, 0], out=out)),
+             ((3, 2, 8), lambda out: lrs.embedding(table, ids, out=out)),
+             ((2, 8), lambda out: lrs.embedding_grad(x, ids[:, 0], 2, grad=out)),
+             ((2, 8), lambda out: lrs.embedding_grad(x, ids[:, 0], 2, grad=out, accumulate=True)),
+             ((8,), lambda out: lrs.sort_keys(torch.ones(8, device="cuda"), out=out)),
+             ((8,), lambda out: lrs.sort_keys(torch.ones(8, device="cuda"), out=out, digit_bits=11)),
+             ((8,), lambda out: lrs.sort_pairs(torch.ones(8, device="cuda"), values, keys_out=out))]
+    for i, (shape, call) in enumerate(calls):
+        leaf = torch.ones(shape, device="cuda", requires_grad=True)
+        out = torch.full(shape, 2.0, device="cuda")
+        y = (leaf * out).sum()
+        call(out)
+        assert out._version == 1, i
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    values_out = torch.empty_like(values)
+    lrs.sort_pairs(keys, values, values_out=values_out)
+    assert values_out._version == 1
+    assert [t._version for t in read] == versions

@@ -89,6 +89,7 @@ def fake_streams(monkeypatch):
     monkeypatch.setattr(torch.cuda, "device", lambda index: contextlib.nullcontext())
     monkeypatch.setattr(torch.cuda, "ExternalStream", external)
     rows._type_codes()
+    monkeypatch.setattr(rows, "_current_handle", lambda index: current.cuda_stream)
     calls = []
     monkeypatch.setitem(rows._functions, "a_call", lambda *args: calls.append(args) or 0)
     return types.SimpleNamespace(current=current, default=default, made=made, calls=calls)
@@ -133,3 +134,25 @@ def test_default_stream_of_another_device_is_refused(fake_streams):
             rows._run("a_call", other, (t,), ())
         assert not other.waited
     assert len(f.calls) == 1 and not t.recorded
+
+
+# -------------------------------------------------------------- torch's bookkeeping
+
+
+def test_a_written_tensor_counts_as_changed(fake_streams):
+    """A tensor that a call was given to write has a new version afterwards, so that
+    autograd notices if it had been saved for a gradient; also on a side stream."""
+    f, t = fake_streams, FakeTensor()
+    saved = torch.ones(3, requires_grad=True)
+    for stream in (None, 12):
+        kept = torch.full((3,), 2.0)
+        y = (saved * kept).sum()
+        rows._run("a_call", stream, (t,), (), kept)
+        assert kept._version == 1
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    kept = torch.zeros(3)
+    lrs._written(kept, None)
+    assert kept._version == 1
+    with torch.inference_mode():
+        lrs._written(torch.zeros(3))  # has no version: nothing to count
