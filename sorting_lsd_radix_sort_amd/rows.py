@@ -52,6 +52,15 @@ def _code(codes, t) -> int:
     return codes[t] if isinstance(t, str) else int(t)
 
 
+def _int64(name, v) -> int:
+    if v == 0:
+        return 0
+    v = int(v)
+    if not -2**63 <= v < 2**63:
+        raise ValueError("%s %d is no int64" % (name, v))
+    return v
+
+
 # ------------------------------------------------------------------ C calls
 
 
@@ -63,8 +72,8 @@ def lrs_group_tokens(d_temp, temp_bytes, id_type, d_ids, n, first_id, num_groups
     temp = _ptr(d_temp)
     st = None if temp is None else _stream(stream)
     _check(load_library().lrs_group_tokens(temp, ctypes.byref(tb), _code(ID_TYPE_CODES, id_type), _ptr(d_ids), int(n),
-                                           int(first_id), int(num_groups), _ptr(d_order), _ptr(d_position),
-                                           _ptr(d_offsets), st), "lrs_group_tokens")
+                                           _int64("first_id", first_id), int(num_groups), _ptr(d_order),
+                                           _ptr(d_position), _ptr(d_offsets), st), "lrs_group_tokens")
     return tb.value
 
 
@@ -100,8 +109,8 @@ def lrs_embedding(row_type, d_table, ld_table, num_ids, id_type, d_ids, n, first
                   stream=None) -> None:
     """Calls the C function of the same name."""
     _check(load_library().lrs_embedding(_code(ROW_TYPE_CODES, row_type), _ptr(d_table), int(ld_table), int(num_ids),
-                                        _code(ID_TYPE_CODES, id_type), _ptr(d_ids), int(n), int(first_id), float(scale),
-                                        int(cols), _ptr(d_y), int(ld_y), _stream(stream)), "lrs_embedding")
+                                        _code(ID_TYPE_CODES, id_type), _ptr(d_ids), int(n),
+                                        _int64("first_id", first_id), float(scale), int(cols), _ptr(d_y), int(ld_y), _stream(stream)), "lrs_embedding")
 
 
 def lrs_embedding_grad(d_temp, temp_bytes, row_type, d_grad_y, ld_grad_y, id_type, d_ids, n, first_id, scale, grad_type,
@@ -113,8 +122,9 @@ def lrs_embedding_grad(d_temp, temp_bytes, row_type, d_grad_y, ld_grad_y, id_typ
     st = None if temp is None else _stream(stream)
     _check(load_library().lrs_embedding_grad(temp, ctypes.byref(tb), _code(ROW_TYPE_CODES, row_type), _ptr(d_grad_y),
                                              int(ld_grad_y), _code(ID_TYPE_CODES, id_type), _ptr(d_ids), int(n),
-                                             int(first_id), float(scale), _code(ROW_TYPE_CODES, grad_type), _ptr(d_grad),
-                                             int(ld_grad), int(num_ids), int(cols), int(bool(accumulate)), st),
+                                             _int64("first_id", first_id), float(scale),
+                                             _code(ROW_TYPE_CODES, grad_type), _ptr(d_grad), int(ld_grad), int(num_ids),
+                                             int(cols), int(bool(accumulate)), st),
            "lrs_embedding_grad")
     return tb.value
 
@@ -221,15 +231,6 @@ def _weights(weights, position):
     if weights.get_device() != position.get_device():
         raise _elsewhere("weights", weights, position)
     return weights.contiguous(), _row_code("weights", weights.dtype)
-
-
-def _int64(name, v) -> int:
-    if v == 0:
-        return 0
-    v = int(v)
-    if not -2**63 <= v < 2**63:
-        raise ValueError("%s %d is no int64" % (name, v))
-    return v
 
 
 def _at(t):

@@ -156,3 +156,17 @@ def test_a_written_tensor_counts_as_changed(fake_streams):
     assert kept._version == 1
     with torch.inference_mode():
         lrs._written(torch.zeros(3))  # has no version: nothing to count
+
+
+# ------------------------------------------------------------------ wide numbers
+
+
+@pytest.mark.parametrize("first", [2**63, -2**63 - 1, 2**64, 2**64 + 3])
+def test_first_id_that_is_no_int64_is_refused_by_the_c_calls(first):
+    """ctypes would keep its low 64 bits: 2**64 + 3 would be taken for 3."""
+    with pytest.raises(ValueError, match="int64"):
+        lrs.lrs_group_tokens(None, 0, "i64", A, 100, first, 8, B, C, D, 0)
+    with pytest.raises(ValueError, match="int64"):
+        lrs.lrs_embedding("bf16", A, 64, 10, "i64", B, 0, first, 1.0, 64, C, 64, 0)
+    with pytest.raises(ValueError, match="int64"):
+        lrs.lrs_embedding_grad(None, 0, "bf16", A, 64, "i64", B, 100, first, 1.0, "bf16", C, 64, 10, 64, 0, 0)
