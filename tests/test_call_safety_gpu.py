@@ -125,3 +125,47 @@ def test_autograd_notices_what_the_calls_write():
     lrs.sort_pairs(keys, values, values_out=values_out)
     assert values_out._version == 1
     assert [t._version for t in read] == versions
+
+
+def test_captured_conveniences_replay():
+    """The conveniences captured as a program calls them, temp storage and outputs from
+    the graph's own memory: replays on new inputs, with eager calls between them, give
+    the eager results; two graphs of other sizes do not disturb each other."""
+    import torch
+    announce("captured conveniences")
+
+    def step(s):
+        order, position, offsets = lrs.group_tokens(s["ids"], 20, first_id=2)
+        rows = lrs.dispatch_rows(s["x"], position, out=s["rows"])
+        y = lrs.combine_rows(rows, position, s["w"])
+        grad_rows, grad_w = lrs.combine_rows_grad(y, rows, position, s["w"])
+        e = lrs.embedding(s["x"], s["ids"][:, 0], scale=0.5)
+        grad = lrs.embedding_grad(e, s["ids"][:, 0], 24, scale=0.5, dtype=torch.float32)
+        keys = lrs.sort_keys(s["ids"].view(-1))
+        return order, position, offsets, rows, y, grad_rows, grad_w, e, grad, keys
+
+    def fresh(tokens, cols, seed):
+        g = torch.Generator("cuda").manual_seed(seed)
+        return {"ids": torch.randint(0, 24, (tokens, 3), generator=g, device="cuda"),
+                "x": torch.randn(tokens, cols, generator=g, device="cuda", dtype=torch.bfloat16),
+                "w": torch.rand(tokens, 3, generator=g, device="cuda"),
+                "rows": torch.zeros(tokens * 3, cols, device="cuda", dtype=torch.bfloat16)}
+
+    sizes = ((700, 264), (9000, 72))
+    states, graphs, outs = [fresh(*size, 1) for size in sizes], [], []
+    for s in states:
+        step(s)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(step(s))
+    for rep in range(3):
+        new = [fresh(*size, 10 + rep) for size in sizes]
+        for s, other, graph in zip(states, new, graphs):
+            for name in s:
+                s[name].copy_(other[name])
+            graph.replay()
+        want = [step(other) for other in new]
+        torch.cuda.synchronize()
+        for got, expected in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(got, expected)), rep
