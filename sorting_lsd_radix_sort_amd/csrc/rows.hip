@@ -183,9 +183,9 @@ constexpr int64_t kDirectGroups = kManyBins - 1, kDirectSlots = 1 << 20;
 constexpr int64_t kSelfCountSlots = 12 * kPlaceThreads;
 
 int place_items(int64_t n, int64_t bins) { return n <= (bins <= kFewBins ? 128 : 32) * kPlaceThreads ? 1 : 4; }
-int place_blocks(int64_t n, int64_t bins)
+int place_blocks(int64_t n, int items)
 {
-    const int64_t slots = (int64_t)kPlaceThreads * place_items(n, bins);
+    const int64_t slots = (int64_t)kPlaceThreads * items;
     return (int)std::max<int64_t>(1, (n + slots - 1) / slots);
 }
 
@@ -193,7 +193,7 @@ template <int MAX_BINS, int ITEMS, typename SRC>
 lrs_status run_pass(const SRC &src, const Pass &ps, uint32_t *counts, const PlaceOut &out, uint32_t *clear,
                     hipStream_t stream)
 {
-    const int blocks = place_blocks(ps.n, ps.bins);
+    const int blocks = place_blocks(ps.n, ITEMS);
     const bool count = blocks > 1 && ps.n > kSelfCountSlots;
     if (count) {
         count_kernel<SRC, MAX_BINS, ITEMS><<<blocks, kPlaceThreads, 0, stream>>>(src, ps, counts, clear);
@@ -205,16 +205,14 @@ lrs_status run_pass(const SRC &src, const Pass &ps, uint32_t *counts, const Plac
     return launched();
 }
 
+// A pass in blocks of 1024 slots: every pass of an order of ids, which are 131,072 at
+// most, and of digits above nine bits 32,768.
 template <typename SRC>
 lrs_status run_pass(const SRC &src, const Pass &ps, uint32_t *counts, const PlaceOut &out, uint32_t *clear,
                     hipStream_t stream)
 {
-    const bool one = place_items(ps.n, ps.bins) == 1;
-    if (ps.bins <= kFewBins)
-        return one ? run_pass<kFewBins, 1>(src, ps, counts, out, clear, stream)
-                   : run_pass<kFewBins, 4>(src, ps, counts, out, clear, stream);
-    return one ? run_pass<kManyBins, 1>(src, ps, counts, out, clear, stream)
-               : run_pass<kManyBins, 4>(src, ps, counts, out, clear, stream);
+    return ps.bins <= kFewBins ? run_pass<kFewBins, 1>(src, ps, counts, out, clear, stream)
+                               : run_pass<kManyBins, 1>(src, ps, counts, out, clear, stream);
 }
 
 int bits_of(int64_t values)  // bits that hold 0..values - 1
@@ -257,8 +255,7 @@ lrs_status group_layout(int64_t n, int64_t groups, GroupLayout *L)
     L->off_sort = off;
     lrs_status st = LRS_OK;
     if (n <= kDirectIds) {
-        const int64_t bins = (int64_t)1 << digit_bits(n, L->bits);
-        L->sort_bytes = (size_t)place_blocks(n, bins) * (size_t)bins * 4;
+        L->sort_bytes = ((size_t)place_blocks(n, 1) * 4) << digit_bits(n, L->bits);
     } else {
         // the size depends on n and the bit range alone: any distinct pointers will do
         const uintptr_t some = (uintptr_t)1 << 40;
@@ -342,7 +339,10 @@ lrs_status group_direct(const void *ids, int64_t n, int64_t first, int64_t group
 {
     const IdSource<ID> src{(const ID *)ids, first, (uint32_t)groups};
     const Pass ps{(int)n, ~0u, (uint16_t)(groups + 1), 0, (uint8_t)bits_of(groups + 1)};
-    return run_pass(src, ps, counts, PlaceOut{nullptr, (uint32_t *)order, position, offsets}, nullptr, stream);
+    const PlaceOut out{nullptr, (uint32_t *)order, position, offsets};
+    if (place_items(n, ps.bins) == 1) return run_pass(src, ps, counts, out, nullptr, stream);
+    return ps.bins <= kFewBins ? run_pass<kFewBins, 4>(src, ps, counts, out, nullptr, stream)
+                               : run_pass<kManyBins, 4>(src, ps, counts, out, nullptr, stream);
 }
 
 lrs_status group_entry(void *d_temp, size_t *temp_bytes, lrs_id_type id_type, const void *d_ids, int64_t n,
@@ -364,7 +364,9 @@ lrs_status group_entry(void *d_temp, size_t *temp_bytes, lrs_id_type id_type, co
     GroupLayout L;
     lrs_status st = LRS_OK;
     if (direct)
-        L.total = n > kSelfCountSlots ? (size_t)place_blocks(n, groups + 1) * (size_t)(groups + 1) * 4 : 0;
+        L.total = n <= kSelfCountSlots
+                      ? 0
+                      : (size_t)place_blocks(n, place_items(n, groups + 1)) * (size_t)(groups + 1) * 4;
     else
         st = group_layout(n, groups, &L);
     if (st != LRS_OK) return st;
