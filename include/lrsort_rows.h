@@ -39,9 +39,12 @@
  *    query with d_temp == NULL checks the arguments too); the size depends on the
  *    sizes and types alone, not on the pointers' values, and a size of 255 (what
  *    alignment may take) means that nothing is stored there.
- *  - Outputs must not overlap inputs or other outputs (columns of one buffer that
- *    are interleaved with equal row strides may), except where a call allows it;
- *    an overlap that the library sees gives LRS_ERR_INVALID_ARG.
+ *  - Outputs must not overlap inputs or other outputs, except where a call allows
+ *    it: LRS_ERR_INVALID_ARG.  Columns of one buffer do not overlap where their
+ *    rows are equally far apart, nor do a single row, ids, positions or weights
+ *    that lie between a matrix's rows; matrices of different strides are taken to
+ *    overlap if the memory from first to last row does.  Overlap of d_temp with
+ *    any array is undefined.
  *  - Sizes may be zero.  tokens * slots and the number of ids are at most
  *    2^31 - 1 (positions are int32), rows and columns likewise, the counts of
  *    groups and of a gradient's ids at most 2^31 - 2; strides are 64-bit.  Negative

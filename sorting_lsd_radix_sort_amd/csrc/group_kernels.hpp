@@ -1,14 +1,15 @@
 // group_kernels.hpp -- gfx950 (CDNA4, wave64) kernels that order ids stably: one
-// counting pass for a grouping by expert, two or three for an embedding's ids.
+// counting pass for a grouping by expert, one to four for an embedding's ids (of up to
+// eleven bits each, by the number of ids and of rows).
 //
 // Few ids are ordered here, up to a million: their bytes are nothing (12 to 20 per
 // id), so launches and dependent steps bound them.  A pass is one launch (a block
 // counts and places, and counts the other blocks' ids too) or two (count, place), and
 // an embedding's few thousand ids take all their passes in one launch of one block.
 // 1024 threads a block: 16 waves rank 64 ids each by ballots, and the counts of the
-// waves before are summed bin by bin.  32 ids of 256 groups take 3.6 us, 4,096 5.6,
-// 131,072 11.5 (kernels back to back); the launch itself is some 2 us of each.
-// Larger orders take the library's sort.
+// waves before are summed bin by bin.  32 ids of 128 groups take 3.1 us (the kernel
+// alone), 4,096 of 256 groups 5.6, 131,072 11.4 (calls back to back in a captured graph);
+// the launch itself is some 2 us of each.  Larger orders take the library's sort.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -153,7 +154,8 @@ __global__ __launch_bounds__(kPlaceThreads) void count_kernel(SRC src, Pass ps, 
         if (first + i * kPlaceThreads < ps.n) count_digit(s_count, d[i], ps.bins - 1);
     }
     __syncthreads();
-    for (uint32_t b = threadIdx.x; b < ps.bins; b += kPlaceThreads) counts[(int64_t)blockIdx.x * ps.bins + b] = s_count[b];
+    uint32_t *mine = counts + (int64_t)blockIdx.x * ps.bins;
+    for (uint32_t b = threadIdx.x; b < ps.bins; b += kPlaceThreads) mine[b] = s_count[b];
 }
 
 // LDS of a placement by 1024 threads.

@@ -193,7 +193,9 @@ __device__ __forceinline__ void store_scalar(void *p, int type, int64_t i, float
 // Kernels take their counts as 32-bit words, work out what follows from them (vectors,
 // tiles, the grid itself) and ask for nothing that the runtime passes beside their own
 // arguments: a launch with up to 96 bytes of arguments takes 2.8 us of the host's time,
-// one with 128 or more 3.5 to 3.9, and a use of gridDim adds 66 bytes and more.
+// one with 128 or more 3.5 to 3.9, and a use of gridDim adds 66 bytes and more.  (The
+// two that prepare and finish an order by the library's sort do use it, beside the sort's
+// own launches.)
 constexpr int64_t kMaxGridX = 1 << 20, kMaxGridY = 65535;
 
 // The row that this thread serves in row tile `tile`; the same for a whole wave
@@ -281,7 +283,8 @@ __global__ __launch_bounds__(kThreads) void group_finish_kernel(const uint32_t *
     if (position != nullptr)
         for (int64_t j = first; j < n; j += stride) position[order[j]] = keys[j] < groups ? (int32_t)j : -1;
     if (offsets != nullptr)
-        for (int64_t g = first; g <= (int64_t)groups; g += stride) offsets[g] = (int32_t)lower_bound(keys, n, (uint32_t)g);
+        for (int64_t g = first; g <= (int64_t)groups; g += stride)
+            offsets[g] = (int32_t)lower_bound(keys, n, (uint32_t)g);
 }
 
 // ------------------------------------------------------- rows to their places
@@ -290,8 +293,9 @@ __global__ __launch_bounds__(kThreads) void group_finish_kernel(const uint32_t *
 // written and of x, nothing else (reading x once per row written, in the rows' order,
 // took 293 us instead of 245 at 16,384 tokens x 8 x 4096 bf16).  One vector a thread:
 // with two, four times as much is being written at once, and it took 333.  Bound by
-// HBM: 226 us for 1.21 GB, 5.3 TB/s, where rows in sequence would take 221 and a fill
-// of the same bytes 157.  T: an unsigned word of the element's size.
+// HBM: 225 us for 1.21 GB, 5.4 TB/s, where rows in sequence would take 213 and a fill
+// of the same bytes 157.  A token's row is read also where none of its slots has a
+// position.  T: an unsigned word of the element's size.
 template <typename T, bool WAVE_ROW>
 __global__ __launch_bounds__(kThreads) void dispatch_kernel(const T *__restrict__ x, int64_t ld_x,
                                                             const int32_t *__restrict__ position, int tokens,
@@ -309,9 +313,10 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(const T *__restrict_
 }
 
 // A token's rows are summed in the order of its slots, in float32, SLOTS of them in
-// flight per lane.  Bound by HBM: 16,384 tokens x 8 x 4096 bf16 in 198 us, 1.21 GB at
-// 6.1 TB/s (a read of as much reaches 7.1), with one slot in flight; two take 209,
-// eight 217.
+// flight per lane.  Bound by HBM: 16,384 tokens x 8 x 4096 bf16 in 200 us, 1.21 GB at
+// 6.0 TB/s (a read of as much reaches 7.1), calls back to back with one slot in flight
+// (two take 11 us more, eight 17); right behind their gradient, whose stores the caches
+// still hold, 213.  Rows in sequence would take 190.
 template <typename T, bool WAVE_ROW, int SLOTS, bool NT>
 __global__ __launch_bounds__(kThreads) void combine_kernel(const T *__restrict__ rows, int64_t ld_rows,
                                                            uint32_t num_rows, int weight_type,
@@ -353,7 +358,8 @@ __device__ __forceinline__ float lanes_sum(float v, int tx_log2)
 {
     if constexpr (WAVE_ROW) {
         auto add = [&](auto ctrl, auto rows) {
-            const int other = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), ctrl.value, rows.value, 0xf, false);
+            const int other =
+                __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), ctrl.value, rows.value, 0xf, false);
             v += __builtin_bit_cast(float, other);
         };
         using std::integral_constant;
@@ -376,9 +382,10 @@ __device__ __forceinline__ float lanes_sum(float v, int tx_log2)
 // slot.  rows and grad_rows may be the same memory: a thread reads each element before
 // it stores there (a row's last vector also loads elements of the one before it, which
 // may be stored meanwhile, and shifts them out).  Bound
-// by HBM: 16,384 tokens x 8 x 4096 bf16 in 443 us, 2.28 GB at 5.15 TB/s; a copy reaches
-// 5.9, and the same rows in sequence 395 to 413.  Slots two or eight at a time took
-// 447 and 469, a wave per token (no barrier) 478, a workgroup per slot 468.
+// by HBM: 16,384 tokens x 8 x 4096 bf16 in 442 us, 2.28 GB at 5.15 TB/s (calls back to
+// back; 430 behind a sum of rows); a copy reaches 5.9, and the same rows in sequence 395
+// to 413 us.  Slots two or eight at a time took 447 and 469, a wave per token (no
+// barrier) 478, a workgroup per slot 465.
 template <typename T, bool WAVE_ROW, bool NT>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(const T *__restrict__ grad_y, int64_t ld_grad_y,
                                                                 const T *rows, int64_t ld_rows,
@@ -460,14 +467,15 @@ __global__ __launch_bounds__(kThreads) void embedding_kernel(const T *__restrict
     });
 }
 
-// The gradient's sums, bound by HBM: 65,536 ids x 4096 bf16 of 131,072 rows take 302 us
-// here for 1.6 GB (5.3 TB/s), after 26 us of ordering and before 12 of joining.  Sums
+// The gradient's sums, bound by HBM: 65,536 ids x 4096 bf16 of 131,072 rows take 309 us
+// here for 1.6 GB (5.3 TB/s), after 26 us of ordering and before 13 of joining.  Sums
 // and empty rows in separate phases of one launch: mixed evenly they took 25 us more.
 //
 // The sorted ids are cut into pieces of `piece` slots, one piece of a column tile per
 // unit of work, whatever the ids: a run of equal ids may be one slot or all of them,
-// and no unit sums more than two pieces' slots.  A run is summed in registers and stored at once by the piece in which it begins, also where
-// it goes on into the next one (which passes over it).  Only a run that goes on
+// and no unit sums more than two pieces' slots.  A run is summed in registers and stored
+// at once by the piece in which it begins, also where it goes on into the next one
+// (which passes over it).  Only a run that goes on
 // beyond that is left as float32 partial sums, one for each piece that it touches:
 // slot 1 of the piece in which it begins, slot 0 of those after it.  The piece in
 // which it begins also enters itself in a list (in any order: each run is joined by

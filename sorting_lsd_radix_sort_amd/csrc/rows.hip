@@ -107,17 +107,27 @@ dim3 grid_of(const Tiling &t)
 
 bool wave_row(const Tiling &t) { return (1 << t.tx_log2) >= kWave; }
 
-unsigned flat_grid(int64_t n) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>((n + kThreads - 1) / kThreads, 8192)); }
+unsigned flat_grid(int64_t n)
+{
+    return (unsigned)std::max<int64_t>(1, std::min<int64_t>((n + kThreads - 1) / kThreads, 8192));
+}
 
+// Times here and below: rows of 4096 bf16, 8 slots a token, calls back to back.
+//
 // Below this many workgroups (eight a CU) the chip is not full, and a token's slots
-// are taken at once: 128 tokens x 8 slots x 4096 bf16, gradient 10.7 us instead of
-// 15.6.  Above it slot by slot: 16,384 tokens, sum 198 us instead of 217, gradient
-// 443 instead of 468 (more rows open at once cost HBM more than they hide).
+// are taken at once: the gradient of 128 tokens in 10.4 us instead of 15.5, of 512 in
+// 20.6 instead of 23.3 and their sum in 8.1 instead of 9.5.  Above it slot by slot:
+// 16,384 tokens, sum 200 us instead of 217, gradient 442 instead of 465; 4,096 tokens,
+// gradient 111 instead of 119 (more rows open at once cost HBM more than they hide).
+// At 1,024 tokens the limit is off by some us either way: the gradient takes 35.3 at
+// once and 29.8 slot by slot, the sum 16.8 slot by slot and 13.8 at once.
 constexpr int64_t kFewTiles = 2048;
 
-// More bytes than the L2s hold (32 MB) go past them: 16,384 tokens x 8 x 4096 bf16,
-// sum 198 us instead of 230, gradient 443 instead of 458; 2,048 tokens, 27 instead
-// of 33 and 65 instead of 70; 512 tokens (38 MB) the same either way.
+// More bytes than the L2s hold (32 MB) go past them: 16,384 tokens, sum 200 us instead
+// of 230, gradient 442 instead of 456; 2,048 tokens, 28 instead of 33 and 64 instead of
+// 69; 512 tokens (38 MB) the same either way, 1,024 (75 MB) 17 instead of 14 and 35
+// instead of 37.  The bytes are those of all slots, also of those without a position:
+// a rank with a share of the experts is taken for one that holds them all.
 bool streams(int64_t bytes) { return bytes > ((int64_t)32 << 20); }
 
 // A gradient of more bytes than the last-level cache is read past the L2s; a smaller
@@ -125,9 +135,9 @@ bool streams(int64_t bytes) { return bytes > ((int64_t)32 << 20); }
 constexpr int64_t kLastCacheBytes = (int64_t)256 << 20;
 
 // LDS that a dispatch asks for and does not use, so that six workgroups fit a CU
-// and not eight: fewer rows are being written at once.  16,384 tokens x 8 x 4096
-// bf16 in 226 us instead of 245, 4,096 x 8 x 8192 in 115 instead of 128; rows of
-// 4 KB the same, and small calls too.
+// and not eight: fewer rows are being written at once.  16,384 tokens in 225 us
+// instead of 244, 4,096 in 58 instead of 60; rows of 4 KB the same, and small calls
+// too.
 constexpr unsigned kDispatchLds = 26 * 1024;
 
 // Calls f with the truth value as a constant.
@@ -166,20 +176,24 @@ lrs_status guarded(F &&f)
 
 // ------------------------------------------------------------------ grouping
 
-// Few ids are ordered by counting passes of this file's own: a grouping of up to 2048
-// groups and a million ids in one (262,144 ids of 256 groups in 13.8 us; by the sort
-// 31.4), an embedding's ids in passes of up to eleven bits.  The others take the
-// library's sort.
+// Few ids are ordered by counting passes of this file's own, the others by the
+// library's sort.  (Times of orders: a call's on the GPU, calls back to back in a
+// captured graph, ids uniform.)
+//
+// A grouping of up to 2048 groups and 2^20 ids takes one pass: 262,144 ids of 256
+// groups 14 us, by the sort 32, 2^20 ids 24 and 47, 2^21 57 and 62; of 2048 groups 25
+// and 44, 59 and 63, 179 and 82 (and if all ids are equal, 22 and 27, 50 and 38).
 constexpr int kFewBins = 513, kManyBins = 2049;
 constexpr int64_t kDirectGroups = kManyBins - 1, kDirectSlots = 1 << 20;
 
 // Blocks of 1024 slots, or of 4096 where those would be many (a block reads every
 // block's counts; a wave's ranking is what they share): 131,072 ids of 256 groups in
-// 11.5 us with 128 blocks, 15 with 32; of 2048 groups 28.5 with 128, and 262,144 ids
-// 24.5 with 64.  Up to 12K slots the blocks count one another's slots and need no
-// count launch: 6,000 ids of 256 groups in 6.4 us instead of 7.8, 12,282 in 8.2
-// instead of 8.7, 16,384 in 9.3 instead of 7.7 (kernels alone; a launch is 3 us of
-// the host's).
+// 11.8 us by 1024, 12.5 by 4096, 262,144 in 16.5 and 14.1; of 2048 groups 32,768 ids in
+// 14.5 and 15.9, 65,536 in 19.1 and 17.2.  Up to 12K slots the blocks count one
+// another's slots and need no count launch (which is 3 us of the host's too): 8,192 ids
+// of 256 groups in 7.0 us instead of 7.9, 12,288 in 8.1 instead of 8.9, 16,384 in 9.3
+// instead of 7.6; of 8 groups 8,192 in 6.3 either way, 12,288 in 7.5 instead of 6.4; of
+// 2048 groups 12,288 in 11.0 instead of 13.5, 24,576 in 14.6 instead of 13.4.
 constexpr int64_t kSelfCountSlots = 12 * kPlaceThreads;
 
 int place_items(int64_t n, int64_t bins) { return n <= (bins <= kFewBins ? 128 : 32) * kPlaceThreads ? 1 : 4; }
@@ -229,7 +243,11 @@ struct GroupLayout {
     int bits = 0;
 };
 
-constexpr int64_t kDirectIds = 1 << 17, kOrderSlots = 4 * kPlaceThreads;  // (one block has all passes up to here)
+// An embedding's ids are ordered by passes of up to eleven bits up to kDirectIds of
+// them: 131,072 of 65,536 ids 30 us, by the sort 44, of 1,000,000 ids 41 and 53, all
+// equal 26 and 40.  262,144 would take 41 and 49, 50 and 70, 33 and 32; 524,288 80 and
+// 58, 75 and 80.  Up to kOrderSlots one block has all passes.
+constexpr int64_t kDirectIds = 1 << 17, kOrderSlots = 4 * kPlaceThreads;
 int passes_of(int bits, int digit) { return (std::max(bits, 1) + digit - 1) / digit; }
 
 // Bits of a pass's digit.  Digits of eleven bits save a launch or two in some orders,
@@ -270,7 +288,8 @@ lrs_status group_layout(int64_t n, int64_t groups, GroupLayout *L)
 // storage).  The first kernel sets *clear to zero, where it is given.
 template <typename ID>
 lrs_status sort_ids(const GroupLayout &L, char *temp, const void *ids, int64_t n, int64_t first, int64_t groups,
-                    int32_t *order, const uint32_t **sorted, const uint32_t **index, uint32_t *clear, hipStream_t stream)
+                    int32_t *order, const uint32_t **sorted, const uint32_t **index, uint32_t *clear,
+                    hipStream_t stream)
 {
     uint32_t *keys = (uint32_t *)(temp + L.off_keys), *at = (uint32_t *)(temp + L.off_index);
     uint32_t *out = (uint32_t *)(temp + L.off_sorted);
@@ -281,10 +300,8 @@ lrs_status sort_ids(const GroupLayout &L, char *temp, const void *ids, int64_t n
     if (n <= kDirectIds) {
         const int width = digit_bits(n, L.bits), passes = passes_of(L.bits, width);
         if (n <= kOrderSlots) {
-            if (n <= kPlaceThreads)
-                order_kernel<ID, kFewBins, 1><<<1, kPlaceThreads, 0, stream>>>(src, (int)n, L.bits, width, out, ord, clear);
-            else
-                order_kernel<ID, kFewBins, 4><<<1, kPlaceThreads, 0, stream>>>(src, (int)n, L.bits, width, out, ord, clear);
+            auto *k = n <= kPlaceThreads ? order_kernel<ID, kFewBins, 1> : order_kernel<ID, kFewBins, 4>;
+            k<<<1, kPlaceThreads, 0, stream>>>(src, (int)n, L.bits, width, out, ord, clear);
             return launched();
         }
         uint32_t *counts = (uint32_t *)(temp + L.off_sort);
@@ -302,8 +319,8 @@ lrs_status sort_ids(const GroupLayout &L, char *temp, const void *ids, int64_t n
         }
         return LRS_OK;
     }
-    group_keys_kernel<ID><<<flat_grid(n), kThreads, 0, stream>>>((const ID *)ids, (int)n, first, (uint32_t)groups, keys, at,
-                                                                clear);
+    group_keys_kernel<ID><<<flat_grid(n), kThreads, 0, stream>>>((const ID *)ids, (int)n, first, (uint32_t)groups, keys,
+                                                                at, clear);
     const lrs_status st = launched();
     if (st != LRS_OK) return st;
     size_t bytes = L.sort_bytes;
@@ -425,7 +442,8 @@ LRS_API lrs_status lrs_dispatch_rows(lrs_row_type type, const void *d_x, int64_t
         const Tiling t = tiling_of(tokens, cols, kVec<W>);
         auto *k = wave_row(t) ? dispatch_kernel<W, true> : dispatch_kernel<W, false>;
         k<<<grid_of(t), kThreads, kDispatchLds, stream>>>((const W *)d_x, ld_x, d_position, (int)tokens, (int)slots,
-                                                          (int)cols, (uint32_t)num_rows, (W *)d_rows, ld_rows, t.tx_log2);
+                                                          (int)cols, (uint32_t)num_rows, (W *)d_rows, ld_rows,
+                                                          t.tx_log2);
         return launched();
     };
     return b == 4 ? run(uint32_t{}) : run(uint16_t{});
@@ -599,7 +617,8 @@ lrs_status embedding_grad_entry(void *d_temp, size_t *temp_bytes, lrs_row_type t
     const uint32_t *sorted, *index;
     float *partial = (float *)(temp + align_up(L.total));
     uint32_t *list = (uint32_t *)(temp + align_up(L.total) + S.partial_bytes);
-    st = sort_ids(L, temp, id_type, d_ids, n, first, num_ids, nullptr, &sorted, &index, S.joins() ? list : nullptr, stream);
+    st = sort_ids(L, temp, id_type, d_ids, n, first, num_ids, nullptr, &sorted, &index, S.joins() ? list : nullptr,
+                  stream);
     if (st != LRS_OK) return st;
     const Pieces pc{sorted, index, partial, list, (int)n, S.piece, (uint32_t)num_ids, (int)cols};
     return with_type(type, [&](auto elem) {

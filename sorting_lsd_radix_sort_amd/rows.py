@@ -110,7 +110,8 @@ def lrs_embedding(row_type, d_table, ld_table, num_ids, id_type, d_ids, n, first
     """Calls the C function of the same name."""
     _check(load_library().lrs_embedding(_code(ROW_TYPE_CODES, row_type), _ptr(d_table), int(ld_table), int(num_ids),
                                         _code(ID_TYPE_CODES, id_type), _ptr(d_ids), int(n),
-                                        _int64("first_id", first_id), float(scale), int(cols), _ptr(d_y), int(ld_y), _stream(stream)), "lrs_embedding")
+                                        _int64("first_id", first_id), float(scale), int(cols), _ptr(d_y), int(ld_y),
+                                        _stream(stream)), "lrs_embedding")
 
 
 def lrs_embedding_grad(d_temp, temp_bytes, row_type, d_grad_y, ld_grad_y, id_type, d_ids, n, first_id, scale, grad_type,
@@ -413,8 +414,8 @@ def combine_rows_grad(grad_y, rows, position, weights, grad_rows=None, stream=No
     grad_y, ld_y = _rows_in(grad_y, tokens, cols)
     rows, ld = _rows_in(rows, num_rows, cols)
     _run("lrs_combine_rows_grad", stream, (rows, grad_y, pos, w, grad_rows, grad_w),
-         (code, grad_y.data_ptr(), ld_y, rows.data_ptr(), ld, num_rows, pos.data_ptr(), wcode, _at(w), tokens, slots, cols,
-          grad_rows.data_ptr(), ld_out, _at(grad_w)), given)
+         (code, grad_y.data_ptr(), ld_y, rows.data_ptr(), ld, num_rows, pos.data_ptr(), wcode, _at(w), tokens, slots,
+          cols, grad_rows.data_ptr(), ld_out, _at(grad_w)), given)
     return grad_rows, grad_w
 
 
