@@ -14,6 +14,10 @@ allocate outputs and temp storage as torch tensors.
 ``embedding`` and ``embedding_grad`` (``rows.py``, ``include/lrsort_rows.h``) move
 and sum the rows of a matrix in the order of small integer keys: tokens sorted by
 expert and back, and an embedding's gradient by sorted tokens.
+
+``route_tokens``, ``route_tokens_grad``, ``beam_select`` and ``beam_reorder``
+(``choose.py``, ``include/lrsort_choose.h``) choose the best few of a row, the keys by
+which rows are moved: a router's experts, beam search's continuations.
 """
 from __future__ import annotations
 
@@ -41,7 +45,8 @@ EXPORTED = SORT_FUNCTIONS + ("lrs_sort_digits", "lrs_status_string", "lrs_device
                              "lrs_prof_stop", "lrs_prof_count", "lrs_prof_read",
                              "lrs_prof_release", "lrs_bench_read", "lrs_sort_digits_noalloc",
                              "lrs_group_tokens", "lrs_dispatch_rows", "lrs_combine_rows",
-                             "lrs_combine_rows_grad", "lrs_embedding", "lrs_embedding_grad")
+                             "lrs_combine_rows_grad", "lrs_embedding", "lrs_embedding_grad",
+                             "lrs_route_tokens", "lrs_route_tokens_grad", "lrs_beam_select", "lrs_beam_reorder")
 
 
 class LrsError(RuntimeError):
@@ -92,6 +97,7 @@ def load_library() -> ctypes.CDLL:
     lib.lrs_bench_read.argtypes = [vp, sz, vp, vp]
     lib.lrs_bench_read.restype = ci
     rows.declare(lib)
+    choose.declare(lib)
     _lib = lib
     return lib
 
@@ -417,3 +423,6 @@ from . import rows  # noqa: E402  (uses the helpers above)
 from .rows import (combine_rows, combine_rows_grad, dispatch_rows, embedding, embedding_grad,  # noqa: E402,F401
                    group_tokens, lrs_combine_rows, lrs_combine_rows_grad, lrs_dispatch_rows, lrs_embedding,
                    lrs_embedding_grad, lrs_group_tokens)
+from . import choose  # noqa: E402  (uses the helpers of rows)
+from .choose import (beam_reorder, beam_select, lrs_beam_reorder, lrs_beam_select, lrs_route_tokens,  # noqa: E402,F401
+                     lrs_route_tokens_grad, route_tokens, route_tokens_grad)

@@ -1,10 +1,12 @@
 """Builds the HIP library liblrsort.so in-tree for gfx950 with hipcc.
 
 Run ``python -m sorting_lsd_radix_sort_amd.build``; ``__graft_entry__.build()``
-calls :func:`build` too.  The library is two translation units, compiled side
-by side: the sort (``csrc/lrsort.hip`` with the kernels of ``csrc/kernels.hpp``)
-and the row operators (``csrc/rows.hip`` with those of ``csrc/row_kernels.hpp``
-and ``csrc/group_kernels.hpp``).
+calls :func:`build` too.  The library is four translation units, compiled side
+by side: the sort (``csrc/lrsort.hip`` with the kernels of ``csrc/kernels.hpp``),
+the row operators (``csrc/rows.hip`` with those of ``csrc/row_kernels.hpp``
+and ``csrc/group_kernels.hpp``), a router's choice (``csrc/route.hip``,
+``csrc/route_kernels.hpp``) and beam search (``csrc/beam.hip``,
+``csrc/beam_kernels.hpp``).
 """
 from __future__ import annotations
 
@@ -16,11 +18,11 @@ import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCES = [os.path.join(PKG, "csrc", "lrsort.hip"), os.path.join(PKG, "csrc", "rows.hip")]
-DEPS = SOURCES + [os.path.join(PKG, "csrc", "kernels.hpp"), os.path.join(PKG, "csrc", "row_kernels.hpp"),
-                  os.path.join(PKG, "csrc", "group_kernels.hpp"),
-                  os.path.join(ROOT, "include", "lrsort.h"), os.path.join(ROOT, "include", "lrsort_prof.h"),
-                  os.path.join(ROOT, "include", "lrsort_rows.h")]
+SOURCES = [os.path.join(PKG, "csrc", name + ".hip") for name in ("lrsort", "rows", "route", "beam")]
+DEPS = SOURCES + [os.path.join(PKG, "csrc", name + ".hpp")
+                  for name in ("kernels", "row_vectors", "row_args", "row_kernels", "group_kernels", "choose_common",
+                               "route_kernels", "beam_kernels")] + \
+    [os.path.join(ROOT, "include", name + ".h") for name in ("lrsort", "lrsort_prof", "lrsort_rows", "lrsort_choose")]
 LIB = os.path.join(PKG, "liblrsort.so")
 ARCH = "gfx950"
 
