@@ -14,20 +14,22 @@ using namespace lrs_choose;
 
 static_assert(kMaxContinuations == LRS_MAX_BEAM_COUNT && kMaxBeams == LRS_MAX_BEAMS, "limits of the header");
 
-// How the rows of a selection are cut: parts of whole steps of a wave.
+// How the rows of a selection are cut: parts of a workgroup's lanes with `vectors` of 16
+// bytes each.
 struct ScanLayout {
-    int64_t parts = 0, part = 0;
+    int vectors = 8;
+    int64_t parts = 0;
     size_t best_bytes = 0, part_bytes = 0;
 };
 
-ScanLayout scan_layout(int64_t rows, int64_t vocab, int64_t count, int64_t step)
+constexpr int64_t kScanParts = 512;
+
+ScanLayout scan_layout(int64_t rows, int64_t vocab, int64_t count, int64_t vec)
 {
     ScanLayout s;
-    const int64_t most = std::max<int64_t>(1, (vocab + step - 1) / step);  // parts of one step
-    const int64_t wanted = std::max<int64_t>(1, 4096 / std::max<int64_t>(1, rows));
-    s.parts = std::min(std::min(most, wanted), (int64_t)64);
-    s.part = (most + s.parts - 1) / s.parts * step;
-    s.parts = std::max<int64_t>(1, (vocab + s.part - 1) / s.part);
+    auto parts = [&] { return (vocab + kScanThreads * vec * s.vectors - 1) / (kScanThreads * vec * s.vectors); };
+    while (s.vectors > 1 && rows * parts() < kScanParts) s.vectors /= 2;
+    s.parts = parts();
     s.best_bytes = align_up((size_t)(rows * s.parts * count) * 8);
     s.part_bytes = align_up((size_t)(rows * s.parts) * sizeof(Part));
     return s;
@@ -56,19 +58,29 @@ lrs_status beam_entry(void *d_temp, size_t *temp_bytes, lrs_row_type type, const
         for (int j = 0; j < i; ++j)
             if (overlap(out[i], out[j])) return LRS_ERR_INVALID_ARG;
     }
-    const ScanLayout s = scan_layout(rows, vocab, count, kWave * 16 / b);
+    const ScanLayout s = scan_layout(rows, vocab, count, 16 / b);
     char *temp;
     const lrs_status st = take_temp(d_temp, temp_bytes, s.best_bytes + s.part_bytes, &temp);
     if (st != LRS_OK || temp == nullptr || n == 0) return st;
     if (rows > 0) {
-        const Scan scan{d_scores, d_finished, (uint64_t *)temp, (Part *)(temp + s.best_bytes), s.part, (int)rows,
-                        (int)vocab, (int)s.parts, (int)count};
-        const int64_t blocks = (rows * s.parts + kScanWaves - 1) / kScanWaves;
-        const unsigned grid = (unsigned)std::min(blocks, kMaxGridX);
+        const Scan scan{d_scores, d_finished, (uint64_t *)temp, (Part *)(temp + s.best_bytes), (int)rows, (int)vocab,
+                        (int)s.parts, (int)count};
+        const unsigned grid = (unsigned)std::min(rows * s.parts, kMaxGridX);
         const lrs_status done = with_type(type, [&](auto elem) {
             using T = decltype(elem);
             with_bool(normalize != 0, [&](auto sum) {
-                beam_scan_kernel<T, sum.value><<<grid, kScanThreads, 0, stream>>>((const T *)d_logits, ld, scan);
+                auto run = [&](auto vectors) {
+                    beam_scan_kernel<T, sum.value, vectors.value>
+                        <<<grid, kScanThreads, 0, stream>>>((const T *)d_logits, ld, scan);
+                };
+                if (s.vectors == 8)
+                    run(std::integral_constant<int, 8>{});
+                else if (s.vectors == 4)
+                    run(std::integral_constant<int, 4>{});
+                else if (s.vectors == 2)
+                    run(std::integral_constant<int, 2>{});
+                else
+                    run(std::integral_constant<int, 1>{});
             });
             return launched();
         });
@@ -77,8 +89,7 @@ lrs_status beam_entry(void *d_temp, size_t *temp_bytes, lrs_row_type type, const
     const Join join{d_scores, d_finished, (const uint64_t *)temp, (const Part *)(temp + s.best_bytes), d_out_scores,
                     d_parents, d_tokens, (int)beams, (int)vocab, (int)s.parts, (int)count, (int)end_id,
                     normalize != 0, id_type == LRS_ID_I64};
-    beam_join_kernel<<<(unsigned)std::min(batch, kMaxGridX), kJoinThreads, (unsigned)(beams * 8), stream>>>(join,
-                                                                                                         (int)batch);
+    beam_join_kernel<<<(unsigned)std::min(batch, kMaxGridX), kJoinThreads, 0, stream>>>(join, (int)batch);
     return launched();
 }
 

@@ -10,9 +10,10 @@
 
 namespace lrs_choose {
 
-constexpr int kScanThreads = 256, kScanWaves = kScanThreads / kWave;
+constexpr int kScanThreads = 512, kScanWaves = kScanThreads / kWave;
 constexpr int kMaxContinuations = 64, kMaxBeams = 1024;  // of one search
-constexpr int kHeld = 2 * kWave;   // candidates that a wave holds
+constexpr int kListed = kScanWaves * kMaxContinuations;  // candidates that a part collects
+constexpr int kHeld = 2 * kWave;                         // and that a wave holds among ties
 
 // A candidate is its logit's order key above the complement of its token: larger is
 // better, and of equal logits the lowest token.
@@ -24,15 +25,15 @@ __device__ __forceinline__ uint64_t candidate_of(float l, int token)
 __device__ __forceinline__ float logit_of(uint64_t c) { return value_of((uint32_t)(c >> 32)); }
 __device__ __forceinline__ int token_of(uint64_t c) { return (int)~(uint32_t)c; }
 
-// What a wave leaves of its part of a row beside its best candidates: the largest logit
-// and the sum of exp(l - top).
+// What is left of a part of a row beside its best candidates: the largest logit and the
+// sum of exp(l - top).
 struct Part {
     double sum;
     float top;
     float pad;
 };
 
-// Of the first `n` <= kHeld candidates in LDS keeps the `count` best, in order, and
+// Of the first `n` <= kHeld candidates of a wave keeps the `count` best, in order, and
 // returns how many these are.
 __device__ __forceinline__ int keep_best(uint64_t *held, int n, int count, int lane)
 {
@@ -56,111 +57,175 @@ struct Scan {
     const uint8_t *finished;
     uint64_t *best;  // rows x parts x count
     Part *of_part;   // rows x parts
-    int64_t part;    // logits of one, a multiple of a wave's step
     int rows, vocab, parts, count;
 };
 
-// A wave reads its part of a row once, 16 bytes a lane at a time, keeping the `count`
-// best logits and (SUM) the maximum and the sum of the softmax.  A logit becomes a
-// candidate where it is above the worst kept one; of the first step's logits those that
-// the `count`-th of the lanes' maxima does not exceed.
-template <typename T, bool SUM>
+// A workgroup takes a part of a row, R vectors a lane, which it reads once and keeps in
+// registers: first the lanes' maxima; then, with the largest of them known, (SUM) the
+// part's sum of exponentials and the logits that are candidates.  A bound for these:
+// the `count`-th largest of 64 maxima, each over an equal share of the part, so that
+// some `count` ln(64 / (64 - count)) / (count / 64) logits reach it (18 for 16).
+// (Where ties make them too many, a wave keeps its best in a list of its own.)
+template <typename T, bool SUM, int R>
 __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const T *__restrict__ logits, int64_t ld, Scan a)
 {
-    constexpr int VEC = kVec<T>, STEP = kWave * VEC;
+    constexpr int VEC = kVec<T>;
+    constexpr int64_t PART = (int64_t)kScanThreads * VEC * R;
+    __shared__ uint32_t maxima[kScanWaves][kWave];
+    __shared__ uint64_t list[kListed];
     __shared__ uint64_t of_wave[kScanWaves][kHeld];
-    const int lane = (int)threadIdx.x % kWave;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
-    uint64_t *held = of_wave[wave];
+    __shared__ double sums[kScanWaves];
+    __shared__ uint32_t bound, largest;
+    __shared__ int listed;
+    const int tid = (int)threadIdx.x, lane = tid % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const float none = -__builtin_inff();
 
     const int64_t jobs = (int64_t)a.rows * a.parts;
-    for (int64_t job = (int64_t)blockIdx.x * kScanWaves + wave; job < jobs; job += kMaxGridX * kScanWaves) {
+    for (int64_t job = blockIdx.x; job < jobs; job += kMaxGridX) {
         const int row_at = (int)(job / a.parts);
-        // (64 bits: a step past the end of a vocabulary of 2^31 - 1 is no int)
-        const int64_t from = job % a.parts * a.part;
-        const int64_t to = a.vocab - from < a.part ? a.vocab : from + a.part;
+        // (64 bits: a place past the end of a vocabulary of 2^31 - 1 is no int)
+        const int64_t from = job % a.parts * PART;
         const float score = a.scores[row_at];
         if (score == none || (a.finished != nullptr && a.finished[row_at] != 0)) continue;
         const T *row = logits + row_at * ld;
 
-        int n = 0;                // held
-        uint64_t above = 0ull;    // a candidate is larger
-        float least = none;       // and its logit not below this
-        float top = none;
-        double sum = 0.0;
-        bool first = true;
-        for (int64_t c0 = from; c0 < to; c0 += STEP) {
-            const Col col = col_of<T>(to, c0 + lane * VEC);
-            const u32x4 r = load_col<T, true>(row, col);
-            float l[VEC];
-            float most = none;
+        u32x4 r[R];
+        if (from + PART <= a.vocab) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                l[i] = i < col.valid ? element<T>(r, i) : none;
-                most = __builtin_fmaxf(most, l[i]);
+            for (int j = 0; j < R; ++j)
+                r[j] = __builtin_nontemporal_load(
+                    reinterpret_cast<const u32x4_any *>(row + from + (int64_t)(j * kScanThreads + tid) * VEC));
+        } else {  // the last part: -infinity behind the end
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+                r[j] = issue<T, true>(row, col_of<T>(a.vocab, from + (int64_t)(j * kScanThreads + tid) * VEC));
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                const Col col = col_of<T>(a.vocab, from + (int64_t)(j * kScanThreads + tid) * VEC);
+                r[j] = settle<T>(r[j], col);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (i >= col.valid) r[j] = with_element<T>(r[j], i, none);
             }
-            if constexpr (SUM) {
-                const float higher = __builtin_fmaxf(top, most);
-                if (higher != none) {
-                    float part = 0.0f;
+        }
+        float most[R], of_lane = none;
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) part += __builtin_amdgcn_exp2f((l[i] - higher) * 1.44269504f);
-                    sum = sum * (double)__builtin_amdgcn_exp2f((top - higher) * 1.44269504f) + (double)part;
-                    top = higher;
-                } else {
+        for (int j = 0; j < R; ++j) {
+            most[j] = element<T>(r[j], 0);
+#pragma unroll
+            for (int i = 1; i < VEC; ++i) most[j] = __builtin_fmaxf(most[j], element<T>(r[j], i));
+            of_lane = __builtin_fmaxf(of_lane, most[j]);
+        }
+        maxima[wave][lane] = key_of(of_lane);
+        if (tid == 0) listed = 0;
+        __syncthreads();
+        if (wave == 0) {
+            uint32_t m = 0u;
+#pragma unroll
+            for (int w = 0; w < kScanWaves; ++w) m = maxima[w][lane] > m ? maxima[w][lane] : m;
+            // the upper half of the count-th largest key, bit by bit
+            uint32_t key = 0u;
+#pragma unroll
+            for (int bit = 15; bit >= 0; --bit) {
+                const uint32_t trial = key | 1u << bit;
+                if (__builtin_popcountll(__builtin_amdgcn_ballot_w64(m >> 16 >= trial)) >= a.count) key = trial;
+            }
+            const uint32_t top = team_max<kWave>(m);
+            if (lane == 0) bound = key == 0u ? 1u : key << 16, largest = top;
+        }
+        __syncthreads();
+        const uint32_t least_key = bound;
+        const float least = least_key == 1u ? -3.402823466e38f : value_of(least_key);
+        const float top = value_of(largest);
+
+        if constexpr (SUM) {
+            double sum = 0.0;
+            if (largest != 0u) {
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+                    float e[VEC];
 #pragma unroll
                     for (int i = 0; i < VEC; ++i)
-                        if (l[i] != l[i]) sum += (double)l[i];  // NaN beside nothing but -infinity
+                        e[i] = __builtin_amdgcn_exp2f((element<T>(r[j], i) - top) * 1.44269504f);
+#pragma unroll
+                    for (int n = VEC / 2; n > 0; n /= 2)
+#pragma unroll
+                        for (int i = 0; i < n; ++i) e[i] += e[i + n];
+                    sum += (double)e[0];
                 }
+            } else {  // nothing but -infinity, or NaN, which shows
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        const float l = element<T>(r[j], i);
+                        sum += l != l ? (double)l : 0.0;
+                    }
             }
-            if (first) {
-                // at least `count` logits are not below the count-th largest maximum
-                const uint32_t mine = key_of(most);
-                int before = 0;
-                for (int i = 0; i < kWave; ++i) {
-                    const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)mine, i);
-                    before += o > mine || (o == mine && i < lane);
-                }
-                const uint64_t there = __builtin_amdgcn_ballot_w64(before == a.count - 1);
-                const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)mine, __builtin_ctzll(there));
-                above = key == 0u ? 0xFFFFFFFFull : ((uint64_t)key << 32) - 1;
-                least = value_of(key);
-                first = false;
-            }
-            if (__builtin_amdgcn_ballot_w64(most >= least && most != none) == 0ull) continue;
+            sum = team_sum64<kWave>(sum);
+            if (lane == 0) sums[wave] = sum;
+        }
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            if (__builtin_amdgcn_ballot_w64(most[j] >= least) == 0ull) continue;
+            const int token = (int)from + (j * kScanThreads + tid) * VEC;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const int token = (int)col.c + i;
-                uint64_t c = candidate_of(l[i], token);
-                bool takes = l[i] >= least && c > above && (uint32_t)(c >> 32) != 0u;
-                uint64_t all = __builtin_amdgcn_ballot_w64(takes);
-                if (all == 0ull) continue;
-                if (n + __builtin_popcountll(all) > kHeld) {
-                    n = keep_best(held, n, a.count, lane);
-                    if (n == a.count) {
-                        above = held[n - 1];
-                        least = logit_of(above);
-                    }
-                    takes = takes && c > above;
-                    all = __builtin_amdgcn_ballot_w64(takes);
+                const float l = element<T>(r[j], i);
+                if (l >= least) {
+                    const int at = atomicAdd(&listed, 1);
+                    if (at < kListed) list[at] = candidate_of(l, token + i);
                 }
-                if (takes) held[n + __builtin_popcountll(all & ((1ull << lane) - 1))] = c;
-                n += __builtin_popcountll(all);
             }
         }
-        n = keep_best(held, n, a.count, lane);
-        if (lane < a.count) a.best[job * a.count + lane] = lane < n ? held[lane] : 0ull;
-        if constexpr (SUM) {
-            float high = top;
+        __syncthreads();
+        int n = listed;
+        if (n > kListed) {
+            uint64_t *held = of_wave[wave];
+            uint64_t above = 0ull;
+            n = 0;
 #pragma unroll
-            for (int d = 1; d < kWave; d *= 2) high = __builtin_fmaxf(high, __shfl_xor(high, d, kWave));
-            double s = top == none ? sum : sum * exp((double)top - (double)high);
+            for (int j = 0; j < R; ++j) {
+                const int token = (int)from + (j * kScanThreads + tid) * VEC;
 #pragma unroll
-            for (int d = 1; d < kWave; d *= 2) s += __shfl_xor(s, d, kWave);
-            if (lane == 0) a.of_part[job] = Part{s, high, 0.0f};
+                for (int i = 0; i < VEC; ++i) {
+                    const float l = element<T>(r[j], i);
+                    const uint64_t c = candidate_of(l, token + i);
+                    bool takes = l >= least && c > above;
+                    uint64_t all = __builtin_amdgcn_ballot_w64(takes);
+                    if (all == 0ull) continue;
+                    if (n + __builtin_popcountll(all) > kHeld) {
+                        n = keep_best(held, n, a.count, lane);
+                        if (n == a.count) above = held[n - 1];
+                        takes = takes && c > above;
+                        all = __builtin_amdgcn_ballot_w64(takes);
+                    }
+                    if (takes) held[n + __builtin_popcountll(all & ((1ull << lane) - 1))] = c;
+                    n += __builtin_popcountll(all);
+                }
+            }
+            n = keep_best(held, n, a.count, lane);
+            if (lane < a.count) list[wave * a.count + lane] = lane < n ? held[lane] : 0ull;
+            n = kScanWaves * a.count;
+            __syncthreads();
         }
-        wave_sync();
+        // each candidate's place, by counting those that are better
+        uint64_t *best = a.best + job * a.count;
+        if (tid < n) {
+            const uint64_t mine = list[tid];
+            int before = 0;
+            for (int i = 0; i < n; ++i) before += list[i] > mine;
+            if (mine != 0ull && before < a.count) best[before] = mine;
+        }
+        if (n < a.count && tid >= n && tid < a.count) best[tid] = 0ull;
+        if constexpr (SUM)
+            if (tid == 0) {
+                double sum = 0.0;
+                for (int w = 0; w < kScanWaves; ++w) sum += sums[w];
+                a.of_part[job] = Part{sum, top, 0.0f};
+            }
+        __syncthreads();
     }
 }
 
@@ -178,7 +243,11 @@ struct Join {
     uint8_t normalize, wide_ids;
 };
 
-constexpr int kJoinThreads = 1024;
+constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / kWave;
+constexpr int kJoinHeld = 2;                          // candidates a thread holds
+constexpr int kJoinBlock = kJoinThreads * kJoinHeld;  // and the workgroup
+constexpr int kRankLanes = 16;                        // lanes that rank one together
+constexpr int kRanked = kJoinThreads / kRankLanes;
 
 // A continuation: its total's order key (float64), then its beam and token.
 struct Total {
@@ -191,30 +260,60 @@ __device__ __forceinline__ bool better(const Total &a, const Total &b)
     return a.key > b.key || (a.key == b.key && a.flat < b.flat);
 }
 
-// One workgroup per search: the beams' log sums from their parts, the `count`-th best
-// of the parts' best as a bound, and what reaches it ranked by counting.
+// Totals in LDS, and how many of the first n are better than the i-th: for the 16 lanes
+// that ask for the same i.
+template <int SIZE>
+struct Totals {
+    uint64_t key[SIZE];
+    uint32_t flat[SIZE];
+    __device__ __forceinline__ Total at(int i) const { return {key[i], flat[i]}; }
+    __device__ __forceinline__ void set(int i, const Total &t) { key[i] = t.key, flat[i] = t.flat; }
+    __device__ __forceinline__ int before(int i, int n) const
+    {
+        const Total mine = at(i);
+        uint32_t b = 0;
+        for (int o = (int)threadIdx.x % kRankLanes; o < n; o += kRankLanes) b += better(at(o), mine);
+        return (int)team_reduce<kRankLanes>(b, [](uint32_t x, uint32_t y) { return x + y; });
+    }
+};
+
+// One workgroup per search: the beams' log sums from their parts; then the candidates of
+// all parts at once, a few a thread, those that do not reach the `count`-th largest of 64
+// maxima left out, the others ranked by counting.
 __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(Join a, int batch)
 {
-    // the candidates taken, the first `count` of them the best so far
-    __shared__ uint64_t taken_key[kMaxContinuations + kJoinThreads];
-    __shared__ uint32_t taken_flat[kMaxContinuations + kJoinThreads];
-    __shared__ int taken;
+    __shared__ Totals<kJoinThreads> of_thread;
+    __shared__ Totals<kWave> maxima;
+    __shared__ Totals<kMaxContinuations> kept;
+    __shared__ Totals<kJoinBlock + kMaxBeams> taken;
+    __shared__ double norm[kMaxBeams];  // of each beam: what its logits are less
+    __shared__ float score[kMaxBeams];  // -infinity: takes no part
+    __shared__ int taken_count;
     __shared__ uint64_t bound_key;
     __shared__ uint32_t bound_flat;
-    extern __shared__ uint64_t lds[];
-    double *norm = reinterpret_cast<double *>(lds);  // of each beam: what its logits are less
-    const int tid = (int)threadIdx.x;
+    const int tid = (int)threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const float none = -__builtin_inff();
+    const Total nothing{0ull, ~0u};
+    const int lists = a.beams * a.parts;
+    const int64_t all = (int64_t)lists * a.count;
 
     for (int64_t b = blockIdx.x; b < batch; b += kMaxGridX) {
-        // a wave per beam: log of the sum over its parts
-        for (int beam = tid / kWave; beam < a.beams; beam += kJoinThreads / kWave) {
+        // the first block's candidates are on their way while the sums are formed
+        uint64_t c[kJoinHeld];
+        auto load = [&](int64_t base) {
+#pragma unroll
+            for (int i = 0; i < kJoinHeld; ++i) {
+                const int64_t at = base + i * kJoinThreads + tid;
+                c[i] = at < all ? a.best[b * all + at] : 0ull;
+            }
+        };
+        load(0);
+        for (int beam = wave; beam < a.beams; beam += kJoinWaves) {
             const int64_t row = b * a.beams + beam;
-            const int lane = tid % kWave;
-            const float score = a.scores[row];
+            const float s = a.scores[row];
             const bool over = a.finished != nullptr && a.finished[row] != 0;
             double less = 0.0;
-            if (a.normalize && score != none && !over) {
+            if (a.normalize && s != none && !over) {
                 float high = none;
                 for (int p = lane; p < a.parts; p += kWave)
                     high = __builtin_fmaxf(high, a.of_part[row * a.parts + p].top);
@@ -225,88 +324,74 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(Join a, int bat
                     const Part q = a.of_part[row * a.parts + p];
                     sum += q.top == none ? q.sum : q.sum * exp((double)q.top - (double)high);
                 }
-#pragma unroll
-                for (int d = 1; d < kWave; d *= 2) sum += __shfl_xor(sum, d, kWave);
-                less = (double)high + log(sum);
+                less = (double)high + log(team_sum64<kWave>(sum));
             }
-            if (lane == 0) norm[beam] = less;
+            if (lane == 0) norm[beam] = less, score[beam] = over ? none : s;
         }
-        if (tid == 0) taken = 0, bound_key = 0ull, bound_flat = ~0u;
+        int kept_count = 0;
         __syncthreads();
 
-        auto total_of = [&](int beam, uint64_t c) -> Total {
-            if ((uint32_t)(c >> 32) == 0u) return {0ull, ~0u};
-            const double l = (double)logit_of(c);
-            const double score = (double)a.scores[b * a.beams + beam];
-            return {key_of(score + (l - norm[beam])), (uint32_t)(beam * a.vocab + token_of(c))};
-        };
-        // list i: part i % parts of beam i / parts, its best first; the last `beams`
-        // lists hold a finished beam's only continuation
-        const int lists = a.beams * a.parts;
-        auto candidate = [&](int list, int k) -> Total {
-            if (list >= lists) {
-                const int beam = list - lists;
-                const int64_t row = b * a.beams + beam;
-                const float score = a.scores[row];
-                if (k > 0 || a.finished == nullptr || a.finished[row] == 0 || score == none) return {0ull, ~0u};
-                return {key_of((double)score), (uint32_t)(beam * a.vocab + a.end_id)};
-            }
-            const int beam = list / a.parts;
-            const int64_t row = b * a.beams + beam;
-            if (a.scores[row] == none || (a.finished != nullptr && a.finished[row] != 0)) return {0ull, ~0u};
-            return total_of(beam, a.best[(b * lists + list) * a.count + k]);
-        };
-
-        // The best of every list first: the `count`-th of them bounds what the others have
-        // to beat.  Then the rest, every list's k-th before any list's next, in blocks of
-        // as many as the workgroup has threads.  What is not better than the bound so far
-        // is left out; a block of which nothing is taken, and in which every list stood,
-        // is the last, since lists get worse.
-        const int everything = lists + (a.finished != nullptr ? a.beams : 0);
-        const int64_t all = (int64_t)everything * a.count;
-        for (int64_t from = 0; from < all;) {
-            const int64_t to = from < everything ? everything : all;
-            const int64_t at = from + tid;
-            Total t{0ull, ~0u};
-            if (at < to) t = candidate((int)(at % everything), (int)(at / everything));
-            const bool takes = t.key != 0ull && better(t, Total{bound_key, bound_flat});
-            if (takes) {
-                const int slot = atomicAdd(&taken, 1);
-                taken_key[slot] = t.key, taken_flat[slot] = t.flat;
-            }
-            const int more = __syncthreads_or(takes);
-            if (!more && from >= everything && everything <= kJoinThreads) break;
-            from = from + kJoinThreads < to ? from + kJoinThreads : to;
-            if (!more) continue;
-            const int n = taken;
-            Total mine[2];  // ranked by counting, at most two a thread
-            int before[2] = {0, 0};
+        for (int64_t base = 0; base == 0 || base < all; base += kJoinBlock) {
+            if (base > 0) load(base);
+            if (tid == 0) taken_count = 0, bound_key = 0ull, bound_flat = ~0u;
+            Total t[kJoinHeld + 1];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int slot = tid + i * kJoinThreads;
-                mine[i] = slot < n ? Total{taken_key[slot], taken_flat[slot]} : Total{0ull, ~0u};
+            for (int i = 0; i < kJoinHeld; ++i) {
+                const int64_t at = base + i * kJoinThreads + tid;
+                t[i] = nothing;
+                if (at >= all || (uint32_t)(c[i] >> 32) == 0u) continue;
+                const int beam = (int)(at / ((int64_t)a.parts * a.count));
+                if (score[beam] == none) continue;  // (what is there was left by another call)
+                t[i] = {key_of((double)score[beam] + ((double)logit_of(c[i]) - norm[beam])),
+                        (uint32_t)(beam * a.vocab + token_of(c[i]))};
             }
-            if (tid < n)
-                for (int o = 0; o < n; ++o) {
-                    const Total other{taken_key[o], taken_flat[o]};
-                    before[0] += better(other, mine[0]);
-                    before[1] += better(other, mine[1]);
-                }
+            // with the first block finished beams, with later ones the best so far
+            t[kJoinHeld] = nothing;
+            if (base > 0) {
+                if (tid < kept_count) t[kJoinHeld] = kept.at(tid);
+            } else if (tid < a.beams && a.finished != nullptr) {
+                const int64_t row = b * a.beams + tid;
+                const float s = a.scores[row];
+                if (a.finished[row] != 0 && s != none)
+                    t[kJoinHeld] = {key_of((double)s), (uint32_t)(tid * a.vocab + a.end_id)};
+            }
+            Total mine = t[0];
+#pragma unroll
+            for (int i = 1; i <= kJoinHeld; ++i)
+                if (better(t[i], mine)) mine = t[i];
+            of_thread.set(tid, mine);
             __syncthreads();
+            if (tid < kWave) {
+                for (int w = 1; w < kJoinWaves; ++w)
+                    if (better(of_thread.at(w * kWave + tid), mine)) mine = of_thread.at(w * kWave + tid);
+                maxima.set(tid, mine);
+            }
+            __syncthreads();
+            {
+                // (of fewer than `count` there is none at that place, and all are taken)
+                const int i = tid / kRankLanes;
+                const int before = maxima.before(i, kWave);
+                if (tid % kRankLanes == 0 && before == a.count - 1) bound_key = maxima.key[i], bound_flat = maxima.flat[i];
+            }
+            __syncthreads();
+            const Total bound{bound_key, bound_flat};
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (tid + i * kJoinThreads < n && before[i] < a.count) {
-                    taken_key[before[i]] = mine[i].key, taken_flat[before[i]] = mine[i].flat;
-                    if (before[i] == a.count - 1) bound_key = mine[i].key, bound_flat = mine[i].flat;
-                }
-            if (tid == 0) taken = n < a.count ? n : a.count;
+            for (int i = 0; i <= kJoinHeld; ++i)
+                if (t[i].key != 0ull && !better(bound, t[i])) taken.set(atomicAdd(&taken_count, 1), t[i]);
+            __syncthreads();
+            const int n = taken_count;
+            for (int i = tid / kRankLanes; i < n; i += kRanked) {
+                const int before = taken.before(i, n);
+                if (tid % kRankLanes == 0 && before < a.count) kept.set(before, taken.at(i));
+            }
+            kept_count = n < a.count ? n : a.count;
             __syncthreads();
         }
         for (int k = tid; k < a.count; k += kJoinThreads) {
             const int64_t at = b * a.count + k;
-            const bool there = k < taken;
-            const uint32_t flat = there ? taken_flat[k] : 0u;
-            a.out_scores[at] = there ? (float)value_of(taken_key[k]) : none;
+            const bool there = k < kept_count;
+            const uint32_t flat = there ? kept.flat[k] : 0u;
+            a.out_scores[at] = there ? (float)value_of(kept.key[k]) : none;
             a.parents[at] = there ? (int32_t)(flat / (uint32_t)a.vocab) : -1;
             const int token = there ? (int)(flat % (uint32_t)a.vocab) : -1;
             if (a.wide_ids)

@@ -143,6 +143,19 @@ __device__ __forceinline__ float element(u32x4 r, int e)
     }
 }
 
+// The vector with element e replaced.
+template <typename T>
+__device__ __forceinline__ u32x4 with_element(u32x4 r, int e, float v)
+{
+    if constexpr (sizeof(T) == 4) {
+        r[e] = __builtin_bit_cast(uint32_t, v);
+    } else {
+        const uint32_t h = __builtin_bit_cast(uint16_t, (T)v);
+        r[e / 2] = e & 1 ? (r[e / 2] & 0xFFFFu) | h << 16 : (r[e / 2] & 0xFFFF0000u) | h;
+    }
+    return r;
+}
+
 // float32 values rounded once, to nearest even, to a vector of T.
 template <typename T>
 __device__ __forceinline__ u32x4 pack(const float (&v)[kVec<T>])
