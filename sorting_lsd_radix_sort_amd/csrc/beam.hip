@@ -65,7 +65,8 @@ lrs_status beam_entry(void *d_temp, size_t *temp_bytes, lrs_row_type type, const
     if (rows > 0) {
         const Scan scan{d_scores, d_finished, (uint64_t *)temp, (Part *)(temp + s.best_bytes), (int)rows, (int)vocab,
                         (int)s.parts, (int)count};
-        const unsigned grid = (unsigned)std::min(rows * s.parts, kMaxGridX);
+        const int64_t jobs = rows * s.parts;
+        const dim3 grid((unsigned)std::min(jobs, kMaxGridX), (unsigned)((jobs + kMaxGridX - 1) / kMaxGridX));
         const lrs_status done = with_type(type, [&](auto elem) {
             using T = decltype(elem);
             with_bool(normalize != 0, [&](auto sum) {

@@ -10,9 +10,10 @@
 
 namespace lrs_choose {
 
-constexpr int kScanThreads = 512, kScanWaves = kScanThreads / kWave;
+constexpr int kScanThreads = 256, kScanWaves = kScanThreads / kWave;
 constexpr int kMaxContinuations = 64, kMaxBeams = 1024;  // of one search
 constexpr int kListed = kScanWaves * kMaxContinuations;  // candidates that a part collects
+constexpr int kQueued = 512;                             // vectors in which there are some
 constexpr int kHeld = 2 * kWave;                         // and that a wave holds among ties
 
 // A candidate is its logit's order key above the complement of its token: larger is
@@ -25,13 +26,16 @@ __device__ __forceinline__ uint64_t candidate_of(float l, int token)
 __device__ __forceinline__ float logit_of(uint64_t c) { return value_of((uint32_t)(c >> 32)); }
 __device__ __forceinline__ int token_of(uint64_t c) { return (int)~(uint32_t)c; }
 
-// What is left of a part of a row beside its best candidates: the largest logit and the
-// sum of exp(l - top).
+// What is left of a part of a row beside its best candidates: the sum of its exp(l) is
+// sum * exp(base).
 struct Part {
-    double sum;
-    float top;
-    float pad;
+    double sum, base;
 };
+
+// 2^(l * kLog2e) is exp(l * (1 - kLog2eLess)): log2(e) rounded to float32, and what that
+// takes from an exponent.
+constexpr float kLog2e = 1.44269504f;
+constexpr double kLn2 = 0.693147180559945309417, kLog2eLess = 1.0 - (double)kLog2e * kLn2;
 
 // Of the first `n` <= kHeld candidates of a wave keeps the `count` best, in order, and
 // returns how many these are.
@@ -62,10 +66,11 @@ struct Scan {
 
 // A workgroup takes a part of a row, R vectors a lane, which it reads once and keeps in
 // registers: first the lanes' maxima; then, with the largest of them known, (SUM) the
-// part's sum of exponentials and the logits that are candidates.  A bound for these:
+// part's sum of exponentials and the vectors that hold candidates.  A bound for these:
 // the `count`-th largest of 64 maxima, each over an equal share of the part, so that
-// some `count` ln(64 / (64 - count)) / (count / 64) logits reach it (18 for 16).
-// (Where ties make them too many, a wave keeps its best in a list of its own.)
+// some 64 ln(64 / (64 - count)) logits reach it (18 for 16, above that the more).  Their
+// vectors are queued in LDS and taken apart there, a logit a thread.  (Where ties make
+// them too many, a wave keeps its best in a list of its own.)
 template <typename T, bool SUM, int R>
 __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const T *__restrict__ logits, int64_t ld, Scan a)
 {
@@ -73,160 +78,199 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const T *__rest
     constexpr int64_t PART = (int64_t)kScanThreads * VEC * R;
     __shared__ uint32_t maxima[kScanWaves][kWave];
     __shared__ uint64_t list[kListed];
-    __shared__ uint64_t of_wave[kScanWaves][kHeld];
+    __shared__ union {
+        struct {
+            u32x4 vector[kQueued];
+            int token[kQueued];
+        } queue;
+        uint64_t of_wave[kScanWaves][kHeld];
+    } held_all;
     __shared__ double sums[kScanWaves];
     __shared__ uint32_t bound, largest;
-    __shared__ int listed;
+    __shared__ int listed, queued;
     const int tid = (int)threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const float none = -__builtin_inff();
 
-    const int64_t jobs = (int64_t)a.rows * a.parts;
-    for (int64_t job = blockIdx.x; job < jobs; job += kMaxGridX) {
-        const int row_at = (int)(job / a.parts);
-        // (64 bits: a place past the end of a vocabulary of 2^31 - 1 is no int)
-        const int64_t from = job % a.parts * PART;
-        const float score = a.scores[row_at];
-        if (score == none || (a.finished != nullptr && a.finished[row_at] != 0)) continue;
-        const T *row = logits + row_at * ld;
+    const int64_t job = blockIdx.y * kMaxGridX + blockIdx.x;
+    if (job >= (int64_t)a.rows * a.parts) return;
+    const int row_at = (int)(job / a.parts);
+    // (64 bits: a place past the end of a vocabulary of 2^31 - 1 is no int)
+    const int64_t from = job % a.parts * PART;
+    const float score = a.scores[row_at];
+    if (score == none || (a.finished != nullptr && a.finished[row_at] != 0)) return;
+    const T *row = logits + row_at * ld;
 
-        u32x4 r[R];
-        if (from + PART <= a.vocab) {
+    u32x4 r[R];
+    if (from + PART <= a.vocab) {
 #pragma unroll
-            for (int j = 0; j < R; ++j)
-                r[j] = __builtin_nontemporal_load(
-                    reinterpret_cast<const u32x4_any *>(row + from + (int64_t)(j * kScanThreads + tid) * VEC));
-        } else {  // the last part: -infinity behind the end
+        for (int j = 0; j < R; ++j)
+            r[j] = __builtin_nontemporal_load(
+                reinterpret_cast<const u32x4_any *>(row + from + (int64_t)(j * kScanThreads + tid) * VEC));
+    } else if (a.vocab >= VEC) {
+        // the last part: what ends behind the row is loaded from its end, and shifted
+        // into place before -infinity
 #pragma unroll
-            for (int j = 0; j < R; ++j)
-                r[j] = issue<T, true>(row, col_of<T>(a.vocab, from + (int64_t)(j * kScanThreads + tid) * VEC));
+        for (int j = 0; j < R; ++j) {
+            const int64_t c = from + (int64_t)(j * kScanThreads + tid) * VEC;
+            r[j] = __builtin_nontemporal_load(
+                reinterpret_cast<const u32x4_any *>(row + (c < a.vocab - VEC ? c : a.vocab - VEC)));
+        }
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            __builtin_amdgcn_sched_barrier(0);
+            const int64_t back = from + (int64_t)(j * kScanThreads + tid + 1) * VEC - a.vocab;
+            if (back <= 0) continue;
+            r[j] = shift_down<T>(r[j], back < VEC ? (int)back : 0);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (i + back >= VEC) r[j] = with_element<T>(r[j], i, none);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    } else {
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                r[j] = with_element<T>(r[j], i, j == 0 && tid == 0 && i < a.vocab ? (float)row[i] : none);
+    }
+    float most[R], of_lane = none;
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        most[j] = element<T>(r[j], 0);
+#pragma unroll
+        for (int i = 1; i < VEC; ++i) most[j] = __builtin_fmaxf(most[j], element<T>(r[j], i));
+        of_lane = __builtin_fmaxf(of_lane, most[j]);
+    }
+    maxima[wave][lane] = key_of(of_lane);
+    if (tid == 0) listed = 0, queued = 0;
+    __syncthreads();
+    if (wave == 0) {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int w = 0; w < kScanWaves; ++w) m = maxima[w][lane] > m ? maxima[w][lane] : m;
+        // the upper half of the count-th largest key, bit by bit
+        uint32_t key = 0u;
+#pragma unroll
+        for (int bit = 15; bit >= 0; --bit) {
+            const uint32_t trial = key | 1u << bit;
+            if (__builtin_popcountll(__builtin_amdgcn_ballot_w64(m >> 16 >= trial)) >= a.count) key = trial;
+        }
+        const uint32_t top = team_max<kWave>(m);
+        if (lane == 0) bound = key == 0u ? 1u : key << 16, largest = top;
+    }
+    __syncthreads();
+    // (the logits that were taken apart are not kept: registers are better used by more
+    // waves)
+    auto forget = [&] {
+#pragma unroll
+        for (int j = 0; j < R; ++j) asm("" : "+v"(r[j]));
+    };
+    forget();
+    const uint32_t least_key = bound;
+    const float least = least_key == 1u ? -3.402823466e38f : value_of(least_key);
+    const float top = value_of(largest);
+
+    if constexpr (SUM) {
+        double sum = 0.0;
+        auto add = [&](auto &&exponent) {
 #pragma unroll
             for (int j = 0; j < R; ++j) {
-                const Col col = col_of<T>(a.vocab, from + (int64_t)(j * kScanThreads + tid) * VEC);
-                r[j] = settle<T>(r[j], col);
+                u32x4 v = r[j];
+                asm("" : "+v"(v));
+                float e[VEC];
 #pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    if (i >= col.valid) r[j] = with_element<T>(r[j], i, none);
+                for (int i = 0; i < VEC; ++i) e[i] = __builtin_amdgcn_exp2f(exponent(element<T>(v, i)));
+#pragma unroll
+                for (int n = VEC / 2; n > 0; n /= 2)
+#pragma unroll
+                    for (int i = 0; i < n; ++i) e[i] += e[i + n];
+                sum += (double)e[0];
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        if (__builtin_fabsf(top) < 1e38f) {
+            const float base = -(top * kLog2e);
+            add([&](float l) { return __builtin_fmaf(l, kLog2e, base); });
+        } else {  // large ones, infinities, nothing at all; NaN shows
+            add([&](float l) { return l == none ? none : (l - top) * kLog2e; });
+        }
+        sum = team_sum64<kWave>(sum);
+        if (lane == 0) sums[wave] = sum;
+        forget();
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        const bool has = most[j] >= least;
+        const uint64_t those = __builtin_amdgcn_ballot_w64(has);
+        if (those == 0ull) continue;
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&queued, __builtin_popcountll(those));
+        at = __builtin_amdgcn_readfirstlane(at) + __builtin_popcountll(those & ((1ull << lane) - 1));
+        if (has && at < kQueued) {
+            held_all.queue.vector[at] = r[j];
+            held_all.queue.token[at] = (int)from + (j * kScanThreads + tid) * VEC;
+        }
+    }
+    __syncthreads();
+    const int vectors = queued;
+    if (vectors <= kQueued)
+        for (int at = tid; at < vectors * VEC; at += kScanThreads) {
+            const T *v = reinterpret_cast<const T *>(&held_all.queue.vector[at / VEC]);
+            const float l = (float)v[at % VEC];
+            if (l >= least) {
+                const int to = atomicAdd(&listed, 1);
+                if (to < kListed) list[to] = candidate_of(l, held_all.queue.token[at / VEC] + at % VEC);
             }
         }
-        float most[R], of_lane = none;
+    __syncthreads();
+    int n = listed;
+    if (vectors > kQueued || n > kListed) {
+        forget();
+        uint64_t *held = held_all.of_wave[wave];
+        uint64_t above = 0ull;
+        n = 0;
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            most[j] = element<T>(r[j], 0);
-#pragma unroll
-            for (int i = 1; i < VEC; ++i) most[j] = __builtin_fmaxf(most[j], element<T>(r[j], i));
-            of_lane = __builtin_fmaxf(of_lane, most[j]);
-        }
-        maxima[wave][lane] = key_of(of_lane);
-        if (tid == 0) listed = 0;
-        __syncthreads();
-        if (wave == 0) {
-            uint32_t m = 0u;
-#pragma unroll
-            for (int w = 0; w < kScanWaves; ++w) m = maxima[w][lane] > m ? maxima[w][lane] : m;
-            // the upper half of the count-th largest key, bit by bit
-            uint32_t key = 0u;
-#pragma unroll
-            for (int bit = 15; bit >= 0; --bit) {
-                const uint32_t trial = key | 1u << bit;
-                if (__builtin_popcountll(__builtin_amdgcn_ballot_w64(m >> 16 >= trial)) >= a.count) key = trial;
-            }
-            const uint32_t top = team_max<kWave>(m);
-            if (lane == 0) bound = key == 0u ? 1u : key << 16, largest = top;
-        }
-        __syncthreads();
-        const uint32_t least_key = bound;
-        const float least = least_key == 1u ? -3.402823466e38f : value_of(least_key);
-        const float top = value_of(largest);
-
-        if constexpr (SUM) {
-            double sum = 0.0;
-            if (largest != 0u) {
-#pragma unroll
-                for (int j = 0; j < R; ++j) {
-                    float e[VEC];
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        e[i] = __builtin_amdgcn_exp2f((element<T>(r[j], i) - top) * 1.44269504f);
-#pragma unroll
-                    for (int n = VEC / 2; n > 0; n /= 2)
-#pragma unroll
-                        for (int i = 0; i < n; ++i) e[i] += e[i + n];
-                    sum += (double)e[0];
-                }
-            } else {  // nothing but -infinity, or NaN, which shows
-#pragma unroll
-                for (int j = 0; j < R; ++j)
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        const float l = element<T>(r[j], i);
-                        sum += l != l ? (double)l : 0.0;
-                    }
-            }
-            sum = team_sum64<kWave>(sum);
-            if (lane == 0) sums[wave] = sum;
-        }
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            if (__builtin_amdgcn_ballot_w64(most[j] >= least) == 0ull) continue;
             const int token = (int)from + (j * kScanThreads + tid) * VEC;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 const float l = element<T>(r[j], i);
-                if (l >= least) {
-                    const int at = atomicAdd(&listed, 1);
-                    if (at < kListed) list[at] = candidate_of(l, token + i);
+                const uint64_t c = candidate_of(l, token + i);
+                bool takes = l >= least && c > above;
+                uint64_t all = __builtin_amdgcn_ballot_w64(takes);
+                if (all == 0ull) continue;
+                if (n + __builtin_popcountll(all) > kHeld) {
+                    n = keep_best(held, n, a.count, lane);
+                    if (n == a.count) above = held[n - 1];
+                    takes = takes && c > above;
+                    all = __builtin_amdgcn_ballot_w64(takes);
                 }
+                if (takes) held[n + __builtin_popcountll(all & ((1ull << lane) - 1))] = c;
+                n += __builtin_popcountll(all);
             }
         }
-        __syncthreads();
-        int n = listed;
-        if (n > kListed) {
-            uint64_t *held = of_wave[wave];
-            uint64_t above = 0ull;
-            n = 0;
-#pragma unroll
-            for (int j = 0; j < R; ++j) {
-                const int token = (int)from + (j * kScanThreads + tid) * VEC;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float l = element<T>(r[j], i);
-                    const uint64_t c = candidate_of(l, token + i);
-                    bool takes = l >= least && c > above;
-                    uint64_t all = __builtin_amdgcn_ballot_w64(takes);
-                    if (all == 0ull) continue;
-                    if (n + __builtin_popcountll(all) > kHeld) {
-                        n = keep_best(held, n, a.count, lane);
-                        if (n == a.count) above = held[n - 1];
-                        takes = takes && c > above;
-                        all = __builtin_amdgcn_ballot_w64(takes);
-                    }
-                    if (takes) held[n + __builtin_popcountll(all & ((1ull << lane) - 1))] = c;
-                    n += __builtin_popcountll(all);
-                }
-            }
-            n = keep_best(held, n, a.count, lane);
-            if (lane < a.count) list[wave * a.count + lane] = lane < n ? held[lane] : 0ull;
-            n = kScanWaves * a.count;
-            __syncthreads();
-        }
-        // each candidate's place, by counting those that are better
-        uint64_t *best = a.best + job * a.count;
-        if (tid < n) {
-            const uint64_t mine = list[tid];
-            int before = 0;
-            for (int i = 0; i < n; ++i) before += list[i] > mine;
-            if (mine != 0ull && before < a.count) best[before] = mine;
-        }
-        if (n < a.count && tid >= n && tid < a.count) best[tid] = 0ull;
-        if constexpr (SUM)
-            if (tid == 0) {
-                double sum = 0.0;
-                for (int w = 0; w < kScanWaves; ++w) sum += sums[w];
-                a.of_part[job] = Part{sum, top, 0.0f};
-            }
+        n = keep_best(held, n, a.count, lane);
+        if (lane < a.count) list[wave * a.count + lane] = lane < n ? held[lane] : 0ull;
+        n = kScanWaves * a.count;
         __syncthreads();
     }
+    // each candidate's place, by counting those that are better
+    uint64_t *best = a.best + job * a.count;
+    if (tid < n) {
+        const uint64_t mine = list[tid];
+        int before = 0;
+        for (int i = 0; i < n; ++i) before += list[i] > mine;
+        if (mine != 0ull && before < a.count) best[before] = mine;
+    }
+    if (n < a.count && tid >= n && tid < a.count) best[tid] = 0ull;
+    if constexpr (SUM)
+        if (tid == 0) {
+            double sum = 0.0;
+            for (int w = 0; w < kScanWaves; ++w) sum += sums[w];
+            const double base = (double)-(top * kLog2e);
+            a.of_part[job] = Part{sum, __builtin_fabsf(top) < 1e38f ? (double)top * kLog2eLess - base * kLn2 : (double)top};
+        }
 }
 
 // -------------------------------------------------------------------- joining
@@ -314,17 +358,17 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(Join a, int bat
             const bool over = a.finished != nullptr && a.finished[row] != 0;
             double less = 0.0;
             if (a.normalize && s != none && !over) {
-                float high = none;
+                double high = (double)none;
                 for (int p = lane; p < a.parts; p += kWave)
-                    high = __builtin_fmaxf(high, a.of_part[row * a.parts + p].top);
+                    high = __builtin_fmax(high, a.of_part[row * a.parts + p].base);
 #pragma unroll
-                for (int d = 1; d < kWave; d *= 2) high = __builtin_fmaxf(high, __shfl_xor(high, d, kWave));
+                for (int d = 1; d < kWave; d *= 2) high = __builtin_fmax(high, __shfl_xor(high, d, kWave));
                 double sum = 0.0;
                 for (int p = lane; p < a.parts; p += kWave) {
                     const Part q = a.of_part[row * a.parts + p];
-                    sum += q.top == none ? q.sum : q.sum * exp((double)q.top - (double)high);
+                    sum += q.base == (double)none ? q.sum : q.sum * exp(q.base - high);
                 }
-                less = (double)high + log(team_sum64<kWave>(sum));
+                less = high + log(team_sum64<kWave>(sum));
             }
             if (lane == 0) norm[beam] = less, score[beam] = over ? none : s;
         }
