@@ -163,33 +163,37 @@ LRS_API lrs_status lrs_beam_reorder(const void *d_in, const lrs_beam_layout *in_
 
     const int word = row_bytes % 4 == 0 ? 4 : row_bytes % 2 == 0 ? 2 : 1;
     Reorder a{};
-    a.parents = d_parents;
-    a.row_bytes = row_bytes;
-    a.vecs = row_bytes / 16 + row_bytes % 16 / word;
+    a.vecs = row_bytes / 16;
+    a.words = (int8_t)(row_bytes % 16 / word);
     a.all_rows = (int)(outer * batch * middle * rows);
     a.rows = (int)rows, a.middle = (int)middle, a.batch = (int)batch, a.beams = (int)beams, a.count = (int)count;
-    while ((1 << a.tx_log2) < kThreads && (1 << a.tx_log2) < a.vecs) ++a.tx_log2;
+    const int64_t lanes = std::max<int64_t>(a.vecs, a.words);
+    while ((1 << a.tx_log2) < kThreads && (1 << a.tx_log2) < lanes) ++a.tx_log2;
     a.in_place = in_place;
-    const Places src{in_layout->outer_step, in_layout->batch_step, in_layout->beam_step, in_layout->middle_step,
-                     in_layout->row_step};
-    const Places dst{out_layout->outer_step, out_layout->batch_step, out_layout->beam_step, out_layout->middle_step,
-                     out_layout->row_step};
-    const int64_t col_tiles = (a.vecs + (1 << a.tx_log2) - 1) >> a.tx_log2;
+    // (the kernel loads some state for every place and drops what no parent names: without
+    // beams before the step there is none, and it loads from the new ones)
+    const lrs_beam_layout &il = beams > 0 ? *in_layout : *out_layout, &ol = *out_layout;
+    const char *in_at = (const char *)(beams > 0 ? d_in : d_out);
+    const Places src{il.outer_step, il.batch_step, il.beam_step, il.middle_step, il.row_step};
+    const Places dst{ol.outer_step, ol.batch_step, ol.beam_step, ol.middle_step, ol.row_step};
+    a.tiles = (a.vecs + (1 << a.tx_log2) - 1) >> a.tx_log2;
+    const int64_t col_tiles = a.tiles + (a.words > 0);
     const int64_t row_tiles = (a.all_rows + (kThreads >> a.tx_log2) - 1) / (kThreads >> a.tx_log2);
-    const dim3 grid((unsigned)std::min(col_tiles, kMaxGridX), (unsigned)std::min(row_tiles, kMaxGridY));
+    const dim3 grid((unsigned)std::min(col_tiles, kMaxGridX), (unsigned)std::min(row_tiles, kMaxGridY),
+                    (unsigned)((row_tiles + kMaxGridY - 1) / kMaxGridY));
     auto run = [&](auto w, auto most) {
         with_bool((1 << a.tx_log2) >= kWave, [&](auto wave) {
-            reorder_kernel<w.value, most.value, wave.value>
-                <<<grid, kThreads, 0, stream>>>((const char *)d_in, (char *)d_out, src, dst, a);
+            reorder_kernel<decltype(w), most.value, wave.value>
+                <<<grid, kThreads, 0, stream>>>(in_at, (char *)d_out, d_parents, src, dst, a);
         });
     };
     auto with_word = [&](auto most) {
         if (word == 4)
-            run(std::integral_constant<int, 4>{}, most);
+            run(Word4{}, most);
         else if (word == 2)
-            run(std::integral_constant<int, 2>{}, most);
+            run(Word2{}, most);
         else
-            run(std::integral_constant<int, 1>{}, most);
+            run(Word1{}, most);
     };
     if (count <= 4)
         with_word(std::integral_constant<int, 4>{});

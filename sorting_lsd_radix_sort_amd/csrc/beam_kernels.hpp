@@ -454,70 +454,87 @@ struct Places {
 };
 
 struct Reorder {
-    const int32_t *parents;
-    int64_t row_bytes, vecs;  // vecs: columns of a row
-    int all_rows, rows, middle, batch, beams, count, tx_log2;
+    int64_t vecs, tiles;  // whole vectors of a row, and of these the tiles
+    int all_rows, rows, middle, batch, beams, count;
+    int8_t words, tx_log2;  // words behind a row's vectors
     bool in_place;
 };
 
-typedef uint32_t u32x4_byte __attribute__((ext_vector_type(4), aligned(1)));
-typedef uint32_t u32_byte __attribute__((aligned(1)));
-typedef uint16_t u16_byte __attribute__((aligned(1)));
+// What is moved at once, at any address.
+struct Vector {
+    typedef uint32_t type __attribute__((ext_vector_type(4), aligned(1)));
+};
+struct Word4 {
+    typedef uint32_t type __attribute__((aligned(1)));
+};
+struct Word2 {
+    typedef uint16_t type __attribute__((aligned(1)));
+};
+struct Word1 {
+    typedef uint8_t type;
+};
 
 // A lane moves one column, of 16 bytes or (at a row's end) of one word, of all beams of
 // a search: it has read what it needs of the old states before it stores the first of
-// the new ones, so they may be the same memory.
+// the new ones, so they may be the same memory.  in and out are the same for the whole
+// wave, `at` is the lane's; parents too, where a wave serves one row.
 template <typename W, int MOST>
-__device__ __forceinline__ void move_column(const char *in, char *out, const Places &from, const Places &to,
+__device__ __forceinline__ void move_column(const char *in, int64_t in_step, char *out, int64_t out_step, uint32_t at,
                                             const int32_t *parents, int beams, int count, bool in_place)
 {
-    W v[MOST];
+    using T = typename W::type;
+    int p[MOST];  // all of them first: each is a load
 #pragma unroll
-    for (int j = 0; j < MOST; ++j) {
-        v[j] = W{};
-        if (j >= count) continue;
-        const int p = parents[j];
-        if ((uint32_t)p < (uint32_t)beams && !(in_place && p == j))
-            v[j] = *reinterpret_cast<const W *>(in + p * from.beam_step);
-    }
+    for (int j = 0; j < MOST; ++j) p[j] = parents[j < count ? j : 0];
+    // a beam whose state is not needed (its own parent in place, no parent at all) loads
+    // another's again, or the first, which is always there: branches between the loads
+    // cost more
+    auto named = [&](int j) { return (uint32_t)p[j] < (uint32_t)beams; };
+    auto stays = [&](int j) { return in_place && p[j] == j && named(j); };
+    int spare = 0;
+#pragma unroll
+    for (int j = MOST - 1; j >= 0; --j) spare = j < count && named(j) && !stays(j) ? p[j] : spare;
+    T v[MOST];
 #pragma unroll
     for (int j = 0; j < MOST; ++j)
-        if (j < count && !(in_place && parents[j] == j)) *reinterpret_cast<W *>(out + j * to.beam_step) = v[j];
+        v[j] = *reinterpret_cast<const T *>(in + (j < count && named(j) && !stays(j) ? p[j] : spare) * in_step + at);
+#pragma unroll
+    for (int j = 0; j < MOST; ++j)
+        if (j < count && !stays(j)) __builtin_nontemporal_store(named(j) ? v[j] : T{}, reinterpret_cast<T *>(out + j * out_step + at));
 }
 
-// WORD: bytes of the words that a row's last columns are moved in; MOST: beams whose
+// WORD: the words that a row's last columns are moved in; MOST: beams whose
 // columns a lane holds at once (more of them one after another, not in place).
-template <int WORD, int MOST, bool WAVE_ROW>
-__global__ __launch_bounds__(kThreads) void reorder_kernel(const char *in, char *out, Places from, Places to, Reorder a)
+template <typename WORD, int MOST, bool WAVE_ROW>
+__global__ __launch_bounds__(kThreads) void reorder_kernel(const char *in, char *out,
+                                                           const int32_t *__restrict__ all_parents, Places from,
+                                                           Places to, Reorder a)
 {
-    for (int64_t tile = blockIdx.y; tile << (kThreadsLog2 - a.tx_log2) < a.all_rows; tile += kMaxGridY) {
-        const int64_t r64 = row_of<WAVE_ROW>(a.tx_log2, tile);
-        if (r64 >= a.all_rows) continue;
-        const uint32_t r = (uint32_t)r64;
-        const uint32_t block = r / (uint32_t)a.rows, row = r % (uint32_t)a.rows;
-        const uint32_t state = block / (uint32_t)a.middle, middle = block % (uint32_t)a.middle;
-        const uint32_t outer = state / (uint32_t)a.batch, b = state % (uint32_t)a.batch;
-        const char *src =
-            in + outer * from.outer_step + b * from.batch_step + middle * from.middle_step + row * from.row_step;
-        char *dst = out + outer * to.outer_step + b * to.batch_step + middle * to.middle_step + row * to.row_step;
-        const int64_t whole = a.row_bytes / 16;
-        for (int64_t x = blockIdx.x; x << a.tx_log2 < a.vecs; x += kMaxGridX) {
-            const int64_t vec = (x << a.tx_log2) + (threadIdx.x & ((1 << a.tx_log2) - 1));
-            if (vec >= a.vecs) continue;
+    const int64_t r64 = row_of<WAVE_ROW>(a.tx_log2, (int64_t)blockIdx.z * kMaxGridY + blockIdx.y);
+    if (r64 >= a.all_rows) return;
+    const uint32_t r = (uint32_t)r64;
+    const uint32_t block = r / (uint32_t)a.rows, row = r % (uint32_t)a.rows;
+    const uint32_t state = block / (uint32_t)a.middle, middle = block % (uint32_t)a.middle;
+    const uint32_t outer = state / (uint32_t)a.batch, b = state % (uint32_t)a.batch;
+    const char *src = in + outer * from.outer_step + b * from.batch_step + middle * from.middle_step + row * from.row_step;
+    char *dst = out + outer * to.outer_step + b * to.batch_step + middle * to.middle_step + row * to.row_step;
+    const int32_t *parents = all_parents + (int64_t)b * a.count;
+    // tiles of vectors, and behind them one of the words that end a row
+    const uint32_t lane = threadIdx.x & ((1u << a.tx_log2) - 1);
 #pragma unroll 1
-            for (int j0 = 0; j0 < a.count; j0 += MOST) {
-                const int32_t *parents = a.parents + (int64_t)b * a.count + j0;
-                const int most = a.count - j0 < MOST ? a.count - j0 : MOST;
-                const int64_t at = vec < whole ? vec * 16 : whole * 16 + (vec - whole) * WORD;
-                char *d = dst + at + j0 * to.beam_step;
-                if (vec < whole)
-                    move_column<u32x4_byte, MOST>(src + at, d, from, to, parents, a.beams, most, a.in_place);
-                else if constexpr (WORD == 4)
-                    move_column<u32_byte, MOST>(src + at, d, from, to, parents, a.beams, most, a.in_place);
-                else if constexpr (WORD == 2)
-                    move_column<u16_byte, MOST>(src + at, d, from, to, parents, a.beams, most, a.in_place);
-                else
-                    move_column<uint8_t, MOST>(src + at, d, from, to, parents, a.beams, most, a.in_place);
+    for (int64_t x = blockIdx.x; x < a.tiles + (a.words > 0); x += kMaxGridX) {
+#pragma unroll 1
+        for (int j = 0; j < a.count; j += MOST) {
+            const int most = a.count - j < MOST ? a.count - j : MOST;
+            if (x < a.tiles) {
+                const int64_t base = x << a.tx_log2;
+                if (base + lane < a.vecs)
+                    move_column<Vector, MOST>(src + base * 16, from.beam_step, dst + base * 16 + j * to.beam_step,
+                                              to.beam_step, lane * 16, parents + j, a.beams, most, a.in_place);
+            } else if (lane < (uint32_t)a.words) {
+                move_column<WORD, MOST>(src + a.vecs * 16, from.beam_step, dst + a.vecs * 16 + j * to.beam_step,
+                                        to.beam_step, lane * (uint32_t)sizeof(typename WORD::type), parents + j, a.beams,
+                                        most, a.in_place);
             }
         }
     }

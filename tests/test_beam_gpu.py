@@ -355,6 +355,14 @@ def test_reorder_in_place_by_count(count):
         want[:, :few] = reordered(states, parents[:, :few].contiguous(), 0)
         lrs.beam_reorder(states, parents[:, :few], out=states[:, :few])
         assert torch.equal(bits(states), want)
+    # more beams afterwards than before, into the memory that begins with them: a place
+    # whose number is no beam is named by none
+    few = max(1, count // 2)
+    for width in (8, 77):
+        buffer = pattern((len(rows), count, width), torch.int16, count)
+        want = reordered(buffer[:, :few], parents, 0)
+        lrs.beam_reorder(buffer[:, :few], parents, out=buffer)
+        assert torch.equal(bits(buffer), want)
     if count == 64:
         with pytest.raises(lrs.LrsError):
             many = pattern((1, 65, 8), torch.int16, 1)
