@@ -40,10 +40,10 @@ void with_team(int64_t experts, F &&f)
 }
 
 template <typename TEAM>
-unsigned team_grid(int64_t tokens)
+dim3 team_grid(int64_t tokens)
 {
-    const int64_t teams = kTeamThreads / TEAM::lanes;
-    return (unsigned)std::min((tokens + teams - 1) / teams, kMaxGridX);
+    const int64_t teams = kTeamThreads / TEAM::lanes, tiles = (tokens + teams - 1) / teams;
+    return dim3((unsigned)std::min(tiles, kMaxGridX), (unsigned)((tiles + kMaxGridX - 1) / kMaxGridX));
 }
 
 bool score_ok(lrs_score_type s) { return s == LRS_SCORE_SOFTMAX || s == LRS_SCORE_SIGMOID; }
@@ -81,16 +81,20 @@ LRS_API lrs_status lrs_route_tokens(lrs_row_type type, const void *d_logits, int
         return LRS_ERR_INVALID_ARG;
     const bool grouped = kept_groups < num_groups;
     const bool top2 = grouped && group_score == LRS_GROUP_TOP2, sums = d_bias != nullptr || top2;
-    const Route a{d_bias, d_ids, d_weights, scale, (int)tokens, (int16_t)experts, (int16_t)(experts / num_groups),
-                  (int16_t)num_groups, (int16_t)kept_groups, (uint8_t)slots, score == LRS_SCORE_SIGMOID, top2,
-                  normalize != 0, id_type == LRS_ID_I64, (uint8_t)weight_type};
+    const int size = (int)(experts / num_groups);
+    Route a{d_bias, d_ids, d_weights, scale, (int)tokens, (int16_t)experts, (int16_t)size, (int16_t)num_groups,
+            (int16_t)kept_groups, (uint8_t)slots, score == LRS_SCORE_SIGMOID, top2, normalize != 0,
+            id_type == LRS_ID_I64, (uint8_t)weight_type, 0};
     // a token's list of the chosen, and its scores and groups where they are needed
-    const int cells = sums ? 8 : grouped ? 4 : 0;
+    const int cells = sums || b == 4 ? 8 : grouped ? 4 : 0;
     const int team_bytes = team_align((slots + 2) * (int64_t)sizeof(Chosen) + cells * (experts + num_groups));
     return with_type(type, [&](auto elem) {
         using T = decltype(elem);
         with_team(experts, [&](auto team) {
             using TEAM = decltype(team);
+            const int lanes = size / kVec<T>;
+            if (size % kVec<T> == 0 && (lanes & (lanes - 1)) == 0 && lanes <= std::min(TEAM::lanes, 16))
+                a.lane_groups = (uint8_t)lanes;
             const unsigned lds = (unsigned)team_bytes * (kTeamThreads / TEAM::lanes);
             with_bool(sums, [&](auto by_sums) {
                 route_kernel<T, TEAM::lanes, TEAM::logits, by_sums.value>

@@ -39,6 +39,7 @@ struct Route {
     int tokens;
     int16_t experts, size, groups, kept;  // size: of a group
     uint8_t slots, sigmoid, top2, normalize, wide_ids, weight_type;
+    uint8_t lane_groups;  // a group is this many lanes' vectors; 0: it is no such number
 };
 
 // A token's list of the chosen, in LDS.
@@ -47,30 +48,77 @@ struct Chosen {
     uint32_t key;
 };
 
-// The choice by float64, for the token whose scores are too close to one another in
-// float32: all of its scores again, from memory to LDS (cells: experts, then groups).
-template <typename T, int L>
+// exp(x) in float64 for any x but NaN: 2^n exp(r) with n the nearest integer to x log2(e)
+// and |r| <= ln(2) / 2, by Taylor's series up to r^13 / 13! (the next term is below
+// 2^-57).
+__device__ __forceinline__ double exp64(double x)
+{
+    x = __builtin_fmin(__builtin_fmax(x, -745.0), 709.0);
+    const double n = __builtin_rint(x * 1.44269504088896340736);
+    // ln(2) in two parts, the first with zeros at its end
+    double r = __builtin_fma(n, -0x1.62e42fefap-1, x);
+    r = __builtin_fma(n, -0x1.cf79abc9e3b39p-40, r);
+    double y = 1.0 / 6227020800.0;
+    constexpr double terms[] = {1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0,
+                                1.0 / 5040.0,      1.0 / 720.0,      1.0 / 120.0,     1.0 / 24.0,     1.0 / 6.0,
+                                0.5,               1.0,              1.0};
+#pragma unroll
+    for (int i = 0; i < 13; ++i) y = __builtin_fma(y, r, terms[i]);
+    return __builtin_ldexp(y, (int)n);
+}
+
+// What an expert of logit l is compared by, in float64, as an order key.  By sums: its
+// score, for the softmax with the maximum and the sum of its token, and its bias; the
+// logit otherwise.
+template <bool SUMS>
+__device__ __forceinline__ uint64_t choice64(const Route &a, float l, float bias, float top, double sum)
+{
+    if (l == -__builtin_inff()) return 0ull;
+    if constexpr (!SUMS) return key_of((double)l);
+    if (bias == -__builtin_inff()) return 0ull;
+    double s;
+    if (a.sigmoid)
+        s = l != l ? (double)l : 1.0 / (1.0 + exp64(-(double)l));
+    else
+        s = sum != sum ? sum : exp64((double)l - (double)top) / sum;
+    return key_of(s + (double)bias);
+}
+
+// The softmax's sum in float64, from memory.
+template <typename T, int L, int V>
+__device__ __forceinline__ double sum64(const T *row, const Route &a, int lane, float top)
+{
+    if (a.sigmoid) return 1.0;
+    double sum = 0.0;
+#pragma unroll 4
+    for (int i = 0; i < V; ++i) {
+        const int e = i * L + lane;
+        const float l = e < a.experts ? load_logit(row, e) : -__builtin_inff();
+        const double x = (double)l - (double)top;
+        sum += l == -__builtin_inff() ? 0.0 : x != x ? x : exp64(x);
+    }
+    return team_sum64<L>(sum);
+}
+
+// The choice by float64 throughout, for the token whose scores are too close to one
+// another in float32 (or hold NaN or infinity): all of them again, from memory to LDS
+// (cells: experts, then groups).
+template <typename T, int L, int V, bool SUMS>
 __device__ void choose_in_64(const T *row, const Route &a, int lane, float top, uint64_t *cells, Chosen *list)
 {
-    double sum = 1.0;
-    if (!a.sigmoid) {
-        sum = 0.0;
-        for (int e = lane; e < a.experts; e += L) {
-            const float l = load_logit(row, e);
-            sum += l == -__builtin_inff() ? 0.0 : exp((double)l - (double)top);
-        }
-        sum = team_sum64<L>(sum);
-    }
-    for (int e = lane; e < a.experts; e += L) {
-        const float l = load_logit(row, e), b = a.bias != nullptr ? a.bias[e] : 0.0f;
-        const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)top) / sum;
-        cells[e] = l == -__builtin_inff() || b == -__builtin_inff() ? 0ull : key_of(s + (double)b);
+    const double sum = SUMS ? sum64<T, L, V>(row, a, lane, top) : 1.0;
+#pragma unroll 4
+    for (int i = 0; i < V; ++i) {
+        const int e = i * L + lane;
+        if (e < a.experts)
+            cells[e] = choice64<SUMS>(a, load_logit(row, e), SUMS && a.bias != nullptr ? a.bias[e] : 0.0f, top, sum);
     }
     wave_sync();
     if (a.kept < a.groups) {
         uint64_t *of_group = cells + a.experts;
         for (int g = lane; g < a.groups; g += L) {
             uint64_t first = 0, second = 0;
+#pragma unroll 4
             for (int i = 0; i < a.size; ++i) {
                 const uint64_t k = cells[g * a.size + i];
                 second = k > first ? first : k > second ? k : second;
@@ -90,8 +138,13 @@ __device__ void choose_in_64(const T *row, const Route &a, int lane, float top, 
     for (int k = 0; k < a.slots; ++k) {
         uint64_t best = 0;
         uint32_t at = ~0u;
-        for (int e = lane; e < a.experts; e += L)
-            if (cells[e] > best) best = cells[e], at = (uint32_t)e;
+#pragma unroll 4
+        for (int i = 0; i < V; ++i) {
+            const int e = i * L + lane;
+            const uint64_t c = e < a.experts ? cells[e] : 0ull;
+            at = c > best ? (uint32_t)e : at;
+            best = c > best ? c : best;
+        }
         const uint64_t of_all = team_max64<L>(best);
         at = team_min<L>(best == of_all ? at : ~0u);
         if (of_all != 0 && (int)at % L == lane) cells[at] = 0;
@@ -100,9 +153,77 @@ __device__ void choose_in_64(const T *row, const Route &a, int lane, float top, 
     }
 }
 
+// The first `n` of the list, which are the best n of their token, in the order of
+// float64.
+template <typename T, int L, int V, bool SUMS>
+__device__ void order_in_64(const T *row, const Route &a, int lane, float top, uint64_t *cells, Chosen *list, int n)
+{
+    const double sum = SUMS ? sum64<T, L, V>(row, a, lane, top) : 1.0;
+    for (int k = lane; k < n; k += L) {
+        const int e = list[k].expert;
+        cells[k] = e < 0 ? 0ull
+                         : choice64<SUMS>(a, load_logit(row, e), SUMS && a.bias != nullptr ? a.bias[e] : 0.0f, top, sum);
+    }
+    wave_sync();
+    // (a lane has one or a few of them: it reads them all before any is replaced)
+    int expert[kMaxSlots / 8 + 1], place[kMaxSlots / 8 + 1];
+#pragma unroll
+    for (int i = 0; i < kMaxSlots / L + 1; ++i) {
+        const int k = i * L + lane;
+        if (k >= n) continue;
+        expert[i] = list[k].expert;
+        place[i] = 0;
+        const uint64_t mine = cells[k];
+        for (int o = 0; o < n; ++o)
+            place[i] += cells[o] > mine || (cells[o] == mine && (uint32_t)list[o].expert < (uint32_t)expert[i]) ||
+                        (mine == 0ull && cells[o] == 0ull && o < k);
+    }
+    wave_sync();
+#pragma unroll
+    for (int i = 0; i < kMaxSlots / L + 1; ++i)
+        if (i * L + lane < n) list[place[i]].expert = expert[i];
+    wave_sync();
+}
+
+// The bits of an order key that follow from a 16-bit logit's others: zeros, or ones where
+// it is negative.
+constexpr uint32_t kFree = 0x1FFFu;
+
+__device__ __forceinline__ float logit_of_key(uint32_t k)
+{
+    return value_of(k & 0x80000000u ? k & ~kFree : k | kFree);
+}
+
+// Sorts a lane's keys, the largest first, by Batcher's odd-even merges.
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&k)[N])
+{
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j <= N - 1 - q; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const uint32_t x = k[i + j], y = k[i + j + q];
+                        k[i + j] = x > y ? x : y;
+                        k[i + j + q] = x > y ? y : x;
+                    }
+}
+
 // The choice of `slots` experts per token, and their weights.  Team of L lanes, V logits a
 // lane.  SUMS: the choice is by sums (a bias, or groups by their two best) and not by the
 // logits themselves.
+//
+// Each lane sorts its keys; then the best of the lanes' first keys is taken off, one after
+// another.  So that a key tells its expert, its last bits are replaced: the 13 that a
+// 16-bit logit leaves free by the expert's id, which changes no order, or the last few
+// bits of float32 by the place within the lane.  These then decide nothing: where two
+// neighbours of the list are closer than that and the sums' rounding, they are ordered by
+// float64, and where the end of the list is not certain either, the choice is made by
+// float64 throughout.
 template <typename T, int L, int V, bool SUMS>
 __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict__ logits, int64_t ld, Route a,
                                                              int team_bytes)
@@ -110,74 +231,132 @@ __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict
     extern __shared__ uint64_t lds[];
     constexpr int VEC = kVec<T>;
     static_assert(V % VEC == 0, "whole vectors");
-    constexpr int kTeams = kTeamThreads / L;
+    constexpr int kTeams = kTeamThreads / L, J = V / VEC;
+    constexpr bool EXACT = !SUMS && sizeof(T) == 2;
     const int lane = (int)threadIdx.x % L, team = (int)threadIdx.x / L;
     Chosen *list = reinterpret_cast<Chosen *>(reinterpret_cast<char *>(lds) + team * team_bytes);
     uint64_t *cells64 = reinterpret_cast<uint64_t *>(list + a.slots + 2);
     uint32_t *cells = reinterpret_cast<uint32_t *>(cells64);
     const float none = -__builtin_inff();
 
-    for (int64_t t = (int64_t)blockIdx.x * kTeams + team; t - team < a.tokens; t += kMaxGridX * kTeams) {
-        const bool live = t < a.tokens;
-        const T *row = logits + (live ? t : 0) * ld;
-        u32x4 raw[V / VEC];
+    const int64_t t = (blockIdx.y * kMaxGridX + blockIdx.x) * kTeams + team;
+    const bool live = t < a.tokens;
+    const T *row = logits + (live ? t : 0) * ld;
+    u32x4 raw[J];
 #pragma unroll
-        for (int j = 0; j < V / VEC; ++j) raw[j] = issue<T>(row, col_of<T>(a.experts, (int64_t)(j * L + lane) * VEC));
-        // element i of a lane is expert (i / VEC * L + lane) * VEC + i % VEC
-        uint32_t key[V];
+    for (int j = 0; j < J; ++j) raw[j] = issue<T>(row, col_of<T>(a.experts, (int64_t)(j * L + lane) * VEC));
+    // element i of a lane is expert (i / VEC * L + lane) * VEC + i % VEC
+    uint32_t key[V];
+    uint32_t best = 0u;
 #pragma unroll
-        for (int j = 0; j < V / VEC; ++j) {
-            const Col col = col_of<T>(a.experts, (int64_t)(j * L + lane) * VEC);
-            const u32x4 r = settle<T>(raw[j], col);
+    for (int j = 0; j < J; ++j) {
+        const Col col = col_of<T>(a.experts, (int64_t)(j * L + lane) * VEC);
+        const u32x4 r = settle<T>(raw[j], col);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) key[j * VEC + i] = live && i < col.valid ? key_of(element<T>(r, i)) : 0u;
+        for (int i = 0; i < VEC; ++i) {
+            const uint32_t k = live && i < col.valid ? key_of(element<T>(r, i)) : 0u;
+            key[j * VEC + i] = k;
+            best = k > best ? k : best;
         }
-        uint32_t local = 0u;
-#pragma unroll
-        for (int i = 0; i < V; ++i) local = key[i] > local ? key[i] : local;
+    }
 
-        // the softmax's maximum and sum over all experts, where they are needed
-        float top = 0.0f, sum = 1.0f;
-        if (!a.sigmoid && (SUMS || !a.normalize)) {
-            const uint32_t best = team_max<L>(local);
-            top = value_of(best);
-            sum = 0.0f;
+    // the softmax's maximum and sum over all experts, where they are needed; the
+    // exponent's product in two parts, so that its rounding is all that is lost
+    float top = 0.0f, sum = 1.0f;
+    if (!a.sigmoid && (SUMS || !a.normalize)) {
+        best = team_max<L>(best);
+        top = value_of(best);
+        sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum += key[i] == 0u ? 0.0f : expf(value_of(key[i]) - top);
-            sum = best == 0u ? 1.0f : team_sum<L>(sum);
+        for (int i = 0; i < V; ++i) {
+            const float d = value_of(key[i]) - top;
+            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(d, 1.44269504f, d * 1.92596303e-8f));
+            sum += key[i] == 0u ? 0.0f : e;
         }
+        sum = best == 0u ? 1.0f : team_sum<L>(sum);
+    }
 
-        // what is compared: the logits, or the scores with their bias, off by at most
-        // `error` (counted below) but for the sum's rounding
-        float error = 0.0f;
-        if constexpr (SUMS) {
-            const float each = 1.0f / sum;
-            error = a.sigmoid ? 8 * 0x1p-24f : 64 * 0x1p-24f * each;
-            local = 0u;
+    // What is compared: the logits, or the scores with their bias, off by at most
+    // `error` but for the sum's own rounding: exponents (2 |d| + 4) 2^-24 relative,
+    // |d| s being at most 0.37 of the largest, a reciprocal, the sum of all.
+    float error = 0.0f;
+    bool close = false;  // too close for float32
+    if constexpr (SUMS) {
+        const float each = 1.0f / sum;
+        error = a.sigmoid ? 8 * 0x1p-24f : 64 * 0x1p-24f * each;
 #pragma unroll
-            for (int j = 0; j < V / VEC; ++j) {
-                const int c = (j * L + lane) * VEC;
+        for (int j = 0; j < J; ++j) {
+            const int c = (j * L + lane) * VEC;
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    uint32_t &k = key[j * VEC + i];
-                    const float l = value_of(k), b = a.bias != nullptr && c + i < a.experts ? a.bias[c + i] : 0.0f;
-                    const float s = a.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top) * each;
-                    k = k == 0u || b == none ? 0u : key_of(s + b);
-                    local = k > local ? k : local;
-                }
+            for (int i = 0; i < VEC; ++i) {
+                uint32_t &k = key[j * VEC + i];
+                const float l = value_of(k), b = a.bias != nullptr && c + i < a.experts ? a.bias[c + i] : 0.0f;
+                const float x = (a.sigmoid ? -l : l - top) * 1.44269504f;
+                const float e = __builtin_amdgcn_exp2f(x);
+                const float sc = (a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + e) : e * each) + b;
+                const bool out = k == 0u || b == none;
+                close |= !out && !(__builtin_fabsf(sc) < __builtin_inff());
+                const uint32_t bits = __builtin_bit_cast(uint32_t, sc + 0.0f);
+                k = out ? 0u : bits ^ ((uint32_t)((int32_t)bits >> 31) | 0x80000000u);
             }
         }
+    }
 
-        bool close = false;  // too close for float32
-        if (a.kept < a.groups) {
-            uint32_t *of_group = cells + a.experts;
+    if (a.kept < a.groups) {
+        uint32_t *of_group = cells + a.experts;
+        float magnitude = 0.0f;  // of what is added up: its rounding counts, not the sum's
+        auto score = [&](uint32_t first, uint32_t second) {
+            if (!a.top2 || second == 0u) return first;
+            const float x = value_of(first), y = value_of(second);
+            magnitude = __builtin_fmaxf(magnitude, __builtin_fabsf(x) + __builtin_fabsf(y));
+            return key_of(x + y);
+        };
+        auto before = [&](uint32_t mine, int g) {
+            int n = 0;
+            for (int o = 0; o < a.groups; ++o) n += of_group[o] > mine || (of_group[o] == mine && o < g);
+            return n;
+        };
+        uint32_t least = ~0u, most = 0u;  // of the kept, of the others
+        if (a.lane_groups != 0) {
+            // a group's vectors lie in neighbouring lanes
+            uint32_t mine[J];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                uint32_t first = key[j * VEC], second = 0u;
+                auto join = [&](uint32_t f, uint32_t s) {
+                    const uint32_t low = f < first ? f : first;
+                    second = s > second ? s : second;
+                    second = low > second ? low : second;
+                    first = f > first ? f : first;
+                };
+#pragma unroll
+                for (int i = 1; i < VEC; ++i) join(key[j * VEC + i], 0u);
+                if (a.lane_groups > 1) join(dpp<0xB1>(first), dpp<0xB1>(second));
+                if (a.lane_groups > 2) join(dpp<0x4E>(first), dpp<0x4E>(second));
+                if (a.lane_groups > 4) join(dpp<0x141>(first), dpp<0x141>(second));
+                if (a.lane_groups > 8) join(dpp<0x140>(first), dpp<0x140>(second));
+                mine[j] = score(first, second);
+                const int g = (j * L + lane) / a.lane_groups;
+                if (g < a.groups && lane % a.lane_groups == 0) of_group[g] = mine[j];
+            }
+            wave_sync();
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int g = (j * L + lane) / a.lane_groups;
+                if (g >= a.groups) continue;
+                const bool stays = before(mine[j], g) < a.kept;
+                least = stays && mine[j] < least ? mine[j] : least;
+                most = !stays && mine[j] > most ? mine[j] : most;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) key[j * VEC + i] = stays ? key[j * VEC + i] : 0u;
+            }
+        } else {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int e = (i / VEC * L + lane) * VEC + i % VEC;
                 if (e < a.experts) cells[e] = key[i];
             }
             wave_sync();
-            float magnitude = 0.0f;  // of what is added up: its rounding counts, not the sum's
             for (int g = lane; g < a.groups; g += L) {
                 uint32_t first = 0u, second = 0u;
                 int i = lane % a.size;  // lanes begin at different banks
@@ -187,17 +366,12 @@ __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict
                     first = k > first ? k : first;
                     i = i + 1 == a.size ? 0 : i + 1;
                 }
-                const float x = value_of(first), y = a.top2 && second != 0u ? value_of(second) : 0.0f;
-                of_group[g] = first == 0u ? 0u : key_of(x + y);
-                if (first != 0u) magnitude = __builtin_fmaxf(magnitude, __builtin_fabsf(x) + __builtin_fabsf(y));
+                of_group[g] = score(first, second);
             }
             wave_sync();
-            uint32_t least = ~0u, most = 0u;  // of the kept, of the others
             for (int g = lane; g < a.groups; g += L) {
                 const uint32_t mine = of_group[g];
-                int before = 0;
-                for (int o = 0; o < a.groups; ++o) before += of_group[o] > mine || (of_group[o] == mine && o < g);
-                if (before < a.kept) {
+                if (before(mine, g) < a.kept) {
                     least = mine < least ? mine : least;
                 } else {
                     most = mine > most ? mine : most;
@@ -205,85 +379,112 @@ __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict
                 }
             }
             wave_sync();
-            if constexpr (SUMS) {
-                const float x = value_of(team_min<L>(least)), y = value_of(team_max<L>(most));
-                close = y != none && !(x - y > 4 * error + team_maxf<L>(magnitude) * 0x1p-22f);
-            }
-            local = 0u;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int e = (i / VEC * L + lane) * VEC + i % VEC;
                 key[i] = e < a.experts ? cells[e] : 0u;
-                local = key[i] > local ? key[i] : local;
             }
         }
-
-        // the best, one after another; by sums one more, to see how far it is
-        const int rounds = a.slots + (SUMS ? 1 : 0);
-        for (int k = 0; k < rounds; ++k) {
-            const uint32_t best = team_max<L>(local);
-            int at = V;  // the lowest of this lane's that has that key
-#pragma unroll
-            for (int i = V - 1; i >= 0; --i) at = key[i] == best ? i : at;
-            const uint32_t mine = at == V ? ~0u : (uint32_t)((at / VEC * L + lane) * VEC + at % VEC);
-            const uint32_t e = team_min<L>(mine);
-            const int gone = mine == e ? at : V;
-            local = 0u;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                key[i] = i == gone ? 0u : key[i];
-                local = key[i] > local ? key[i] : local;
-            }
-            if (lane == 0) list[k] = {best == 0u ? -1 : (int)e, best};
-        }
-        wave_sync();
         if constexpr (SUMS) {
-            for (int k = lane; k < a.slots; k += L) {
-                const float x = value_of(list[k].key), y = value_of(list[k + 1].key);
-                close |= y != none && !(x - y > 2 * error + (__builtin_fabsf(x) + __builtin_fabsf(y)) * 0x1p-23f);
-            }
-            if (team_or<L>(close && live) != 0u) choose_in_64<T, L>(row, a, lane, top, cells64, list);
+            const float x = value_of(team_min<L>(least)), y = value_of(team_max<L>(most));
+            const float size = __builtin_fmaxf(team_maxf<L>(magnitude), __builtin_fabsf(x) + __builtin_fabsf(y));
+            close |= y != none && !(x - y > 4 * error + size * 0x1p-22f);
         }
-
-        // weights: of each chosen logit, by the softmax's or the sigmoid's parts
-        float high = none;
-        for (int k = lane; k < a.slots; k += L) {
-            const int e = list[k].expert;
-            const float l = e < 0 ? none : SUMS ? load_logit(row, e) : value_of(list[k].key);
-            list[k].key = __builtin_bit_cast(uint32_t, l);  // from here on the logit
-            high = __builtin_fmaxf(high, l);
-        }
-        float total = 1.0f;
-        if (a.normalize) {
-            high = team_maxf<L>(high);
-            if (a.sigmoid) high = __builtin_fminf(high, 0.0f);
-            total = 0.0f;
-            for (int k = lane; k < a.slots; k += L)
-                if (list[k].expert >= 0) {
-                    const float l = __builtin_bit_cast(float, list[k].key);
-                    total += a.sigmoid ? sigmoid_above(l, high) : expf(l - high);
-                }
-            total = team_sum<L>(total);
-            if (SUMS && sum != sum) total = sum;  // a NaN that was not chosen itself
-        } else {
-            high = a.sigmoid ? 0.0f : top;
-            total = sum;
-        }
-        if (live)
-            for (int k = lane; k < a.slots; k += L) {
-                const int64_t at = t * a.slots + k;
-                const int e = list[k].expert;
-                if (a.wide_ids)
-                    ((int64_t *)a.ids)[at] = e;
-                else
-                    ((int32_t *)a.ids)[at] = e;
-                if (a.weights == nullptr) continue;
-                const float l = __builtin_bit_cast(float, list[k].key);
-                const float s = a.sigmoid ? sigmoid_above(l, high) : expf(l - high);
-                store_scalar(a.weights, a.weight_type, at, e < 0 ? 0.0f : a.scale * (s / total));
-            }
-        wave_sync();  // the list is used again
     }
+
+    // keys that tell their expert
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const uint32_t low = EXACT ? kFree - (uint32_t)((i / VEC * L + lane) * VEC + i % VEC) : (uint32_t)(V - 1 - i);
+        key[i] = key[i] == 0u ? 0u : (key[i] & ~(EXACT ? kFree : (uint32_t)(V - 1))) | low;
+    }
+    sort_down(key);
+    // the best, one after another; where their order is not yet certain two more, to see
+    // how far those behind the list are
+    const int rounds = a.slots + (EXACT ? 0 : 2);
+    constexpr int kShallow = V < 10 ? V : 10;  // a lane gives up no more in so many rounds
+    const bool deep = rounds > kShallow;
+    for (int k = 0; k < rounds; ++k) {
+        best = team_max<L>(key[0]);
+        bool own = key[0] == best && best != 0u;
+        int e;
+        if constexpr (EXACT) {
+            e = (int)(kFree - (best & kFree));
+        } else {
+            // the lowest lane that has it
+            const uint64_t those = __builtin_amdgcn_ballot_w64(own) >> (threadIdx.x % kWave / L * L);
+            const int first = __builtin_ctzll(L == 64 ? those : (those & ((1ull << (L % 64)) - 1)) | 1ull << 63);
+            own = own && first == lane;
+            const int i = V - 1 - (int)(best & (V - 1));
+            e = (i / VEC * L + first) * VEC + i % VEC;
+        }
+#pragma unroll
+        for (int i = 0; i < kShallow; ++i) key[i] = own ? (i + 1 < V ? key[i + 1] : 0u) : key[i];
+        if (V > kShallow && deep) {
+#pragma unroll
+            for (int i = kShallow; i < V; ++i) key[i] = own ? (i + 1 < V ? key[i + 1] : 0u) : key[i];
+        }
+        if (lane == 0) list[k] = {best == 0u ? -1 : e, best};
+    }
+    wave_sync();
+    if constexpr (!EXACT) {
+        bool order = false, end = false;
+        for (int k = lane; k <= a.slots; k += L) {
+            const uint32_t kx = list[k].key & ~(uint32_t)(V - 1), ky = list[k + 1].key & ~(uint32_t)(V - 1);
+            const float x = value_of(kx), y = value_of(ky);
+            // (a logit with other bits above those replaced is larger)
+            const bool near = ky != 0u && (SUMS ? !(x - y > 2 * error + (__builtin_fabsf(x) + __builtin_fabsf(y)) *
+                                                                              ((V + 2) * 0x1p-23f))
+                                                : kx == ky);
+            order |= near && k < a.slots;
+            end |= near && k == a.slots;
+        }
+        // (a close end matters where the list's last place is close to it too)
+        order = team_or<L>(order && live) != 0u;
+        close = team_or<L>((close || (end && order)) && live) != 0u;
+        if (close)
+            choose_in_64<T, L, V, SUMS>(row, a, lane, top, cells64, list);
+        else if (order)
+            order_in_64<T, L, V, SUMS>(row, a, lane, top, cells64, list, a.slots + 1);
+    }
+
+    // weights: of each chosen logit, by the softmax's or the sigmoid's parts
+    float high = none;
+    for (int k = lane; k < a.slots; k += L) {
+        const int e = list[k].expert;
+        const float l = e < 0 ? none : EXACT ? logit_of_key(list[k].key) : load_logit(row, e);
+        list[k].key = __builtin_bit_cast(uint32_t, l);  // from here on the logit
+        high = __builtin_fmaxf(high, l);
+    }
+    float total = 1.0f;
+    if (a.normalize) {
+        high = team_maxf<L>(high);
+        if (a.sigmoid) high = __builtin_fminf(high, 0.0f);
+        total = 0.0f;
+        for (int k = lane; k < a.slots; k += L)
+            if (list[k].expert >= 0) {
+                const float l = __builtin_bit_cast(float, list[k].key);
+                total += a.sigmoid ? sigmoid_above(l, high) : expf(l - high);
+            }
+        total = team_sum<L>(total);
+        if (SUMS && sum != sum) total = sum;  // a NaN that was not chosen itself
+    } else {
+        high = a.sigmoid ? 0.0f : top;
+        total = sum;
+    }
+    if (live)
+        for (int k = lane; k < a.slots; k += L) {
+            const int64_t at = t * a.slots + k;
+            const int e = list[k].expert;
+            if (a.wide_ids)
+                ((int64_t *)a.ids)[at] = e;
+            else
+                ((int32_t *)a.ids)[at] = e;
+            if (a.weights == nullptr) continue;
+            const float l = __builtin_bit_cast(float, list[k].key);
+            const float w = a.sigmoid ? sigmoid_above(l, high) : expf(l - high);
+            store_scalar(a.weights, a.weight_type, at, e < 0 ? 0.0f : a.scale * (w / total));
+        }
 }
 
 // ------------------------------------------------------------------ gradient
@@ -316,111 +517,109 @@ __global__ __launch_bounds__(kTeamThreads) void route_grad_kernel(const T *logit
     Share *list = reinterpret_cast<Share *>(cells + L * V);
     const float none = -__builtin_inff();
 
-    for (int64_t t = (int64_t)blockIdx.x * kTeams + team; t - team < a.tokens; t += kMaxGridX * kTeams) {
-        const bool live = t < a.tokens;
-        const T *row = logits + (live ? t : 0) * ld;
-        float s[WHOLE ? V : 1];
-        float top = 0.0f, sum = 1.0f;
-        if constexpr (WHOLE) {
-            u32x4 raw[V / VEC];
-#pragma unroll
-            for (int j = 0; j < V / VEC; ++j)
-                raw[j] = issue<T>(row, col_of<T>(a.experts, (int64_t)(j * L + lane) * VEC));
-            top = none;
-#pragma unroll
-            for (int j = 0; j < V / VEC; ++j) {
-                const Col col = col_of<T>(a.experts, (int64_t)(j * L + lane) * VEC);
-                const u32x4 r = settle<T>(raw[j], col);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float l = i < col.valid ? element<T>(r, i) : none;
-                    s[j * VEC + i] = l;
-                    top = __builtin_fmaxf(top, l);
-                }
-            }
-            top = team_maxf<L>(top);
-            sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                s[i] = s[i] == none ? 0.0f : expf(s[i] - top);
-                sum += s[i];
-            }
-            sum = team_sum<L>(sum);
-            if (sum == 0.0f) sum = 1.0f;
-        }
+    const int64_t t = (blockIdx.y * kMaxGridX + blockIdx.x) * kTeams + team;
+    const bool live = t < a.tokens;
+    const T *row = logits + (live ? t : 0) * ld;
+    float s[WHOLE ? V : 1];
+    float top = 0.0f, sum = 1.0f;
+    if constexpr (WHOLE) {
+        u32x4 raw[V / VEC];
 #pragma unroll
         for (int j = 0; j < V / VEC; ++j)
+            raw[j] = issue<T>(row, col_of<T>(a.experts, (int64_t)(j * L + lane) * VEC));
+        top = none;
 #pragma unroll
-            for (int i = 0; i < VEC; i += 4)
-                *reinterpret_cast<u32x4 *>(cells + (j * L + lane) * VEC + i) = u32x4{0u, 0u, 0u, 0u};
+        for (int j = 0; j < V / VEC; ++j) {
+            const Col col = col_of<T>(a.experts, (int64_t)(j * L + lane) * VEC);
+            const u32x4 r = settle<T>(raw[j], col);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const float l = i < col.valid ? element<T>(r, i) : none;
+                s[j * VEC + i] = l;
+                top = __builtin_fmaxf(top, l);
+            }
+        }
+        top = team_maxf<L>(top);
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            s[i] = s[i] == none ? 0.0f : expf(s[i] - top);
+            sum += s[i];
+        }
+        sum = team_sum<L>(sum);
+        if (sum == 0.0f) sum = 1.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < V / VEC; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4)
+            *reinterpret_cast<u32x4 *>(cells + (j * L + lane) * VEC + i) = u32x4{0u, 0u, 0u, 0u};
 
-        // each place's expert and logit; then its share
-        float high = none;
-        for (int k = lane; k < a.slots; k += L) {
-            const int64_t at = t * a.slots + k;
-            int64_t id = -1;
-            if (live) id = a.wide_ids ? ((const int64_t *)a.ids)[at] : ((const int32_t *)a.ids)[at];
-            int e = (uint64_t)id < (uint64_t)a.experts ? (int)id : -1;
-            const float l = e < 0 ? none : load_logit(row, e);
-            if (l == none) e = -1;
-            list[k] = {e, l};
-            high = __builtin_fmaxf(high, l);
-        }
-        float total = sum;
-        if (a.normalize) {
-            high = team_maxf<L>(high);
-            if (a.sigmoid) high = __builtin_fminf(high, 0.0f);
-            total = 0.0f;
-            for (int k = lane; k < a.slots; k += L)
-                if (list[k].expert >= 0) total += a.sigmoid ? sigmoid_above(list[k].by, high) : expf(list[k].by - high);
-            total = team_sum<L>(total);
-        } else {
-            high = a.sigmoid ? 0.0f : top;
-        }
-        float dot = 0.0f;  // of the weights and their gradients
+    // each place's expert and logit; then its share
+    float high = none;
+    for (int k = lane; k < a.slots; k += L) {
+        const int64_t at = t * a.slots + k;
+        int64_t id = -1;
+        if (live) id = a.wide_ids ? ((const int64_t *)a.ids)[at] : ((const int32_t *)a.ids)[at];
+        int e = (uint64_t)id < (uint64_t)a.experts ? (int)id : -1;
+        const float l = e < 0 ? none : load_logit(row, e);
+        if (l == none) e = -1;
+        list[k] = {e, l};
+        high = __builtin_fmaxf(high, l);
+    }
+    float total = sum;
+    if (a.normalize) {
+        high = team_maxf<L>(high);
+        if (a.sigmoid) high = __builtin_fminf(high, 0.0f);
+        total = 0.0f;
         for (int k = lane; k < a.slots; k += L)
-            if (list[k].expert >= 0) {
-                const float l = list[k].by, w = (a.sigmoid ? sigmoid_above(l, high) : expf(l - high)) / total;
-                dot += w * (a.scale * load_scalar(a.grad_weights, a.weight_type, t * a.slots + k));
-            }
-        dot = team_sum<L>(dot);
-        for (int k = lane; k < a.slots; k += L)
-            if (list[k].expert >= 0) {
-                const float l = list[k].by, w = (a.sigmoid ? sigmoid_above(l, high) : expf(l - high)) / total;
-                const float g = a.scale * load_scalar(a.grad_weights, a.weight_type, t * a.slots + k);
-                const float d = w * (a.normalize ? g - dot : g);
-                list[k].by = a.sigmoid ? d * sigmoid_above(-l, 0.0f) : d;
-            }
-        wave_sync();
-        // an expert's first place writes the sum over all places that name it, in their order
-        for (int k = lane; k < a.slots; k += L) {
-            const int e = list[k].expert;
-            bool first = e >= 0;
-            for (int o = 0; o < k; ++o) first &= list[o].expert != e;
-            if (!first) continue;
-            float d = list[k].by;
-            for (int o = k + 1; o < a.slots; ++o) d += list[o].expert == e ? list[o].by : 0.0f;
-            cells[e] = d;
+            if (list[k].expert >= 0) total += a.sigmoid ? sigmoid_above(list[k].by, high) : expf(list[k].by - high);
+        total = team_sum<L>(total);
+    } else {
+        high = a.sigmoid ? 0.0f : top;
+    }
+    float dot = 0.0f;  // of the weights and their gradients
+    for (int k = lane; k < a.slots; k += L)
+        if (list[k].expert >= 0) {
+            const float l = list[k].by, w = (a.sigmoid ? sigmoid_above(l, high) : expf(l - high)) / total;
+            dot += w * (a.scale * load_scalar(a.grad_weights, a.weight_type, t * a.slots + k));
         }
-        wave_sync();
-        if (live) {
-            T *out = grad_logits + t * ld_grad;
+    dot = team_sum<L>(dot);
+    for (int k = lane; k < a.slots; k += L)
+        if (list[k].expert >= 0) {
+            const float l = list[k].by, w = (a.sigmoid ? sigmoid_above(l, high) : expf(l - high)) / total;
+            const float g = a.scale * load_scalar(a.grad_weights, a.weight_type, t * a.slots + k);
+            const float d = w * (a.normalize ? g - dot : g);
+            list[k].by = a.sigmoid ? d * sigmoid_above(-l, 0.0f) : d;
+        }
+    wave_sync();
+    // an expert's first place writes the sum over all places that name it, in their order
+    for (int k = lane; k < a.slots; k += L) {
+        const int e = list[k].expert;
+        bool first = e >= 0;
+        for (int o = 0; o < k; ++o) first &= list[o].expert != e;
+        if (!first) continue;
+        float d = list[k].by;
+        for (int o = k + 1; o < a.slots; ++o) d += list[o].expert == e ? list[o].by : 0.0f;
+        cells[e] = d;
+    }
+    wave_sync();
+    if (live) {
+        T *out = grad_logits + t * ld_grad;
 #pragma unroll
-            for (int j = 0; j < V / VEC; ++j) {
-                const Col col = col_of<T>(a.experts, (int64_t)(j * L + lane) * VEC);
-                float d[VEC];
+        for (int j = 0; j < V / VEC; ++j) {
+            const Col col = col_of<T>(a.experts, (int64_t)(j * L + lane) * VEC);
+            float d[VEC];
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    d[i] = cells[(j * L + lane) * VEC + i];
-                    if constexpr (WHOLE) {
-                        const float p = s[j * VEC + i] / sum;
-                        d[i] -= p == 0.0f ? 0.0f : p * dot;
-                    }
+            for (int i = 0; i < VEC; ++i) {
+                d[i] = cells[(j * L + lane) * VEC + i];
+                if constexpr (WHOLE) {
+                    const float p = s[j * VEC + i] / sum;
+                    d[i] -= p == 0.0f ? 0.0f : p * dot;
                 }
-                store_col<T>(out, pack<T>(d), col);
             }
+            store_col<T>(out, pack<T>(d), col);
         }
-        wave_sync();
     }
 }
 
