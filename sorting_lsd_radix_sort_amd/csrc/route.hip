@@ -84,7 +84,7 @@ LRS_API lrs_status lrs_route_tokens(lrs_row_type type, const void *d_logits, int
     const int size = (int)(experts / num_groups);
     Route a{d_bias, d_ids, d_weights, scale, (int)tokens, (int16_t)experts, (int16_t)size, (int16_t)num_groups,
             (int16_t)kept_groups, (uint8_t)slots, score == LRS_SCORE_SIGMOID, top2, normalize != 0,
-            id_type == LRS_ID_I64, (uint8_t)weight_type, 0};
+            id_type == LRS_ID_I64, (uint8_t)weight_type, 0, 0};
     // a token's list of the chosen, and its scores and groups where they are needed
     const int cells = sums || b == 4 ? 8 : grouped ? 4 : 0;
     const int team_bytes = team_align((slots + 2) * (int64_t)sizeof(Chosen) + cells * (experts + num_groups));
@@ -94,7 +94,7 @@ LRS_API lrs_status lrs_route_tokens(lrs_row_type type, const void *d_logits, int
             using TEAM = decltype(team);
             const int lanes = size / kVec<T>;
             if (size % kVec<T> == 0 && (lanes & (lanes - 1)) == 0 && lanes <= std::min(TEAM::lanes, 16))
-                a.lane_groups = (uint8_t)lanes;
+                a.lane_groups = (uint8_t)lanes, a.lane_groups_log2 = (uint8_t)__builtin_ctz((unsigned)lanes);
             const unsigned lds = (unsigned)team_bytes * (kTeamThreads / TEAM::lanes);
             with_bool(sums, [&](auto by_sums) {
                 route_kernel<T, TEAM::lanes, TEAM::logits, by_sums.value>

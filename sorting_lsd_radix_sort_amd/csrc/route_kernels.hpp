@@ -39,7 +39,7 @@ struct Route {
     int tokens;
     int16_t experts, size, groups, kept;  // size: of a group
     uint8_t slots, sigmoid, top2, normalize, wide_ids, weight_type;
-    uint8_t lane_groups;  // a group is this many lanes' vectors; 0: it is no such number
+    uint8_t lane_groups, lane_groups_log2;  // a group is this many lanes' vectors; 0: it is no such number
 };
 
 // A token's list of the chosen, in LDS.
@@ -100,11 +100,10 @@ __device__ __forceinline__ double sum64(const T *row, const Route &a, int lane, 
     return team_sum64<L>(sum);
 }
 
-// The choice by float64 throughout, for the token whose scores are too close to one
-// another in float32 (or hold NaN or infinity): all of them again, from memory to LDS
-// (cells: experts, then groups).
+// A token's scores in float64 as order keys, from memory to LDS (cells: experts, then
+// groups, whose scores follow where there is a choice among them).
 template <typename T, int L, int V, bool SUMS>
-__device__ void choose_in_64(const T *row, const Route &a, int lane, float top, uint64_t *cells, Chosen *list)
+__device__ __forceinline__ void scores_in_64(const T *row, const Route &a, int lane, float top, uint64_t *cells)
 {
     const double sum = SUMS ? sum64<T, L, V>(row, a, lane, top) : 1.0;
 #pragma unroll 4
@@ -114,25 +113,40 @@ __device__ void choose_in_64(const T *row, const Route &a, int lane, float top, 
             cells[e] = choice64<SUMS>(a, load_logit(row, e), SUMS && a.bias != nullptr ? a.bias[e] : 0.0f, top, sum);
     }
     wave_sync();
-    if (a.kept < a.groups) {
-        uint64_t *of_group = cells + a.experts;
-        for (int g = lane; g < a.groups; g += L) {
-            uint64_t first = 0, second = 0;
+    if (a.kept == a.groups) return;
+    for (int g = lane; g < a.groups; g += L) {
+        uint64_t first = 0, second = 0;
 #pragma unroll 4
-            for (int i = 0; i < a.size; ++i) {
-                const uint64_t k = cells[g * a.size + i];
-                second = k > first ? first : k > second ? k : second;
-                first = k > first ? k : first;
-            }
-            of_group[g] = a.top2 && second != 0 ? key_of(value_of(first) + value_of(second)) : first;
+        for (int i = 0; i < a.size; ++i) {
+            const uint64_t k = cells[g * a.size + i];
+            second = k > first ? first : k > second ? k : second;
+            first = k > first ? k : first;
         }
-        wave_sync();
-        for (int g = lane; g < a.groups; g += L) {
-            int before = 0;
-            for (int o = 0; o < a.groups; ++o) before += of_group[o] > of_group[g] || (of_group[o] == of_group[g] && o < g);
-            if (before >= a.kept)
+        cells[a.experts + g] = a.top2 && second != 0 ? key_of(value_of(first) + value_of(second)) : first;
+    }
+    wave_sync();
+}
+
+// Groups that are better than group g: key[0..groups) their scores.
+template <typename K>
+__device__ __forceinline__ int groups_before(const K *key, int groups, K mine, int g)
+{
+    int n = 0;
+    for (int o = 0; o < groups; ++o) n += key[o] > mine || (key[o] == mine && o < g);
+    return n;
+}
+
+// The choice by float64 throughout, for the token whose scores are too close to one
+// another in float32, or hold NaN or infinity.
+template <typename T, int L, int V, bool SUMS>
+__device__ void choose_in_64(const T *row, const Route &a, int lane, float top, uint64_t *cells, Chosen *list)
+{
+    scores_in_64<T, L, V, SUMS>(row, a, lane, top, cells);
+    if (a.kept < a.groups) {
+        const uint64_t *of_group = cells + a.experts;
+        for (int g = lane; g < a.groups; g += L)
+            if (groups_before(of_group, a.groups, of_group[g], g) >= a.kept)
                 for (int i = 0; i < a.size; ++i) cells[g * a.size + i] = 0;
-        }
         wave_sync();
     }
     for (int k = 0; k < a.slots; ++k) {
@@ -245,61 +259,78 @@ __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict
     u32x4 raw[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) raw[j] = issue<T>(row, col_of<T>(a.experts, (int64_t)(j * L + lane) * VEC));
+    for (int k = lane; k < a.slots + 2; k += L) list[k] = {-1, 0u};
     // element i of a lane is expert (i / VEC * L + lane) * VEC + i % VEC
-    uint32_t key[V];
-    uint32_t best = 0u;
+    float l[V];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         const Col col = col_of<T>(a.experts, (int64_t)(j * L + lane) * VEC);
         const u32x4 r = settle<T>(raw[j], col);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const uint32_t k = live && i < col.valid ? key_of(element<T>(r, i)) : 0u;
-            key[j * VEC + i] = k;
-            best = k > best ? k : best;
-        }
+        for (int i = 0; i < VEC; ++i) l[j * VEC + i] = live && i < col.valid ? element<T>(r, i) : none;
     }
 
     // the softmax's maximum and sum over all experts, where they are needed; the
     // exponent's product in two parts, so that its rounding is all that is lost
     float top = 0.0f, sum = 1.0f;
     if (!a.sigmoid && (SUMS || !a.normalize)) {
-        best = team_max<L>(best);
-        top = value_of(best);
+        top = none;
+#pragma unroll
+        for (int i = 0; i < V; ++i) top = __builtin_fmaxf(top, l[i]);
+        top = team_maxf<L>(top);
         sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float d = value_of(key[i]) - top;
+            const float d = l[i] - top;
             const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(d, 1.44269504f, d * 1.92596303e-8f));
-            sum += key[i] == 0u ? 0.0f : e;
+            sum += l[i] == none ? 0.0f : e;
         }
-        sum = best == 0u ? 1.0f : team_sum<L>(sum);
+        sum = team_sum<L>(sum);
+        if (sum == 0.0f) sum = 1.0f;
     }
 
-    // What is compared: the logits, or the scores with their bias, off by at most
-    // `error` but for the sum's own rounding: exponents (2 |d| + 4) 2^-24 relative,
-    // |d| s being at most 0.37 of the largest, a reciprocal, the sum of all.
+    // What is compared, as an order key: the logits, or the scores with their bias, off by
+    // at most `error` but for that sum's rounding.  An exponential is off by (1.3 |d| + 2)
+    // 2^-24 of itself; a sigmoid by a quarter of that (and |l| s (1 - s) is below 0.23), an
+    // addition and a reciprocal, together less than 4 * 2^-24; a softmax's score by that
+    // (|d| s is below 0.37 of the largest), and by the additions of its sum.
     float error = 0.0f;
     bool close = false;  // too close for float32
+    uint32_t key[V];
     if constexpr (SUMS) {
         const float each = 1.0f / sum;
-        error = a.sigmoid ? 8 * 0x1p-24f : 64 * 0x1p-24f * each;
+        error = a.sigmoid ? 4 * 0x1p-24f : 64 * 0x1p-24f * each;
+        const float shift = a.sigmoid ? 0.0f : top;
+        const float by = a.sigmoid ? -1.44269504f : 1.44269504f;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int c = (j * L + lane) * VEC;
+            float b[VEC];
+            if (a.bias != nullptr) {
+                // (float32: one or two vectors for one of the logits)
+#pragma unroll
+                for (int h = 0; h < VEC / 4; ++h) {
+                    const Col col = col_of<float>(a.experts, (int64_t)(j * L + lane) * VEC + 4 * h);
+                    const u32x4 r = load_col<float>(a.bias, col);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) b[4 * h + i] = element<float>(r, i);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) b[i] = 0.0f;
+            }
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                uint32_t &k = key[j * VEC + i];
-                const float l = value_of(k), b = a.bias != nullptr && c + i < a.experts ? a.bias[c + i] : 0.0f;
-                const float x = (a.sigmoid ? -l : l - top) * 1.44269504f;
-                const float e = __builtin_amdgcn_exp2f(x);
-                const float sc = (a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + e) : e * each) + b;
-                const bool out = k == 0u || b == none;
-                close |= !out && !(__builtin_fabsf(sc) < __builtin_inff());
-                const uint32_t bits = __builtin_bit_cast(uint32_t, sc + 0.0f);
-                k = out ? 0u : bits ^ ((uint32_t)((int32_t)bits >> 31) | 0x80000000u);
+                const float x = l[j * VEC + i], e = __builtin_amdgcn_exp2f((x - shift) * by);
+                float c = (a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + e) : e * each) + b[i];
+                c = x == none ? none : c;
+                close |= __builtin_isfpclass(c, 0x203);  // NaN or +infinity
+                const uint32_t bits = __builtin_bit_cast(uint32_t, c + 0.0f);
+                key[j * VEC + i] = c == none ? 0u : bits ^ ((uint32_t)((int32_t)bits >> 31) | 0x80000000u);
             }
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = key_of(l[i]);
     }
 
     if (a.kept < a.groups) {
@@ -311,15 +342,8 @@ __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict
             magnitude = __builtin_fmaxf(magnitude, __builtin_fabsf(x) + __builtin_fabsf(y));
             return key_of(x + y);
         };
-        auto before = [&](uint32_t mine, int g) {
-            int n = 0;
-            for (int o = 0; o < a.groups; ++o) n += of_group[o] > mine || (of_group[o] == mine && o < g);
-            return n;
-        };
-        uint32_t least = ~0u, most = 0u;  // of the kept, of the others
         if (a.lane_groups != 0) {
             // a group's vectors lie in neighbouring lanes
-            uint32_t mine[J];
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 uint32_t first = key[j * VEC], second = 0u;
@@ -335,20 +359,9 @@ __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict
                 if (a.lane_groups > 2) join(dpp<0x4E>(first), dpp<0x4E>(second));
                 if (a.lane_groups > 4) join(dpp<0x141>(first), dpp<0x141>(second));
                 if (a.lane_groups > 8) join(dpp<0x140>(first), dpp<0x140>(second));
-                mine[j] = score(first, second);
-                const int g = (j * L + lane) / a.lane_groups;
-                if (g < a.groups && lane % a.lane_groups == 0) of_group[g] = mine[j];
-            }
-            wave_sync();
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const int g = (j * L + lane) / a.lane_groups;
-                if (g >= a.groups) continue;
-                const bool stays = before(mine[j], g) < a.kept;
-                least = stays && mine[j] < least ? mine[j] : least;
-                most = !stays && mine[j] > most ? mine[j] : most;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) key[j * VEC + i] = stays ? key[j * VEC + i] : 0u;
+                const uint32_t mine = score(first, second);
+                const int g = (j * L + lane) >> a.lane_groups_log2;
+                if (g < a.groups && (lane & (a.lane_groups - 1)) == 0) of_group[g] = mine;
             }
         } else {
 #pragma unroll
@@ -368,31 +381,50 @@ __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict
                 }
                 of_group[g] = score(first, second);
             }
-            wave_sync();
-            for (int g = lane; g < a.groups; g += L) {
-                const uint32_t mine = of_group[g];
-                if (before(mine, g) < a.kept) {
-                    least = mine < least ? mine : least;
-                } else {
-                    most = mine > most ? mine : most;
-                    for (int i = 0; i < a.size; ++i) cells[g * a.size + i] = 0u;
-                }
-            }
-            wave_sync();
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = (i / VEC * L + lane) * VEC + i % VEC;
-                key[i] = e < a.experts ? cells[e] : 0u;
-            }
+        }
+        wave_sync();
+        // each group's place; and the least of the kept, the most of the others
+        uint32_t least = ~0u, most = 0u;
+        uint64_t stays = 0;
+        for (int g = lane; g < a.groups; g += L) {
+            const uint32_t mine = of_group[g];
+            const bool s = groups_before(of_group, a.groups, mine, g) < a.kept;
+            least = s && mine < least ? mine : least;
+            most = !s && mine > most ? mine : most;
+            stays |= (uint64_t)s << g;
         }
         if constexpr (SUMS) {
             const float x = value_of(team_min<L>(least)), y = value_of(team_max<L>(most));
             const float size = __builtin_fmaxf(team_maxf<L>(magnitude), __builtin_fabsf(x) + __builtin_fabsf(y));
-            close |= y != none && !(x - y > 4 * error + size * 0x1p-22f);
+            const bool near = y != none && !(x - y > 4 * error + size * 0x1p-22f);
+            if (near && live) {  // (the same for the whole team)
+                wave_sync();
+                scores_in_64<T, L, V, SUMS>(row, a, lane, top, cells64);
+                const uint64_t *of_group64 = cells64 + a.experts;
+                stays = 0;
+                for (int g = lane; g < a.groups; g += L)
+                    stays |= (uint64_t)(groups_before(of_group64, a.groups, of_group64[g], g) < a.kept) << g;
+            }
+        }
+        const uint32_t low = team_or<L>((uint32_t)stays), high = team_or<L>((uint32_t)(stays >> 32));
+        stays = (uint64_t)high << 32 | low;
+        if (a.lane_groups != 0) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const bool s = stays >> (((j * L + lane) >> a.lane_groups_log2) & 63) & 1;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) key[j * VEC + i] = s ? key[j * VEC + i] : 0u;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = (i / VEC * L + lane) * VEC + i % VEC;
+                key[i] = stays >> (e / a.size & 63) & 1 ? key[i] : 0u;
+            }
         }
     }
 
-    // keys that tell their expert
+    // keys that tell their place
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const uint32_t low = EXACT ? kFree - (uint32_t)((i / VEC * L + lane) * VEC + i % VEC) : (uint32_t)(V - 1 - i);
@@ -405,26 +437,32 @@ __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict
     constexpr int kShallow = V < 10 ? V : 10;  // a lane gives up no more in so many rounds
     const bool deep = rounds > kShallow;
     for (int k = 0; k < rounds; ++k) {
-        best = team_max<L>(key[0]);
+        const uint32_t best = team_max<L>(key[0]);
         bool own = key[0] == best && best != 0u;
-        int e;
-        if constexpr (EXACT) {
-            e = (int)(kFree - (best & kFree));
-        } else {
-            // the lowest lane that has it
-            const uint64_t those = __builtin_amdgcn_ballot_w64(own) >> (threadIdx.x % kWave / L * L);
-            const int first = __builtin_ctzll(L == 64 ? those : (those & ((1ull << (L % 64)) - 1)) | 1ull << 63);
-            own = own && first == lane;
-            const int i = V - 1 - (int)(best & (V - 1));
-            e = (i / VEC * L + first) * VEC + i % VEC;
+        if constexpr (!EXACT) {
+            // of several lanes that have it the lowest (more owners than teams that have any)
+            const uint64_t those = __builtin_amdgcn_ballot_w64(own);
+            constexpr uint64_t kFirst = L == 64 ? 1ull : L == 16 ? 0x0001000100010001ull : 0x0101010101010101ull;
+            if (__builtin_popcountll(those) != __builtin_popcountll(__builtin_amdgcn_ballot_w64(best != 0u) & kFirst)) {
+                const uint64_t mine = those >> (threadIdx.x % kWave / L * L);
+                own = own && (mine & ((1ull << lane) - 1)) == 0ull;
+            }
         }
+        if (own) list[k] = {lane, best};
 #pragma unroll
         for (int i = 0; i < kShallow; ++i) key[i] = own ? (i + 1 < V ? key[i + 1] : 0u) : key[i];
         if (V > kShallow && deep) {
 #pragma unroll
             for (int i = kShallow; i < V; ++i) key[i] = own ? (i + 1 < V ? key[i + 1] : 0u) : key[i];
         }
-        if (lane == 0) list[k] = {best == 0u ? -1 : e, best};
+    }
+    wave_sync();
+    // from the lanes and their keys the experts
+    for (int k = lane; k < rounds; k += L) {
+        const Chosen c = list[k];
+        if (c.expert < 0) continue;
+        const int i = V - 1 - (int)(c.key & (V - 1));
+        list[k].expert = EXACT ? (int)(kFree - (c.key & kFree)) : (i / VEC * L + c.expert) * VEC + i % VEC;
     }
     wave_sync();
     if constexpr (!EXACT) {
@@ -441,7 +479,8 @@ __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict
         }
         // (a close end matters where the list's last place is close to it too)
         order = team_or<L>(order && live) != 0u;
-        close = team_or<L>((close || (end && order)) && live) != 0u;
+        end = team_or<L>(end) != 0u;
+        close = team_or<L>(close && live) != 0u || (end && order);
         if (close)
             choose_in_64<T, L, V, SUMS>(row, a, lane, top, cells64, list);
         else if (order)
@@ -452,9 +491,9 @@ __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict
     float high = none;
     for (int k = lane; k < a.slots; k += L) {
         const int e = list[k].expert;
-        const float l = e < 0 ? none : EXACT ? logit_of_key(list[k].key) : load_logit(row, e);
-        list[k].key = __builtin_bit_cast(uint32_t, l);  // from here on the logit
-        high = __builtin_fmaxf(high, l);
+        const float x = e < 0 ? none : EXACT ? logit_of_key(list[k].key) : load_logit(row, e);
+        list[k].key = __builtin_bit_cast(uint32_t, x);  // from here on the logit
+        high = __builtin_fmaxf(high, x);
     }
     float total = 1.0f;
     if (a.normalize) {
@@ -463,8 +502,8 @@ __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict
         total = 0.0f;
         for (int k = lane; k < a.slots; k += L)
             if (list[k].expert >= 0) {
-                const float l = __builtin_bit_cast(float, list[k].key);
-                total += a.sigmoid ? sigmoid_above(l, high) : expf(l - high);
+                const float x = __builtin_bit_cast(float, list[k].key);
+                total += a.sigmoid ? sigmoid_above(x, high) : expf(x - high);
             }
         total = team_sum<L>(total);
         if (SUMS && sum != sum) total = sum;  // a NaN that was not chosen itself
@@ -481,8 +520,8 @@ __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict
             else
                 ((int32_t *)a.ids)[at] = e;
             if (a.weights == nullptr) continue;
-            const float l = __builtin_bit_cast(float, list[k].key);
-            const float w = a.sigmoid ? sigmoid_above(l, high) : expf(l - high);
+            const float x = __builtin_bit_cast(float, list[k].key);
+            const float w = a.sigmoid ? sigmoid_above(x, high) : expf(x - high);
             store_scalar(a.weights, a.weight_type, at, e < 0 ? 0.0f : a.scale * (w / total));
         }
 }
@@ -543,7 +582,9 @@ __global__ __launch_bounds__(kTeamThreads) void route_grad_kernel(const T *logit
         sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            s[i] = s[i] == none ? 0.0f : expf(s[i] - top);
+            const float d = s[i] - top;
+            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(d, 1.44269504f, d * 1.92596303e-8f));
+            s[i] = s[i] == none ? 0.0f : e;
             sum += s[i];
         }
         sum = team_sum<L>(sum);
@@ -606,6 +647,7 @@ __global__ __launch_bounds__(kTeamThreads) void route_grad_kernel(const T *logit
     wave_sync();
     if (live) {
         T *out = grad_logits + t * ld_grad;
+        const float each = 1.0f / sum;
 #pragma unroll
         for (int j = 0; j < V / VEC; ++j) {
             const Col col = col_of<T>(a.experts, (int64_t)(j * L + lane) * VEC);
@@ -614,7 +656,8 @@ __global__ __launch_bounds__(kTeamThreads) void route_grad_kernel(const T *logit
             for (int i = 0; i < VEC; ++i) {
                 d[i] = cells[(j * L + lane) * VEC + i];
                 if constexpr (WHOLE) {
-                    const float p = s[j * VEC + i] / sum;
+                    // (a score of zero has no share in a NaN that it did not cause)
+                    const float p = s[j * VEC + i] * each;
                     d[i] -= p == 0.0f ? 0.0f : p * dot;
                 }
             }
