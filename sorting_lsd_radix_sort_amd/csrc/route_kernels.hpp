@@ -449,12 +449,15 @@ __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict
             }
         }
         if (own) list[k] = {lane, best};
+        auto shift = [&](int from, int to) {
 #pragma unroll
-        for (int i = 0; i < kShallow; ++i) key[i] = own ? (i + 1 < V ? key[i + 1] : 0u) : key[i];
-        if (V > kShallow && deep) {
-#pragma unroll
-            for (int i = kShallow; i < V; ++i) key[i] = own ? (i + 1 < V ? key[i + 1] : 0u) : key[i];
-        }
+            for (int i = from; i < to; ++i) {
+                const uint32_t here = key[i], next = i + 1 < V ? key[i + 1 < V ? i + 1 : 0] : 0u;
+                key[i] = own ? next : here;
+            }
+        };
+        shift(0, kShallow);
+        if (V > kShallow && deep) shift(kShallow, V);
     }
     wave_sync();
     // from the lanes and their keys the experts
