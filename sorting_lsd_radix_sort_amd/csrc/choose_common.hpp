@@ -46,7 +46,8 @@ __device__ __forceinline__ double value_of(uint64_t k)
 //
 // Reductions over the L lanes of a team, given to all of them: lanes 1 and 2 apart by
 // quad permutations, 4 and 8 by mirrors of half rows and rows (whose lanes hold the
-// same by then), rows of 16 by readlane.  Sums have one order whatever the lane.
+// same by then), rows of 16 and halves by exchanging them between two copies.  Sums have
+// one order whatever the lane.
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v)
 {
@@ -60,10 +61,13 @@ __device__ __forceinline__ uint32_t team_reduce(uint32_t v, F &&f)
     v = f(v, dpp<0x4E>(v));
     v = f(v, dpp<0x141>(v));
     if constexpr (L >= 16) v = f(v, dpp<0x140>(v));
+    if constexpr (L >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = f((uint32_t)r[0], (uint32_t)r[1]);
+    }
     if constexpr (L == 64) {
-        const uint32_t a = f((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16));
-        const uint32_t b = f((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48));
-        v = f(a, b);
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = f((uint32_t)r[0], (uint32_t)r[1]);
     }
     return v;
 }

@@ -32,7 +32,7 @@ void with_team(int64_t experts, F &&f)
     else if (experts <= 256)
         f(Team<16, 16>{});
     else if (experts <= 512)
-        f(Team<16, 32>{});
+        f(Team<32, 16>{});
     else if (experts <= 1024)
         f(Team<64, 16>{});
     else
@@ -131,7 +131,7 @@ LRS_API lrs_status lrs_route_tokens_grad(lrs_row_type type, const void *d_logits
         using T = decltype(elem);
         with_team(experts, [&](auto team) {
             using TEAM = decltype(team);
-            const int team_bytes = team_align(TEAM::lanes * TEAM::logits * 4 + slots * (int64_t)sizeof(Share));
+            const int team_bytes = team_align(TEAM::lanes * TEAM::logits * 4 + slots * ((int64_t)sizeof(Share) + 4));
             const unsigned lds = (unsigned)team_bytes * (kTeamThreads / TEAM::lanes);
             with_bool(score == LRS_SCORE_SOFTMAX && !normalize, [&](auto whole) {
                 route_grad_kernel<T, TEAM::lanes, TEAM::logits, whole.value>

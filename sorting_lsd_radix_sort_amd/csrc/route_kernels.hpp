@@ -1,7 +1,7 @@
 // route_kernels.hpp -- gfx950 (CDNA4, wave64) kernels of a router's choice of experts
 // and its gradient (include/lrsort_choose.h).
 //
-// A team of 8, 16 or 64 lanes serves a token: its logits are loaded once, 16 bytes a
+// A team of 8 to 64 lanes serves a token: its logits are loaded once, 16 bytes a
 // lane at a time, and stay in registers as order keys while the best are taken from
 // them one by one.
 #pragma once
@@ -169,10 +169,10 @@ __device__ void choose_in_64(const T *row, const Route &a, int lane, float top, 
 
 // The first `n` of the list, which are the best n of their token, in the order of
 // float64.
-template <typename T, int L, int V, bool SUMS>
-__device__ void order_in_64(const T *row, const Route &a, int lane, float top, uint64_t *cells, Chosen *list, int n)
+template <typename T, int L, bool SUMS>
+__device__ __forceinline__ void order_in_64(const T *row, const Route &a, int lane, float top, double sum,
+                                            uint64_t *cells, Chosen *list, int n)
 {
-    const double sum = SUMS ? sum64<T, L, V>(row, a, lane, top) : 1.0;
     for (int k = lane; k < n; k += L) {
         const int e = list[k].expert;
         cells[k] = e < 0 ? 0ull
@@ -442,7 +442,10 @@ __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict
         if constexpr (!EXACT) {
             // of several lanes that have it the lowest (more owners than teams that have any)
             const uint64_t those = __builtin_amdgcn_ballot_w64(own);
-            constexpr uint64_t kFirst = L == 64 ? 1ull : L == 16 ? 0x0001000100010001ull : 0x0101010101010101ull;
+            constexpr uint64_t kFirst = L == 64   ? 1ull
+                                        : L == 32 ? 0x0000000100000001ull
+                                        : L == 16 ? 0x0001000100010001ull
+                                                  : 0x0101010101010101ull;
             if (__builtin_popcountll(those) != __builtin_popcountll(__builtin_amdgcn_ballot_w64(best != 0u) & kFirst)) {
                 const uint64_t mine = those >> (threadIdx.x % kWave / L * L);
                 own = own && (mine & ((1ull << lane) - 1)) == 0ull;
@@ -486,8 +489,18 @@ __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict
         close = team_or<L>(close && live) != 0u || (end && order);
         if (close)
             choose_in_64<T, L, V, SUMS>(row, a, lane, top, cells64, list);
-        else if (order)
-            order_in_64<T, L, V, SUMS>(row, a, lane, top, cells64, list, a.slots + 1);
+        else if (order) {
+            double sum = 1.0;
+            if constexpr (SUMS)
+                if (!a.sigmoid) {
+                    // (no NaN is here: it would be close)
+                    sum = 0.0;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum += l[i] == none ? 0.0 : exp64((double)l[i] - (double)top);
+                    sum = team_sum64<L>(sum);
+                }
+            order_in_64<T, L, SUMS>(row, a, lane, top, sum, cells64, list, a.slots + 1);
+        }
     }
 
     // weights: of each chosen logit, by the softmax's or the sigmoid's parts
@@ -557,6 +570,7 @@ __global__ __launch_bounds__(kTeamThreads) void route_grad_kernel(const T *logit
     const int lane = (int)threadIdx.x % L, team = (int)threadIdx.x / L;
     float *cells = reinterpret_cast<float *>(reinterpret_cast<char *>(lds) + team * team_bytes);
     Share *list = reinterpret_cast<Share *>(cells + L * V);
+    float *grads = reinterpret_cast<float *>(list + a.slots);
     const float none = -__builtin_inff();
 
     const int64_t t = (blockIdx.y * kMaxGridX + blockIdx.x) * kTeams + team;
@@ -599,12 +613,16 @@ __global__ __launch_bounds__(kTeamThreads) void route_grad_kernel(const T *logit
         for (int i = 0; i < VEC; i += 4)
             *reinterpret_cast<u32x4 *>(cells + (j * L + lane) * VEC + i) = u32x4{0u, 0u, 0u, 0u};
 
-    // each place's expert and logit; then its share
+    // each place's expert, logit and gradient (loaded with the id: what belongs to no
+    // expert is not used); then its share
     float high = none;
     for (int k = lane; k < a.slots; k += L) {
         const int64_t at = t * a.slots + k;
         int64_t id = -1;
-        if (live) id = a.wide_ids ? ((const int64_t *)a.ids)[at] : ((const int32_t *)a.ids)[at];
+        if (live) {
+            id = a.wide_ids ? ((const int64_t *)a.ids)[at] : ((const int32_t *)a.ids)[at];
+            grads[k] = a.scale * load_scalar(a.grad_weights, a.weight_type, at);
+        }
         int e = (uint64_t)id < (uint64_t)a.experts ? (int)id : -1;
         const float l = e < 0 ? none : load_logit(row, e);
         if (l == none) e = -1;
@@ -626,14 +644,13 @@ __global__ __launch_bounds__(kTeamThreads) void route_grad_kernel(const T *logit
     for (int k = lane; k < a.slots; k += L)
         if (list[k].expert >= 0) {
             const float l = list[k].by, w = (a.sigmoid ? sigmoid_above(l, high) : expf(l - high)) / total;
-            dot += w * (a.scale * load_scalar(a.grad_weights, a.weight_type, t * a.slots + k));
+            dot += w * grads[k];
         }
     dot = team_sum<L>(dot);
     for (int k = lane; k < a.slots; k += L)
         if (list[k].expert >= 0) {
             const float l = list[k].by, w = (a.sigmoid ? sigmoid_above(l, high) : expf(l - high)) / total;
-            const float g = a.scale * load_scalar(a.grad_weights, a.weight_type, t * a.slots + k);
-            const float d = w * (a.normalize ? g - dot : g);
+            const float d = w * (a.normalize ? grads[k] - dot : grads[k]);
             list[k].by = a.sigmoid ? d * sigmoid_above(-l, 0.0f) : d;
         }
     wave_sync();
