@@ -276,6 +276,34 @@ def _beam_dims(name, shape, strides, at, size):
     return row, dims[::-1]
 
 
+_plans: dict = {}  # how states of a shape and strides are reordered, which alone decide it
+
+
+def _beam_plan(shape, strides, dim, size, parents_shape, out_shape, out_strides):
+    """(shape of the new states, batch dimension, sizes for the C call, its layouts)."""
+    nd, at = len(shape), int(dim)
+    at = at + nd if at < 0 else at
+    if not 0 <= at < nd - 1:
+        raise ValueError("states of shape %s have no batch in dimension %d with the beams behind it" %
+                         (tuple(shape), dim))
+    batch, beams = shape[at], shape[at + 1]
+    if len(parents_shape) != 2 or parents_shape[0] != batch:
+        raise ValueError("parents have shape %s, expected (%d, count)" % (tuple(parents_shape), batch))
+    count = parents_shape[1]
+    new_shape = (*shape[:at + 1], count, *shape[at + 2:])
+    if out_shape is not None and tuple(out_shape) != new_shape:
+        raise ValueError("out has shape %s, expected %s" % (tuple(out_shape), new_shape))
+    if out_strides is None:
+        out_strides, step = [0] * nd, 1
+        for d in range(nd - 1, -1, -1):
+            out_strides[d], step = step, step * max(new_shape[d], 1)
+    row, dims = (0, []) if 0 in new_shape else _beam_dims("states", new_shape, (strides, out_strides), at, size)
+    (outer, outer_steps), (middle, middle_steps), (n, row_steps) = [(1, (0, 0))] * (3 - len(dims)) + dims
+    layouts = [BeamLayout(outer_steps[i], s[at] * size, s[at + 1] * size, middle_steps[i], row_steps[i])
+               for i, s in enumerate((strides, out_strides))]
+    return new_shape, (outer, batch, beams, count, middle, n, row), layouts[0], layouts[1]
+
+
 def beam_reorder(states, parents, dim: int = 0, out=None, stream=None):
     """The beams' states after a step: out[..., b, j, ...] = states[..., b, parents[b, j],
     ...], zeros where a parent is outside the beams.  states: any type of 1, 2, 4, 8 or 16
@@ -285,42 +313,28 @@ def beam_reorder(states, parents, dim: int = 0, out=None, stream=None):
     parent), or a new one.  Strides may be any that leave at most three dimensions beside
     batch, beams and a contiguous piece: the filled part of a cache that has room for more
     will do, with layers in front and heads before or behind the positions."""
-    codes, _, int32 = _r._types or _r._type_codes()
-    if parents.dtype is not int32:
+    if parents.dtype is not (_r._types or _r._type_codes())[2]:
         raise TypeError("parents must be int32, not %s" % parents.dtype)
-    nd, at = states.dim(), int(dim)
-    at = at + nd if at < 0 else at
-    if not 0 <= at < nd - 1:
-        raise ValueError("states of shape %s have no batch in dimension %d with the beams behind it" %
-                         (tuple(states.shape), dim))
-    shape = list(states.shape)
-    batch, beams = shape[at], shape[at + 1]
-    if parents.dim() != 2 or parents.shape[0] != batch:
-        raise ValueError("parents have shape %s, expected (%d, count)" % (tuple(parents.shape), batch))
+    key = (states.shape, states.stride(), dim, states.dtype, parents.shape, out is not None and (out.shape, out.stride()))
+    plan = _plans.get(key)
+    if plan is None:
+        plan = _beam_plan(states.shape, states.stride(), dim, states.element_size(), parents.shape,
+                          *((None, None) if out is None else (out.shape, out.stride())))
+        if len(_plans) >= 4096:
+            _plans.clear()
+        _plans[key] = plan
+    shape, sizes, from_layout, to_layout = plan
     _same_device("parents", parents, states)
-    count = parents.shape[1]
-    shape[at + 1] = count
+    given = out
     if out is not None:
         if out.dtype is not states.dtype:
             raise ValueError("out has dtype %s, expected %s" % (out.dtype, states.dtype))
-        if list(out.shape) != shape:
-            raise ValueError("out has shape %s, expected %s" % (tuple(out.shape), tuple(shape)))
         _same_device("out", out, states)
-    given = out
-    size = states.element_size()
-    if out is None:
-        out = states.new_empty(shape)
-    if 0 in shape:
-        row, dims = 0, []
-    else:
-        row, dims = _beam_dims("states", shape, (states.stride(), out.stride()), at, size)
     if not states.is_cuda:
         raise _r._host_tensor(states)
+    if out is None:
+        out = states.new_empty(shape)
     parents = parents.contiguous()
-    (outer, outer_steps), (middle, middle_steps), (n, row_steps) = [(1, (0, 0))] * (3 - len(dims)) + dims
-    layouts = [BeamLayout(outer_steps[i], t.stride(at) * size, t.stride(at + 1) * size, middle_steps[i], row_steps[i])
-               for i, t in enumerate((states, out))]
     _r._run("lrs_beam_reorder", stream, (states, out, parents),
-            (states.data_ptr(), layouts[0], out.data_ptr(), layouts[1], parents.data_ptr(), outer, batch, beams, count,
-             middle, n, row), given)
+            (states.data_ptr(), from_layout, out.data_ptr(), to_layout, parents.data_ptr(), *sizes), given)
     return out

@@ -293,13 +293,13 @@ __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict
     // at most `error` but for that sum's rounding.  An exponential is off by (1.3 |d| + 2)
     // 2^-24 of itself; a sigmoid by a quarter of that (and |l| s (1 - s) is below 0.23), an
     // addition and a reciprocal, together less than 4 * 2^-24; a softmax's score by that
-    // (|d| s is below 0.37 of the largest), and by the additions of its sum.
+    // (|d| s is below 0.37 of the largest), and by the V + 6 additions of its sum.
     float error = 0.0f;
     bool close = false;  // too close for float32
     uint32_t key[V];
     if constexpr (SUMS) {
         const float each = 1.0f / sum;
-        error = a.sigmoid ? 4 * 0x1p-24f : 64 * 0x1p-24f * each;
+        error = a.sigmoid ? 4 * 0x1p-24f : (V + 16) * 0x1p-24f * each;
         const float shift = a.sigmoid ? 0.0f : top;
         const float by = a.sigmoid ? -1.44269504f : 1.44269504f;
 #pragma unroll
