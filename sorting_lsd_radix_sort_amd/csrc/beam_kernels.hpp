@@ -35,6 +35,9 @@ struct Part {
 // 2^(l * kLog2e) is exp(l * (1 - kLog2eLess)): log2(e) rounded to float32, and what that
 // takes from an exponent.
 constexpr float kLog2e = 1.44269504f;
+// Below this l * kLog2e - (top * kLog2e rounded) is formed by one fma: the rounding, half
+// a step of the product, is part of the base, and has to leave the exponent in range.
+constexpr float kOneProduct = 1e6f;
 constexpr double kLn2 = 0.693147180559945309417, kLog2eLess = 1.0 - (double)kLog2e * kLn2;
 
 // Of the first `n` <= kHeld candidates of a wave keeps the `count` best, in order, and
@@ -189,7 +192,7 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const T *__rest
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
-        if (__builtin_fabsf(top) < 1e38f) {
+        if (__builtin_fabsf(top) < kOneProduct) {
             const float base = -(top * kLog2e);
             add([&](float l) { return __builtin_fmaf(l, kLog2e, base); });
         } else {  // large ones, infinities, nothing at all; NaN shows
@@ -269,7 +272,7 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const T *__rest
             double sum = 0.0;
             for (int w = 0; w < kScanWaves; ++w) sum += sums[w];
             const double base = (double)-(top * kLog2e);
-            a.of_part[job] = Part{sum, __builtin_fabsf(top) < 1e38f ? (double)top * kLog2eLess - base * kLn2 : (double)top};
+            a.of_part[job] = Part{sum, __builtin_fabsf(top) < kOneProduct ? (double)top * kLog2eLess - base * kLn2 : (double)top};
         }
 }
 

@@ -543,3 +543,38 @@ def test_reorder_counts_as_a_write():
     assert states._version == 1 and parents._version == 0
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward()
+
+
+def test_served_batch_and_many_searches():
+    """Rows of several parts with the largest number of vectors a lane, and more searches
+    than a grid has workgroups in one step."""
+    torch = torch_()
+    announce("served batch")
+    for name in ("bf16", "f32"):
+        done = torch.from_numpy(np.random.default_rng(3).random((16, 8)) < 0.2).cuda()
+        check(randn((16, 8, 128257), name, 1), beam_scores(16, 8, 1), 16, finished=done, end_id=7)
+    many = (1 << 20) + 5
+    announce("many searches")
+    logits, scores = randn((many, 1, 5), "f32", 2), beam_scores(many, 1, 2)
+    s, p, t = lrs.beam_select(logits, scores, 2)
+    want = torch.topk(logits[:, 0].double(), 2, dim=1)  # (no two of these are equal)
+    assert torch.equal(t.long(), want.indices) and (p == 0).all()
+    total = torch.log_softmax(logits[:, 0].double(), 1).gather(1, want.indices) + scores.double()
+    off = (2 * math.log(5) + 12) * 2.0**-24
+    assert ((s.double() - total).abs() <= off + (total.abs() + off) * 2.0**-24).all()
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+def test_large_logits(name):
+    """Logits whose product with log2(e) no float32 holds, beside small ones in other parts."""
+    torch = torch_()
+    announce("large logits %s" % name)
+    logits = randn((4, 2, 20011), name, 5)
+    logits[0, 0, 17000] = 3e38
+    logits[1, 1, 3] = 2.9e38
+    logits[1, 1, 19000] = 3e38
+    logits[2] = -3e38
+    logits[2, :, 40] = -2.9e38
+    logits[3, 0] *= 1e37
+    for normalize in (True, False):
+        check(logits, beam_scores(4, 2, 1), 9, normalize)

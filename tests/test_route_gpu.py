@@ -569,3 +569,35 @@ def test_route_grad_counts_as_a_write():
     assert out._version == 1 and l._version == 0 and ids._version == 0 and w._version == 0
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward()
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("kind,biased,groups,kept", [("sigmoid", True, 8, 4), ("softmax", True, 8, 3),
+                                                     ("softmax", False, 1, 1), ("sigmoid", False, 4, 2)])
+def test_route_at_the_size_of_a_prompt(name, kind, biased, groups, kept):
+    """Thousands of tokens, of which some have scores that only float64 tells apart; logits
+    in float32 that were rounded to bfloat16 before, so that many are equal."""
+    torch = torch_()
+    announce("prompt %s %s %s %d" % (name, kind, biased, groups))
+    for experts, tokens in ((256, 8200), (160, 4099), (512, 2051)):
+        l = randn((tokens, experts), name, experts)
+        bias = biases(experts, 1) if biased else None
+        ids, w = check_route(l, 8, kind, bias, groups, kept, "top2", kind == "sigmoid", 2.5, "i64")
+        check_grad(randn((tokens, 8), "f32", 2), l, ids, kind, kind == "sigmoid", 2.5)
+        check_route(randn((tokens, experts), "bf16", 3).float(), 8, kind, bias, groups, kept, "max")
+
+
+def test_nan_in_groups_of_lanes():
+    """Groups that are whole vectors of neighbouring lanes: a NaN's group comes first."""
+    torch = torch_()
+    announce("nan in groups")
+    for name in ("f32", "bf16"):
+        l = randn((5, 64), name, 9)
+        l[1, 37], l[3, 63] = float("nan"), INF
+        for group_score in ("max", "top2"):
+            for bias in (None, biases(64, 1)):
+                ids, w = lrs.route_tokens(l, 4, "sigmoid", bias=bias, num_groups=4, kept_groups=1,
+                                          group_score=group_score)
+                assert ids[1, 0] == 37 and (ids[1] // 16 == 2).all() and w[1].isnan().all()
+                assert ids[3, 0] == 63 and (ids[3] // 16 == 3).all()
+                assert torch.isfinite(w[[0, 2, 3, 4]]).all()
