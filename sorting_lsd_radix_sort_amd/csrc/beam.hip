@@ -94,6 +94,11 @@ lrs_status beam_entry(void *d_temp, size_t *temp_bytes, lrs_row_type type, const
     return launched();
 }
 
+// States of more bytes than the last-level cache are read past the caches: 537 MB of 16
+// searches of 8 beams reordered in place in 140 us instead of 150, 1.07 GB in 283 instead
+// of 299; 134 MB of 4 searches take 38 instead of 32.
+constexpr int64_t kLastCacheBytes = (int64_t)256 << 20;
+
 // A state's memory from its first to its last byte, and whether its rows lie apart.
 struct Extent {
     bool ok, apart;
@@ -181,10 +186,13 @@ LRS_API lrs_status lrs_beam_reorder(const void *d_in, const lrs_beam_layout *in_
     const int64_t row_tiles = (a.all_rows + (kThreads >> a.tx_log2) - 1) / (kThreads >> a.tx_log2);
     const dim3 grid((unsigned)std::min(col_tiles, kMaxGridX), (unsigned)std::min(row_tiles, kMaxGridY),
                     (unsigned)((row_tiles + kMaxGridY - 1) / kMaxGridY));
+    const __int128 state_bytes = (__int128)a.all_rows * row_bytes * (beams + (in_place ? 0 : count));
     auto run = [&](auto w, auto most) {
         with_bool((1 << a.tx_log2) >= kWave, [&](auto wave) {
-            reorder_kernel<decltype(w), most.value, wave.value>
-                <<<grid, kThreads, 0, stream>>>(in_at, (char *)d_out, d_parents, src, dst, a);
+            with_bool(state_bytes > kLastCacheBytes, [&](auto nt) {
+                reorder_kernel<decltype(w), most.value, wave.value, nt.value>
+                    <<<grid, kThreads, 0, stream>>>(in_at, (char *)d_out, d_parents, src, dst, a);
+            });
         });
     };
     auto with_word = [&](auto most) {

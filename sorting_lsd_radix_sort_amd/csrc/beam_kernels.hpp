@@ -73,7 +73,19 @@ struct Scan {
 // the `count`-th largest of 64 maxima, each over an equal share of the part, so that
 // some 64 ln(64 / (64 - count)) logits reach it (18 for 16, above that the more).  Their
 // vectors are queued in LDS and taken apart there, a logit a thread.  (Where ties make
-// them too many, a wave keeps its best in a list of its own.)
+// them too many, a wave keeps its best in a list of its own: 512 rows of 131,072 bf16
+// logits in 71 us with the join if all are equal, 31 if none.)
+//
+// The part's sum: exponents by base 2 relative to the part's largest logit, eight or four
+// of them added in float32, the rest in float64, so that two totals' order is that of the
+// real numbers down to about 1e-8.
+//
+// Bound by HBM and by instructions about equally: 512 rows of 131,072 bf16 logits in 26
+// us, 134 MB at 5.2 TB/s (22 us without the sums, which are 6 instructions a logit and
+// 16 cycles of its exponential), float32 in 45 (5.9 TB/s).  66 registers a lane (what is
+// taken apart for the maxima is taken apart again), 256 threads a part (512: 4 us more
+// of bf16, 9 of float32; 128: 1 and 3), eight vectors a lane (four: 2 us more, two 15;
+// twelve 6, sixteen 53).  A first form, which kept a list and a bound per wave, took 84.
 template <typename T, bool SUM, int R>
 __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const T *__restrict__ logits, int64_t ld, Scan a)
 {
@@ -326,7 +338,10 @@ struct Totals {
 
 // One workgroup per search: the beams' log sums from their parts; then the candidates of
 // all parts at once, a few a thread, those that do not reach the `count`-th largest of 64
-// maxima left out, the others ranked by counting.
+// maxima left out, the others ranked by counting.  Bound by latency: 5 us for 4 beams of
+// 32,000 logits, 6 for 64 searches of 8 beams of 131,072 (512 candidates each); with 512
+// threads half a microsecond more, with 256 1.5.  Ranking every list's best first, then
+// the lists' next places in rounds, took 17 to 33.
 __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(Join a, int batch)
 {
     __shared__ Totals<kJoinThreads> of_thread;
@@ -481,7 +496,7 @@ struct Word1 {
 // a search: it has read what it needs of the old states before it stores the first of
 // the new ones, so they may be the same memory.  in and out are the same for the whole
 // wave, `at` is the lane's; parents too, where a wave serves one row.
-template <typename W, int MOST>
+template <typename W, int MOST, bool NT>
 __device__ __forceinline__ void move_column(const char *in, int64_t in_step, char *out, int64_t out_step, uint32_t at,
                                             const int32_t *parents, int beams, int count, bool in_place)
 {
@@ -499,16 +514,29 @@ __device__ __forceinline__ void move_column(const char *in, int64_t in_step, cha
     for (int j = MOST - 1; j >= 0; --j) spare = j < count && named(j) && !stays(j) ? p[j] : spare;
     T v[MOST];
 #pragma unroll
-    for (int j = 0; j < MOST; ++j)
-        v[j] = *reinterpret_cast<const T *>(in + (j < count && named(j) && !stays(j) ? p[j] : spare) * in_step + at);
+    for (int j = 0; j < MOST; ++j) {
+        const bool needed = j < count && named(j) && !stays(j);
+        const T *from = reinterpret_cast<const T *>(in + (needed ? p[j] : spare) * in_step + at);
+        if constexpr (NT)
+            v[j] = __builtin_nontemporal_load(from);
+        else
+            v[j] = *from;
+    }
 #pragma unroll
     for (int j = 0; j < MOST; ++j)
-        if (j < count && !stays(j)) __builtin_nontemporal_store(named(j) ? v[j] : T{}, reinterpret_cast<T *>(out + j * out_step + at));
+        if (j < count && !stays(j))
+            __builtin_nontemporal_store(named(j) ? v[j] : T{}, reinterpret_cast<T *>(out + j * out_step + at));
 }
 
-// WORD: the words that a row's last columns are moved in; MOST: beams whose
-// columns a lane holds at once (more of them one after another, not in place).
-template <typename WORD, int MOST, bool WAVE_ROW>
+// WORD: the words that a row's last columns are moved in; MOST: beams whose columns a
+// lane holds at once (more of them one after another, not in place); NT: loads past the
+// caches.
+//
+// Bound by HBM: caches of 16 searches of 8 beams, 795 MB read and written in place, in
+// 140 us (5.7 TB/s; a copy reaches 5.9), of one search of 4 beams (22 MB) in 5.4.  Stores
+// always go past the caches (155 us without, and 41 instead of 32 for 134 MB of states).
+// With a branch around each beam's load it took 364 us, and 244 registers.
+template <typename WORD, int MOST, bool WAVE_ROW, bool NT>
 __global__ __launch_bounds__(kThreads) void reorder_kernel(const char *in, char *out,
                                                            const int32_t *__restrict__ all_parents, Places from,
                                                            Places to, Reorder a)
@@ -532,10 +560,10 @@ __global__ __launch_bounds__(kThreads) void reorder_kernel(const char *in, char 
             if (x < a.tiles) {
                 const int64_t base = x << a.tx_log2;
                 if (base + lane < a.vecs)
-                    move_column<Vector, MOST>(src + base * 16, from.beam_step, dst + base * 16 + j * to.beam_step,
+                    move_column<Vector, MOST, NT>(src + base * 16, from.beam_step, dst + base * 16 + j * to.beam_step,
                                               to.beam_step, lane * 16, parents + j, a.beams, most, a.in_place);
             } else if (lane < (uint32_t)a.words) {
-                move_column<WORD, MOST>(src + a.vecs * 16, from.beam_step, dst + a.vecs * 16 + j * to.beam_step,
+                move_column<WORD, MOST, NT>(src + a.vecs * 16, from.beam_step, dst + a.vecs * 16 + j * to.beam_step,
                                         to.beam_step, lane * (uint32_t)sizeof(typename WORD::type), parents + j, a.beams,
                                         most, a.in_place);
             }
