@@ -117,7 +117,8 @@ typedef struct lrs_beam_layout {
  *  - d_out may be d_in (same pointer and layout, count <= 64): a beam that is its own
  *    parent is then neither read nor written for itself.  Otherwise they must not
  *    overlap: LRS_ERR_INVALID_ARG if the memory from first to last byte does.
- *  - The rows of d_out must not overlap one another; those of d_in may (a step of 0 is
+ *  - The rows of d_out must not overlap one another, which is taken from its steps: each
+ *    has to pass over all that the smaller ones reach.  Those of d_in may (a step of 0 is
  *    a state that beams share).  Steps are not negative; outer * batch * middle * rows
  *    is at most 2^31 - 1. */
 lrs_status lrs_beam_reorder(const void *d_in, const lrs_beam_layout *in_layout, void *d_out,

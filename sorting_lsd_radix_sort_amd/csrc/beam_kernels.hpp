@@ -18,9 +18,9 @@ constexpr int kHeld = 2 * kWave;                         // and that a wave hold
 
 // A candidate is its logit's order key above the complement of its token: larger is
 // better, and of equal logits the lowest token.
-__device__ __forceinline__ uint64_t candidate_of(float l, int token)
+__device__ __forceinline__ uint64_t candidate_of(float l, uint32_t token)
 {
-    return (uint64_t)key_of(l) << 32 | (uint32_t)~token;
+    return (uint64_t)key_of(l) << 32 | ~token;
 }
 
 __device__ __forceinline__ float logit_of(uint64_t c) { return value_of((uint32_t)(c >> 32)); }
@@ -96,7 +96,7 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const T *__rest
     __shared__ union {
         struct {
             u32x4 vector[kQueued];
-            int token[kQueued];
+            uint32_t token[kQueued];  // of a vector's first logit
         } queue;
         uint64_t of_wave[kScanWaves][kHeld];
     } held_all;
@@ -224,18 +224,20 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const T *__rest
         at = __builtin_amdgcn_readfirstlane(at) + __builtin_popcountll(those & ((1ull << lane) - 1));
         if (has && at < kQueued) {
             held_all.queue.vector[at] = r[j];
-            held_all.queue.token[at] = (int)from + (j * kScanThreads + tid) * VEC;
+            held_all.queue.token[at] = (uint32_t)from + (uint32_t)(j * kScanThreads + tid) * VEC;
         }
     }
     __syncthreads();
     const int vectors = queued;
     if (vectors <= kQueued)
         for (int at = tid; at < vectors * VEC; at += kScanThreads) {
-            const T *v = reinterpret_cast<const T *>(&held_all.queue.vector[at / VEC]);
-            const float l = (float)v[at % VEC];
+            constexpr int kPerWord = 4 / (int)sizeof(T);
+            const uint32_t word = held_all.queue.vector[at / VEC][at % VEC / kPerWord];
+            const u32x4 v = {word, 0u, 0u, 0u};
+            const float l = kPerWord == 2 && at % 2 ? element<T>(v, 1 % VEC) : element<T>(v, 0);
             if (l >= least) {
                 const int to = atomicAdd(&listed, 1);
-                if (to < kListed) list[to] = candidate_of(l, held_all.queue.token[at / VEC] + at % VEC);
+                if (to < kListed) list[to] = candidate_of(l, held_all.queue.token[at / VEC] + (uint32_t)(at % VEC));
             }
         }
     __syncthreads();
@@ -247,7 +249,7 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const T *__rest
         n = 0;
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            const int token = (int)from + (j * kScanThreads + tid) * VEC;
+            const uint32_t token = (uint32_t)from + (uint32_t)(j * kScanThreads + tid) * VEC;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 const float l = element<T>(r[j], i);
@@ -284,7 +286,8 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const T *__rest
             double sum = 0.0;
             for (int w = 0; w < kScanWaves; ++w) sum += sums[w];
             const double base = (double)-(top * kLog2e);
-            a.of_part[job] = Part{sum, __builtin_fabsf(top) < kOneProduct ? (double)top * kLog2eLess - base * kLn2 : (double)top};
+            const double of_fma = (double)top * kLog2eLess - base * kLn2;
+            a.of_part[job] = Part{sum, __builtin_fabsf(top) < kOneProduct ? of_fma : (double)top};
         }
 }
 
@@ -433,7 +436,8 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(Join a, int bat
                 // (of fewer than `count` there is none at that place, and all are taken)
                 const int i = tid / kRankLanes;
                 const int before = maxima.before(i, kWave);
-                if (tid % kRankLanes == 0 && before == a.count - 1) bound_key = maxima.key[i], bound_flat = maxima.flat[i];
+                if (tid % kRankLanes == 0 && before == a.count - 1)
+                    bound_key = maxima.key[i], bound_flat = maxima.flat[i];
             }
             __syncthreads();
             const Total bound{bound_key, bound_flat};
