@@ -133,13 +133,15 @@ def route_tokens(logits, slots: int, scores: str = "softmax", bias=None, num_gro
     best ("top2").  normalize: a token's weights are divided by their sum; all are
     multiplied by `scale`.  A logit of -inf takes no part; where nothing is left to
     choose the id is -1 and the weight 0, which group_tokens passes over.  dtype of the
-    ids: int32 (default) or int64; weights_dtype: float32 (default), bfloat16 or float16."""
+    ids: int32 (default) or int64; weights_dtype: float32 (default), bfloat16 or float16.
+    At most 64 slots, 64 groups and 2048 experts."""
     code = _r._row_code("logits", logits.dtype)
     score, group = _name("scores", SCORE_CODES, scores), _name("group_score", GROUP_SCORE_CODES, group_score)
     tokens, experts = _r._matrix("logits", logits)
     dtype, id_code = _id_dtype(dtype)
-    torch = _r._torch
-    weights_dtype = torch.float32 if weights_dtype is None else weights_dtype
+    float32 = _r._torch.float32
+    if weights_dtype is None:
+        weights_dtype = float32
     weight_code = _r._row_code("weights", weights_dtype)
     slots, num_groups = int(slots), int(num_groups)
     kept_groups = num_groups if kept_groups is None else int(kept_groups)
@@ -148,7 +150,7 @@ def route_tokens(logits, slots: int, scores: str = "softmax", bias=None, num_gro
     if not 0 <= slots <= kept_groups * (experts // num_groups):
         raise ValueError("%d slots, with %d experts to choose from" % (slots, kept_groups * (experts // num_groups)))
     if bias is not None:
-        if bias.dtype is not torch.float32:
+        if bias.dtype is not float32:
             raise TypeError("bias must be float32, not %s" % bias.dtype)
         if bias.dim() != 1 or bias.shape[0] != experts:
             raise ValueError("bias has shape %s, expected (%d,)" % (tuple(bias.shape), experts))
@@ -158,8 +160,8 @@ def route_tokens(logits, slots: int, scores: str = "softmax", bias=None, num_gro
     logits, ld = _r._rows_in(logits, tokens, experts)
     if bias is not None:
         bias = bias.contiguous()
-    ids = logits.new_empty((tokens, slots), dtype=dtype)
-    weights = logits.new_empty((tokens, slots), dtype=weights_dtype)
+    ids = logits.new_empty(tokens, slots, dtype=dtype)
+    weights = logits.new_empty(tokens, slots, dtype=weights_dtype)
     _r._run("lrs_route_tokens", stream, (logits, bias, ids, weights),
             (code, logits.data_ptr(), ld, tokens, experts, slots, score, _r._at(bias), num_groups, kept_groups, group,
              1 if normalize else 0, float(scale), id_code, ids.data_ptr(), weight_code, weights.data_ptr()))
@@ -207,7 +209,7 @@ def beam_select(logits, scores, count: int, normalize: bool = True, finished=Non
     beam i as int32, the token v as `dtype` (int32 by default, or int64).  A beam of score
     -inf takes no part.  finished (batch, beams), bool or uint8: such a beam offers only
     the token end_id, at its own score.  Where nothing is left the score is -inf, parent
-    and token -1."""
+    and token -1.  At most 64 continuations of at most 1024 beams."""
     code = _r._row_code("logits", logits.dtype)
     if logits.dim() != 3:
         raise ValueError("logits must have the shape (batch, beams, vocab), not %s" % (tuple(logits.shape),))
@@ -228,25 +230,23 @@ def beam_select(logits, scores, count: int, normalize: bool = True, finished=Non
         if not 0 <= end_id < vocab:
             raise ValueError("end_id %d is no token of %d" % (end_id, vocab))
     if vocab < 1 or not 0 <= count <= 64:
-        raise ValueError("count %d of a vocabulary of %d: count must be 0 to 64, the vocabulary not empty" % (count, vocab))
+        raise ValueError("count %d of a vocabulary of %d: count must be 0 to 64, the vocabulary not empty" %
+                         (count, vocab))
     if not logits.is_cuda:
         raise _r._host_tensor(logits)
     # one row per beam, equally far apart
-    if batch > 1 and beams > 1 and logits.stride(0) != beams * logits.stride(1):
-        logits = logits.contiguous()
+    to_batch, step, to_token = logits.stride()
+    if beams == 1:
+        step = to_batch
     rows = batch * beams
-    if batch and beams:
-        step = logits.stride(1) if beams > 1 else logits.stride(0)
-        if (vocab > 1 and logits.stride(2) != 1) or (rows > 1 and step < vocab):
-            logits, step = logits.contiguous(), vocab
-    else:
-        step = vocab
+    if rows > 1 and ((batch > 1 and to_batch != beams * step) or step < vocab) or (rows and vocab > 1 and to_token != 1):
+        logits, step = logits.contiguous(), vocab
     scores = scores.contiguous()
     if finished is not None:
         finished = finished.contiguous()
     new_scores = scores.new_empty(batch, count)
-    parents = scores.new_empty((batch, count), dtype=torch.int32)
-    tokens = scores.new_empty((batch, count), dtype=dtype)
+    parents = scores.new_empty(batch, count, dtype=torch.int32)
+    tokens = parents.new_empty(batch, count) if id_code == 0 else scores.new_empty(batch, count, dtype=dtype)
     args = (code, logits.data_ptr(), step, scores.data_ptr(), _r._at(finished), int(end_id), batch, beams, vocab, count,
             1 if normalize else 0, new_scores.data_ptr(), parents.data_ptr(), id_code, tokens.data_ptr())
     t, size = _r._temp("lrs_beam_select", (code, batch, beams, vocab, count), args, new_scores, temp)
@@ -309,13 +309,14 @@ def beam_reorder(states, parents, dim: int = 0, out=None, stream=None):
     ...], zeros where a parent is outside the beams.  states: any type of 1, 2, 4, 8 or 16
     bytes, with the batch in dimension `dim` and the beams in the next; parents (batch,
     count), int32, as beam_select returns them.  Returns `out`, a tensor of that shape
-    (`states` itself for the reordering in place, which moves only what has another
-    parent), or a new one.  Strides may be any that leave at most three dimensions beside
+    (`states` itself for the reordering in place, of at most 64 beams, which moves only
+    what has another parent), or a new one.  Strides may be any that leave at most three dimensions beside
     batch, beams and a contiguous piece: the filled part of a cache that has room for more
     will do, with layers in front and heads before or behind the positions."""
     if parents.dtype is not (_r._types or _r._type_codes())[2]:
         raise TypeError("parents must be int32, not %s" % parents.dtype)
-    key = (states.shape, states.stride(), dim, states.dtype, parents.shape, out is not None and (out.shape, out.stride()))
+    key = (states.shape, states.stride(), dim, states.dtype, parents.shape,
+           out is not None and (out.shape, out.stride()))
     plan = _plans.get(key)
     if plan is None:
         plan = _beam_plan(states.shape, states.stride(), dim, states.element_size(), parents.shape,

@@ -41,7 +41,8 @@ lrs_status beam_entry(void *d_temp, size_t *temp_bytes, lrs_row_type type, const
                       lrs_id_type id_type, void *d_tokens, hipStream_t stream)
 {
     if (temp_bytes == nullptr || !type_ok(type) || !type_ok(id_type) || !slots_ok(batch, beams) || vocab < 1 ||
-        !slots_ok(beams, vocab) || count < 0 || count > kMaxContinuations || beams > kMaxBeams || !shape_ok(batch * beams, vocab, ld) ||
+        !slots_ok(beams, vocab) || count < 0 || count > kMaxContinuations || beams > kMaxBeams ||
+        !shape_ok(batch * beams, vocab, ld) ||
         (d_finished != nullptr && (end_id < 0 || end_id >= vocab)))
         return LRS_ERR_INVALID_ARG;
     const int64_t b = bytes_of(type), rows = batch * beams, n = batch * count;
@@ -110,7 +111,8 @@ Extent extent_of(const lrs_beam_layout &l, int64_t outer, int64_t batch, int64_t
 {
     struct Dim {
         int64_t step, count;
-    } d[5] = {{l.outer_step, outer}, {l.batch_step, batch}, {l.beam_step, beams}, {l.middle_step, middle}, {l.row_step, rows}};
+    } d[5] = {{l.outer_step, outer}, {l.batch_step, batch}, {l.beam_step, beams}, {l.middle_step, middle},
+              {l.row_step, rows}};
     std::sort(d, d + 5, [](const Dim &a, const Dim &b) { return a.step < b.step; });
     Extent e{true, true, 0};
     __int128 end = row_bytes;
@@ -151,7 +153,8 @@ LRS_API lrs_status lrs_beam_reorder(const void *d_in, const lrs_beam_layout *in_
                                     int64_t row_bytes, hipStream_t stream)
 {
     if (in_layout == nullptr || out_layout == nullptr || !count_ok(outer) || !slots_ok(batch, beams) ||
-        !slots_ok(batch, count) || !count_ok(middle) || !count_ok(rows) || row_bytes < 0 || row_bytes > ((int64_t)1 << 56) ||
+        !slots_ok(batch, count) || !count_ok(middle) || !count_ok(rows) || row_bytes < 0 ||
+        row_bytes > ((int64_t)1 << 56) ||
         (__int128)outer * batch * middle * rows > kMaxCount)
         return LRS_ERR_INVALID_ARG;
     if (outer == 0 || batch == 0 || count == 0 || middle == 0 || rows == 0 || row_bytes == 0) return LRS_OK;

@@ -578,3 +578,30 @@ def test_large_logits(name):
     logits[3, 0] *= 1e37
     for normalize in (True, False):
         check(logits, beam_scores(4, 2, 1), 9, normalize)
+
+
+def test_calls_at_once():
+    """Calls on two streams at the same time, each with its own tensors, and temp storage
+    that is not one block."""
+    torch = torch_()
+    announce("two streams at once")
+    sizes = ((3, 4, 50001), (40, 8, 3001))
+    new = [search_state(*size, 40 + i) for i, size in enumerate(sizes)]
+    states = [{n: v.clone() if n != "count" else v for n, v in s.items()} for s in new]
+    want = []
+    for s in new:
+        want.append([search_step(s) for _ in range(4)])
+    streams = [torch.cuda.Stream() for _ in sizes]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got[i].append(search_step(states[i]))
+    torch.cuda.synchronize()
+    for a, b, s, other in zip(got, want, states, new):
+        assert all(torch.equal(x, y) for one, two in zip(a, b) for x, y in zip(one, two))
+        assert torch.equal(s["cache"], other["cache"]) and torch.equal(s["tokens"], other["tokens"])
+    with pytest.raises(ValueError, match="temp must be contiguous"):
+        lrs.beam_select(states[0]["logits"], states[0]["scores"], 4,
+                        temp=torch.zeros(4096, 4096, dtype=torch.uint8, device="cuda")[:, :2048])
