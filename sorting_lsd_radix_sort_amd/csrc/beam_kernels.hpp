@@ -77,8 +77,8 @@ struct Scan {
 // logits in 71 us with the join if all are equal, 31 if none.)
 //
 // The part's sum: exponents by base 2 relative to the part's largest logit, eight or four
-// of them added in float32, the rest in float64, so that two totals' order is that of the
-// real numbers down to about 1e-8.
+// of them added in float32, the rest in float64: its logarithm is off by 5e-8 on average,
+// the share of log2(e)'s rounding (1.3e-8 of a logit's distance from the largest).
 //
 // Bound by HBM and by instructions about equally: 512 rows of 131,072 bf16 logits in 26
 // us, 134 MB at 5.2 TB/s (22 us without the sums, which are 6 instructions a logit and
