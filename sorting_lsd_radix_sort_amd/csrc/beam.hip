@@ -95,10 +95,11 @@ lrs_status beam_entry(void *d_temp, size_t *temp_bytes, lrs_row_type type, const
     return launched();
 }
 
-// States of more bytes than the last-level cache are read past the caches: 537 MB of 16
-// searches of 8 beams reordered in place in 140 us instead of 150, 1.07 GB in 283 instead
-// of 299; 134 MB of 4 searches take 38 instead of 32.
-constexpr int64_t kLastCacheBytes = (int64_t)256 << 20;
+// States of more bytes than the last-level cache keeps beside what is written are read past
+// the caches: of 16 searches of 8 beams (537 MB) in place in 133 us instead of 149, into
+// others in 153 instead of 159, 201 MB in place in 52 instead of 57.  134 MB would take 35
+// instead of 32, and 67 MB written eight times over 108 instead of 87.
+constexpr int64_t kReadPastBytes = (int64_t)160 << 20;
 
 // A state's memory from its first to its last byte, and whether its rows lie apart.
 struct Extent {
@@ -189,30 +190,41 @@ LRS_API lrs_status lrs_beam_reorder(const void *d_in, const lrs_beam_layout *in_
     const int64_t row_tiles = (a.all_rows + (kThreads >> a.tx_log2) - 1) / (kThreads >> a.tx_log2);
     const dim3 grid((unsigned)std::min(col_tiles, kMaxGridX), (unsigned)std::min(row_tiles, kMaxGridY),
                     (unsigned)((row_tiles + kMaxGridY - 1) / kMaxGridY));
-    const __int128 state_bytes = (__int128)a.all_rows * row_bytes * (beams + (in_place ? 0 : count));
-    auto run = [&](auto w, auto most) {
-        with_bool((1 << a.tx_log2) >= kWave, [&](auto wave) {
-            with_bool(state_bytes > kLastCacheBytes, [&](auto nt) {
-                reorder_kernel<decltype(w), most.value, wave.value, nt.value>
-                    <<<grid, kThreads, 0, stream>>>(in_at, (char *)d_out, d_parents, src, dst, a);
-            });
+    const __int128 read_bytes = (__int128)a.all_rows * row_bytes * std::min(beams, count);
+    auto run = [&](auto w, auto most, auto wave) {
+        with_bool(read_bytes >= kReadPastBytes, [&](auto nt) {
+            reorder_kernel<decltype(w), most.value, wave.value, nt.value>
+                <<<grid, kThreads, 0, stream>>>(in_at, (char *)d_out, d_parents, src, dst, a);
         });
     };
-    auto with_word = [&](auto most) {
+    auto with_word = [&](auto most, auto wave) {
         if (word == 4)
-            run(Word4{}, most);
+            run(Word4{}, most, wave);
         else if (word == 2)
-            run(Word2{}, most);
+            run(Word2{}, most, wave);
         else
-            run(Word1{}, most);
+            run(Word1{}, most, wave);
     };
-    if (count <= 4)
-        with_word(std::integral_constant<int, 4>{});
-    else if (count <= 8 || !in_place)
-        with_word(std::integral_constant<int, 8>{});
-    else if (count <= 16)
-        with_word(std::integral_constant<int, 16>{});
-    else
-        with_word(std::integral_constant<int, 64>{});
+    // MOST, by the beams.  A wave's row: 22 MB of 4 beams in 4.9 us with 4 and 5.4 with 16,
+    // 537 MB of 8 beams in 133 with 16, which takes 94 registers; with 64 it is 255, and 537
+    // MB of 32 take 157.  Narrower rows: 67 MB of 8 beams in 17.9 with 8 and 22.7 with 16.
+    // Beams behind MOST follow one after another, but in place all are held at once.
+    if ((1 << a.tx_log2) >= kWave) {
+        constexpr std::true_type wave{};
+        if (count <= 4)
+            with_word(std::integral_constant<int, 4>{}, wave);
+        else if (count <= 16 || !in_place)
+            with_word(std::integral_constant<int, 16>{}, wave);
+        else
+            with_word(std::integral_constant<int, 64>{}, wave);
+    } else {
+        constexpr std::false_type wave{};
+        if (count <= 8)
+            with_word(std::integral_constant<int, 8>{}, wave);
+        else if (count <= 16 || !in_place)
+            with_word(std::integral_constant<int, 16>{}, wave);
+        else
+            with_word(std::integral_constant<int, 64>{}, wave);
+    }
     return launched();
 }

@@ -496,40 +496,128 @@ struct Word1 {
     typedef uint8_t type;
 };
 
+// Encoding of a wait for the vector memory counter at zero, and for nothing else.
+constexpr int kLoadsDone = 0x0F70;
+
+// What a wave does that serves one row: p[i] is the parent of beam i, and takers[i] the
+// beams that its state goes to, if i is the first of them; zeroed, the beams without one.
+template <int MOST>
+struct Moves {
+    using Beams = std::conditional_t<(MOST > 32), uint64_t, uint32_t>;  // a bit for each
+    int p[MOST];
+    Beams takers[MOST], zeroed;
+};
+
+// Found by the wave's first lanes, one for a beam: all lanes call it.  (With the beams
+// compared pair by pair in scalar registers, 9 of 5 beams, 9 MB, took 7.9 us instead of 4.7.)
+template <int MOST>
+__device__ __forceinline__ Moves<MOST> wave_moves(const int32_t *parents, int beams, int count, bool in_place)
+{
+    const int lane = threadIdx.x & (kWave - 1);
+    const int parent = lane < count ? parents[lane] : -1;
+    const bool named = (uint32_t)parent < (uint32_t)beams;
+    using Beams = typename Moves<MOST>::Beams;
+    const Beams needed = (Beams)__ballot(named && !(in_place && parent == lane));
+    Moves<MOST> m;
+    m.zeroed = (Beams)__ballot(lane < count && !named);
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {
+        m.p[i] = __builtin_amdgcn_readlane(parent, i);
+        const Beams same = (Beams)__ballot(parent == m.p[i]) & needed;
+        m.takers[i] = (same & (0 - same)) == (Beams)1 << i ? same : 0;
+    }
+    return m;
+}
+
 // A lane moves one column, of 16 bytes or (at a row's end) of one word, of all beams of
 // a search: it has read what it needs of the old states before it stores the first of
 // the new ones, so they may be the same memory.  in and out are the same for the whole
-// wave, `at` is the lane's; parents too, where a wave serves one row.
+// wave, `at` is the lane's.  Each state that is needed is read once.
 template <typename W, int MOST, bool NT>
 __device__ __forceinline__ void move_column(const char *in, int64_t in_step, char *out, int64_t out_step, uint32_t at,
-                                            const int32_t *parents, int beams, int count, bool in_place)
+                                            const Moves<MOST> &m)
+{
+    using T = typename W::type;
+    T v[MOST];
+#pragma unroll
+    for (int i = 0; i < MOST; ++i)
+        if (m.takers[i] != 0) {
+            const T *from = reinterpret_cast<const T *>(in + m.p[i] * in_step + at);
+            if constexpr (NT)
+                v[i] = __builtin_nontemporal_load(from);
+            else
+                v[i] = *from;
+        }
+    // all loads are waited for here: a wait among the stores would be for stores too
+    __builtin_amdgcn_s_waitcnt(kLoadsDone);
+    auto store = [&](auto beams, T value) {
+#pragma unroll 1
+        for (; beams != 0; beams &= beams - 1)
+            __builtin_nontemporal_store(value, reinterpret_cast<T *>(out + __builtin_ctzll(beams) * out_step + at));
+    };
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) store(m.takers[i], v[i]);
+    store(m.zeroed, T{});
+}
+
+// The same where a wave serves several rows, whose parents may differ: a lane finds out
+// by itself who takes what.
+template <typename W, int MOST, bool NT>
+__device__ __forceinline__ void move_lane_column(const char *in, int64_t in_step, char *out, int64_t out_step,
+                                                 uint32_t at, const int32_t *parents, int beams, int count,
+                                                 bool in_place)
 {
     using T = typename W::type;
     int p[MOST];  // all of them first: each is a load
 #pragma unroll
     for (int j = 0; j < MOST; ++j) p[j] = parents[j < count ? j : 0];
-    // a beam whose state is not needed (its own parent in place, no parent at all) loads
-    // another's again, or the first, which is always there: branches between the loads
-    // cost more
     auto named = [&](int j) { return (uint32_t)p[j] < (uint32_t)beams; };
     auto stays = [&](int j) { return in_place && p[j] == j && named(j); };
-    int spare = 0;
-#pragma unroll
-    for (int j = MOST - 1; j >= 0; --j) spare = j < count && named(j) && !stays(j) ? p[j] : spare;
+    auto needed = [&](int j) { return j < count && named(j) && !stays(j); };
     T v[MOST];
+    if constexpr (MOST <= 16) {
+        // the first of the beams that have a parent loads it, for all of them
+        bool leads[MOST];
 #pragma unroll
-    for (int j = 0; j < MOST; ++j) {
-        const bool needed = j < count && named(j) && !stays(j);
-        const T *from = reinterpret_cast<const T *>(in + (needed ? p[j] : spare) * in_step + at);
-        if constexpr (NT)
-            v[j] = __builtin_nontemporal_load(from);
-        else
-            v[j] = *from;
+        for (int j = 0; j < MOST; ++j) {
+            leads[j] = needed(j);
+#pragma unroll
+            for (int i = 0; i < j; ++i) leads[j] = leads[j] && !(leads[i] && p[i] == p[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < MOST; ++j)
+            if (leads[j]) {
+                const T *from = reinterpret_cast<const T *>(in + p[j] * in_step + at);
+                if constexpr (NT)
+                    v[j] = __builtin_nontemporal_load(from);
+                else
+                    v[j] = *from;
+            }
+        __builtin_amdgcn_s_waitcnt(kLoadsDone);
+#pragma unroll
+        for (int i = 0; i < MOST; ++i) {
+            if (!leads[i]) continue;
+#pragma unroll
+            for (int j = i; j < MOST; ++j)
+                if (needed(j) && p[j] == p[i])
+                    __builtin_nontemporal_store(v[i], reinterpret_cast<T *>(out + j * out_step + at));
+        }
+    } else {
+        // (a beam whose state is not needed loads another's again, or the first, which is
+        // always there)
+        int spare = 0;
+#pragma unroll
+        for (int j = MOST - 1; j >= 0; --j) spare = needed(j) ? p[j] : spare;
+#pragma unroll
+        for (int j = 0; j < MOST; ++j)
+            v[j] = *reinterpret_cast<const T *>(in + (needed(j) ? p[j] : spare) * in_step + at);
+#pragma unroll
+        for (int j = 0; j < MOST; ++j)
+            if (needed(j)) __builtin_nontemporal_store(v[j], reinterpret_cast<T *>(out + j * out_step + at));
     }
 #pragma unroll
     for (int j = 0; j < MOST; ++j)
-        if (j < count && !stays(j))
-            __builtin_nontemporal_store(named(j) ? v[j] : T{}, reinterpret_cast<T *>(out + j * out_step + at));
+        if (j < count && !named(j)) __builtin_nontemporal_store(T{}, reinterpret_cast<T *>(out + j * out_step + at));
 }
 
 // WORD: the words that a row's last columns are moved in; MOST: beams whose columns a
@@ -537,9 +625,11 @@ __device__ __forceinline__ void move_column(const char *in, int64_t in_step, cha
 // caches.
 //
 // Bound by HBM: caches of 16 searches of 8 beams, 795 MB read and written in place, in
-// 140 us (5.7 TB/s; a copy reaches 5.9), of one search of 4 beams (22 MB) in 5.4.  Stores
-// always go past the caches (155 us without, and 41 instead of 32 for 134 MB of states).
-// With a branch around each beam's load it took 364 us, and 244 registers.
+// 133 us (5.9 TB/s, a copy's rate), of one search of 4 beams (22 MB) in 4.9.  A state that
+// several beams take is read once: with a load for each beam, which the caches do not
+// answer when it goes past them, 140; 9 beams that take one's 27 MB each in 42 us instead
+// of 94.  Stores always go past the caches (154 us without, and 41 instead of 32 for 134
+// MB of states).
 template <typename WORD, int MOST, bool WAVE_ROW, bool NT>
 __global__ __launch_bounds__(kThreads) void reorder_kernel(const char *in, char *out,
                                                            const int32_t *__restrict__ all_parents, Places from,
@@ -561,16 +651,22 @@ __global__ __launch_bounds__(kThreads) void reorder_kernel(const char *in, char 
 #pragma unroll 1
         for (int j = 0; j < a.count; j += MOST) {
             const int most = a.count - j < MOST ? a.count - j : MOST;
-            if (x < a.tiles) {
-                const int64_t base = x << a.tx_log2;
-                if (base + lane < a.vecs)
-                    move_column<Vector, MOST, NT>(src + base * 16, from.beam_step, dst + base * 16 + j * to.beam_step,
-                                              to.beam_step, lane * 16, parents + j, a.beams, most, a.in_place);
-            } else if (lane < (uint32_t)a.words) {
-                move_column<WORD, MOST, NT>(src + a.vecs * 16, from.beam_step, dst + a.vecs * 16 + j * to.beam_step,
-                                        to.beam_step, lane * (uint32_t)sizeof(typename WORD::type), parents + j, a.beams,
-                                        most, a.in_place);
-            }
+            auto move = [&](auto word, int64_t base, uint32_t at, bool mine) {
+                using W = decltype(word);
+                const char *in_at = src + base;
+                char *out_at = dst + base + j * to.beam_step;
+                if constexpr (WAVE_ROW) {
+                    const Moves<MOST> m = wave_moves<MOST>(parents + j, a.beams, most, a.in_place);
+                    if (mine) move_column<W, MOST, NT>(in_at, from.beam_step, out_at, to.beam_step, at, m);
+                } else if (mine) {
+                    move_lane_column<W, MOST, NT>(in_at, from.beam_step, out_at, to.beam_step, at, parents + j,
+                                                  a.beams, most, a.in_place);
+                }
+            };
+            if (x < a.tiles)
+                move(Vector{}, x << a.tx_log2 << 4, lane * 16, (x << a.tx_log2) + lane < a.vecs);
+            else
+                move(WORD{}, a.vecs * 16, lane * (uint32_t)sizeof(typename WORD::type), lane < (uint32_t)a.words);
         }
     }
 }
