@@ -412,6 +412,27 @@ def test_reorder_layouts():
     assert lrs.beam_reorder(torch.zeros(2, 3, 4, device="cuda"), parents[:, :0]).shape == (2, 0, 4)
 
 
+@pytest.mark.parametrize("beams", [3, 8, 16, 20, 40])
+@pytest.mark.parametrize("width", [7, 1001])
+def test_reorder_large_states(beams, width):
+    """States that are read past the caches, in rows of less than a wave and more: beams
+    that share a parent in one step of the kernel's and in different ones."""
+    torch = torch_()
+    batch, rows = 3, 176 * 2**20 // (3 * beams * width * 4) + 1
+    states = pattern((batch, beams, rows, width + 1), torch.int32, beams)[..., :width]
+    for count in (beams, 2 * beams + 1):
+        parents = parents_of(batch, min(beams, 6), count, beams)
+        parents[1, ::3], parents[2, 1] = 0, -1
+        at = parents.clamp(min=0).long()
+        want = torch.stack([states[b][at[b]] for b in range(batch)]) * (parents >= 0)[:, :, None, None].int()
+        announce("reorder %s to %d" % (tuple(states.shape), count))
+        assert torch.equal(lrs.beam_reorder(states, parents), want)
+        if count == beams:
+            buffer = states.clone()
+            lrs.beam_reorder(buffer, parents, out=buffer)
+            assert torch.equal(buffer, want)
+
+
 def test_reorder_far_states_and_many_rows():
     torch = torch_()
     announce("far states")
