@@ -125,8 +125,9 @@ typedef struct lrs_beam_layout {
  *    overlap: LRS_ERR_INVALID_ARG if the memory from first to last byte does.
  *  - The rows of d_out must not overlap one another, which is taken from its steps: each
  *    has to pass over all that the smaller ones reach.  Those of d_in may (a step of 0 is
- *    a state that beams share).  Steps are not negative; outer * batch * middle * rows
- *    is at most 2^31 - 1. */
+ *    a state that beams share), but not in place, where one search would write what
+ *    another reads.  Steps are not negative; outer * batch * middle * rows is at most
+ *    2^31 - 1. */
 lrs_status lrs_beam_reorder(const void *d_in, const lrs_beam_layout *in_layout, void *d_out,
                             const lrs_beam_layout *out_layout, const int32_t *d_parents, int64_t outer,
                             int64_t batch, int64_t beams, int64_t count, int64_t middle, int64_t rows,

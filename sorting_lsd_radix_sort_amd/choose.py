@@ -309,8 +309,8 @@ def beam_reorder(states, parents, dim: int = 0, out=None, stream=None):
     ...], zeros where a parent is outside the beams.  states: any type of 1, 2, 4, 8 or 16
     bytes, with the batch in dimension `dim` and the beams in the next; parents (batch,
     count), int32, as beam_select returns them.  Returns `out`, a tensor of that shape
-    (`states` itself for the reordering in place, of at most 64 beams, which moves only
-    what has another parent), or a new one.  Strides may be any that leave at most three dimensions beside
+    (`states` itself for the reordering in place, of at most 64 beams whose memory lies
+    apart, which moves only what has another parent), or a new one.  Strides may be any that leave at most three dimensions beside
     batch, beams and a contiguous piece: the filled part of a cache that has room for more
     will do, with layers in front and heads before or behind the positions."""
     if parents.dtype is not (_r._types or _r._type_codes())[2]:

@@ -167,7 +167,8 @@ LRS_API lrs_status lrs_beam_reorder(const void *d_in, const lrs_beam_layout *in_
     const bool in_place = from.at == to.at && same_steps(*in_layout, *out_layout, outer, batch, std::max(beams, count),
                                                           middle, rows);
     if (!array_ok(from, 1) || !array_ok(to, 1) || !array_ok(parents, 4) || overlap(to, parents) ||
-        (in_place ? count > kMaxContinuations : overlap(to, from)))
+        // (in place more beams before than after may share memory where those after do not)
+        (in_place ? count > kMaxContinuations || !in.apart : overlap(to, from)))
         return LRS_ERR_INVALID_ARG;
 
     const int word = row_bytes % 4 == 0 ? 4 : row_bytes % 2 == 0 ? 2 : 1;

@@ -412,6 +412,19 @@ def test_reorder_layouts():
     assert lrs.beam_reorder(torch.zeros(2, 3, 4, device="cuda"), parents[:, :0]).shape == (2, 0, 4)
 
 
+def test_reorder_of_windows():
+    """States of which two searches share some: moved into other memory, refused in place."""
+    torch = torch_()
+    announce("windows")
+    buffer = pattern((9, 40), torch.float32, 1)
+    states = buffer.as_strided((8, 2, 40), (40, 40, 1))
+    parents, before = parents_of(8, 2, 1, 1), bits(buffer).clone()
+    with pytest.raises(lrs.LrsError):
+        lrs.beam_reorder(states, parents, out=buffer[:8].unsqueeze(1))
+    assert torch.equal(bits(buffer), before)
+    assert torch.equal(bits(lrs.beam_reorder(states, parents)), reordered(states, parents, 0))
+
+
 @pytest.mark.parametrize("beams", [3, 8, 16, 20, 40])
 @pytest.mark.parametrize("width", [7, 1001])
 def test_reorder_large_states(beams, width):

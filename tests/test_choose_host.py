@@ -113,6 +113,20 @@ def test_beam_reorder_refusals(kw):
     refuses(reorder, **kw)
 
 
+@pytest.mark.parametrize("kw", [
+    # a search's old beams behind the new ones are the next search's new ones
+    dict(batch=4, beams=8, count=4, src_steps=(1 << 20, 4 << 12, 1 << 12, 1 << 11, 1 << 8)),
+    dict(batch=4, beams=5, count=4, src_steps=(1 << 20, 4 << 12, 1 << 12, 1 << 11, 1 << 8)),
+    # both steps the same
+    dict(outer=1, batch=8, beams=2, count=1, middle=1, rows=1, src_steps=(0, 256, 256, 0, 0)),
+    # beams that end within the next layer
+    dict(outer=2, batch=1, beams=6, count=4, src_steps=(4 << 12, 0, 1 << 12, 1 << 11, 1 << 8))])
+def test_beam_reorder_in_place_refuses_states_that_share_memory(kw):
+    """The new states lie apart, the old ones do not: what one search writes, another would
+    read.  Into other memory such states may be reordered."""
+    refuses(reorder, **{"dst": A, "dst_steps": kw["src_steps"], **kw})
+
+
 def test_beam_reorder_needs_layouts_and_passes_over_nothing():
     lib = lrs.load_library()
     assert lib.lrs_beam_reorder(A, None, B, None, C, 1, 1, 1, 1, 1, 1, 16, None) == lrs.LRS_ERR_INVALID_ARG
