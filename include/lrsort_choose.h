@@ -89,8 +89,10 @@ lrs_status lrs_route_tokens_grad(lrs_row_type type, const void *d_logits, int64_
  *   total[b,i,v] = scores[b,i] + l[b,i,v] - log(sum over v of exp(l[b,i,v]))   normalize != 0
  *   total[b,i,v] = scores[b,i] + l[b,i,v]                                      normalize == 0
  * d_out_scores (batch x count, float32) gets the largest totals, d_parents (int32) their
- * i and d_tokens (id_type) their v; equal totals go to the lowest i, then v.
- *  - Tokens of one beam are compared by their logits, beams by totals in float64.  Sums
+ * i and d_tokens (id_type) their v; equal totals go to the lowest i, equal logits of one
+ * beam to the lowest v.
+ *  - Tokens of one beam are compared by their logits (also where a large score, an
+ *    infinite one or NaN makes their totals the same), beams by totals in float64.  Sums
  *    of exponentials add up float32 ones in float64: their logarithms are off by less
  *    than 1.2e-7 where that was measured (mostly by 5e-8 alike for all beams), by (2
  *    log(vocab) + 12) * 2^-24 at most, and totals of two beams closer than that may

@@ -204,7 +204,7 @@ def beam_select(logits, scores, count: int, normalize: bool = True, finished=Non
                 temp=None, stream=None):
     """The `count` best continuations of each search: of all totals scores[b, i] +
     log_softmax(logits[b, i])[v] (normalize False: + logits[b, i, v]) the largest, equal
-    ones by the lowest i, then v.  logits (batch, beams, vocab); scores (batch, beams),
+    ones by the lowest i, then the largest logit, then the lowest v.  logits (batch, beams, vocab); scores (batch, beams),
     float32.  Returns (new scores, parents, tokens), each (batch, count): float32, the
     beam i as int32, the token v as `dtype` (int32 by default, or int64).  A beam of score
     -inf takes no part.  finished (batch, beams), bool or uint8: such a beam offers only

@@ -88,10 +88,13 @@ lrs_status beam_entry(void *d_temp, size_t *temp_bytes, lrs_row_type type, const
         });
         if (done != LRS_OK) return done;
     }
+    uint8_t token_bits = 0;
+    while (vocab > (int64_t)1 << token_bits) ++token_bits;
     const Join join{d_scores, d_finished, (const uint64_t *)temp, (const Part *)(temp + s.best_bytes), d_out_scores,
-                    d_parents, d_tokens, (int)beams, (int)vocab, (int)s.parts, (int)count, (int)end_id,
-                    normalize != 0, id_type == LRS_ID_I64};
-    beam_join_kernel<<<(unsigned)std::min(batch, kMaxGridX), kJoinThreads, 0, stream>>>(join, (int)batch);
+                    d_parents, d_tokens, (int)beams, (int)s.parts, (int)count, (int)end_id,
+                    normalize != 0, id_type == LRS_ID_I64, token_bits};
+    const dim3 searches((unsigned)std::min(batch, kMaxGridX), (unsigned)((batch + kMaxGridX - 1) / kMaxGridX));
+    beam_join_kernel<<<searches, kJoinThreads, 0, stream>>>(join, (int)batch);
     return launched();
 }
 

@@ -24,7 +24,6 @@ __device__ __forceinline__ uint64_t candidate_of(float l, uint32_t token)
 }
 
 __device__ __forceinline__ float logit_of(uint64_t c) { return value_of((uint32_t)(c >> 32)); }
-__device__ __forceinline__ int token_of(uint64_t c) { return (int)~(uint32_t)c; }
 
 // What is left of a part of a row beside its best candidates: the sum of its exp(l) is
 // sum * exp(base).
@@ -301,8 +300,8 @@ struct Join {
     float *out_scores;
     int32_t *parents;
     void *tokens;
-    int beams, vocab, parts, count, end_id;
-    uint8_t normalize, wide_ids;
+    int beams, parts, count, end_id;
+    uint8_t normalize, wide_ids, token_bits;  // bits that hold any token
 };
 
 constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / kWave;
@@ -311,25 +310,32 @@ constexpr int kJoinBlock = kJoinThreads * kJoinHeld;  // and the workgroup
 constexpr int kRankLanes = 16;                        // lanes that rank one together
 constexpr int kRanked = kJoinThreads / kRankLanes;
 
-// A continuation: its total's order key (float64), then its beam and token.
+// A continuation: its total's order key (float64), and by what equal totals are told
+// apart, larger being better: the beam (the lowest first), then the order key of its
+// logit, which a total may have swallowed, then the token (the lowest first).  Beams
+// times tokens are below 2^31, so that the bits of both are 32 at most.
 struct Total {
-    uint64_t key;
-    uint32_t flat;  // beam * vocab + token; ~0: none
+    uint64_t key, place;  // 0, 0: none
 };
 
 __device__ __forceinline__ bool better(const Total &a, const Total &b)
 {
-    return a.key > b.key || (a.key == b.key && a.flat < b.flat);
+    return a.key > b.key || (a.key == b.key && a.place > b.place);
+}
+
+__device__ __forceinline__ uint64_t place_of(const Join &a, int beam, uint64_t candidate)
+{
+    const uint64_t before_token = (uint64_t)(uint32_t)(a.beams - 1 - beam) << 32 | candidate >> 32;
+    return before_token << a.token_bits | __builtin_amdgcn_ubfe((uint32_t)candidate, 0, a.token_bits);
 }
 
 // Totals in LDS, and how many of the first n are better than the i-th: for the 16 lanes
 // that ask for the same i.
 template <int SIZE>
 struct Totals {
-    uint64_t key[SIZE];
-    uint32_t flat[SIZE];
-    __device__ __forceinline__ Total at(int i) const { return {key[i], flat[i]}; }
-    __device__ __forceinline__ void set(int i, const Total &t) { key[i] = t.key, flat[i] = t.flat; }
+    uint64_t key[SIZE], place[SIZE];
+    __device__ __forceinline__ Total at(int i) const { return {key[i], place[i]}; }
+    __device__ __forceinline__ void set(int i, const Total &t) { key[i] = t.key, place[i] = t.place; }
     __device__ __forceinline__ int before(int i, int n) const
     {
         const Total mine = at(i);
@@ -347,125 +353,127 @@ struct Totals {
 // the lists' next places in rounds, took 17 to 33.
 __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(Join a, int batch)
 {
-    __shared__ Totals<kJoinThreads> of_thread;
+    // (a thread's best are looked at for the bound, before what reaches it is taken)
+    __shared__ union {
+        Totals<kJoinThreads> of_thread;
+        Totals<kJoinBlock + kMaxBeams> taken;
+    } all_totals;
+    auto &of_thread = all_totals.of_thread;
+    auto &taken = all_totals.taken;
     __shared__ Totals<kWave> maxima;
     __shared__ Totals<kMaxContinuations> kept;
-    __shared__ Totals<kJoinBlock + kMaxBeams> taken;
     __shared__ double norm[kMaxBeams];  // of each beam: what its logits are less
     __shared__ float score[kMaxBeams];  // -infinity: takes no part
     __shared__ int taken_count;
-    __shared__ uint64_t bound_key;
-    __shared__ uint32_t bound_flat;
+    __shared__ Total bound_total;
     const int tid = (int)threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const float none = -__builtin_inff();
-    const Total nothing{0ull, ~0u};
+    const Total nothing{0ull, 0ull};
     const int lists = a.beams * a.parts;
     const int64_t all = (int64_t)lists * a.count;
 
-    for (int64_t b = blockIdx.x; b < batch; b += kMaxGridX) {
-        // the first block's candidates are on their way while the sums are formed
-        uint64_t c[kJoinHeld];
-        auto load = [&](int64_t base) {
+    const int64_t b = blockIdx.y * kMaxGridX + blockIdx.x;
+    if (b >= batch) return;
+    // the first block's candidates are on their way while the sums are formed
+    uint64_t c[kJoinHeld];
+    auto load = [&](int64_t base) {
 #pragma unroll
-            for (int i = 0; i < kJoinHeld; ++i) {
-                const int64_t at = base + i * kJoinThreads + tid;
-                c[i] = at < all ? a.best[b * all + at] : 0ull;
-            }
-        };
-        load(0);
-        for (int beam = wave; beam < a.beams; beam += kJoinWaves) {
-            const int64_t row = b * a.beams + beam;
-            const float s = a.scores[row];
-            const bool over = a.finished != nullptr && a.finished[row] != 0;
-            double less = 0.0;
-            if (a.normalize && s != none && !over) {
-                double high = (double)none;
-                for (int p = lane; p < a.parts; p += kWave)
-                    high = __builtin_fmax(high, a.of_part[row * a.parts + p].base);
-#pragma unroll
-                for (int d = 1; d < kWave; d *= 2) high = __builtin_fmax(high, __shfl_xor(high, d, kWave));
-                double sum = 0.0;
-                for (int p = lane; p < a.parts; p += kWave) {
-                    const Part q = a.of_part[row * a.parts + p];
-                    sum += q.base == (double)none ? q.sum : q.sum * exp(q.base - high);
-                }
-                less = high + log(team_sum64<kWave>(sum));
-            }
-            if (lane == 0) norm[beam] = less, score[beam] = over ? none : s;
+        for (int i = 0; i < kJoinHeld; ++i) {
+            const int64_t at = base + i * kJoinThreads + tid;
+            c[i] = at < all ? a.best[b * all + at] : 0ull;
         }
-        int kept_count = 0;
-        __syncthreads();
+    };
+    load(0);
+    for (int beam = wave; beam < a.beams; beam += kJoinWaves) {
+        const int64_t row = b * a.beams + beam;
+        const float s = a.scores[row];
+        const bool over = a.finished != nullptr && a.finished[row] != 0;
+        double less = 0.0;
+        if (a.normalize && s != none && !over) {
+            double high = (double)none;
+            for (int p = lane; p < a.parts; p += kWave)
+                high = __builtin_fmax(high, a.of_part[row * a.parts + p].base);
+#pragma unroll
+            for (int d = 1; d < kWave; d *= 2) high = __builtin_fmax(high, __shfl_xor(high, d, kWave));
+            double sum = 0.0;
+            for (int p = lane; p < a.parts; p += kWave) {
+                const Part q = a.of_part[row * a.parts + p];
+                sum += q.base == (double)none ? q.sum : q.sum * exp(q.base - high);
+            }
+            less = high + log(team_sum64<kWave>(sum));
+        }
+        if (lane == 0) norm[beam] = less, score[beam] = over ? none : s;
+    }
+    int kept_count = 0;
+    __syncthreads();
 
-        for (int64_t base = 0; base == 0 || base < all; base += kJoinBlock) {
-            if (base > 0) load(base);
-            if (tid == 0) taken_count = 0, bound_key = 0ull, bound_flat = ~0u;
-            Total t[kJoinHeld + 1];
+    for (int64_t base = 0; base == 0 || base < all; base += kJoinBlock) {
+        if (base > 0) load(base);
+        if (tid == 0) taken_count = 0, bound_total = nothing;
+        Total t[kJoinHeld + 1];
 #pragma unroll
-            for (int i = 0; i < kJoinHeld; ++i) {
-                const int64_t at = base + i * kJoinThreads + tid;
-                t[i] = nothing;
-                if (at >= all || (uint32_t)(c[i] >> 32) == 0u) continue;
-                const int beam = (int)(at / ((int64_t)a.parts * a.count));
-                if (score[beam] == none) continue;  // (what is there was left by another call)
-                t[i] = {key_of((double)score[beam] + ((double)logit_of(c[i]) - norm[beam])),
-                        (uint32_t)(beam * a.vocab + token_of(c[i]))};
-            }
-            // with the first block finished beams, with later ones the best so far
-            t[kJoinHeld] = nothing;
-            if (base > 0) {
-                if (tid < kept_count) t[kJoinHeld] = kept.at(tid);
-            } else if (tid < a.beams && a.finished != nullptr) {
-                const int64_t row = b * a.beams + tid;
-                const float s = a.scores[row];
-                if (a.finished[row] != 0 && s != none)
-                    t[kJoinHeld] = {key_of((double)s), (uint32_t)(tid * a.vocab + a.end_id)};
-            }
-            Total mine = t[0];
-#pragma unroll
-            for (int i = 1; i <= kJoinHeld; ++i)
-                if (better(t[i], mine)) mine = t[i];
-            of_thread.set(tid, mine);
-            __syncthreads();
-            if (tid < kWave) {
-                for (int w = 1; w < kJoinWaves; ++w)
-                    if (better(of_thread.at(w * kWave + tid), mine)) mine = of_thread.at(w * kWave + tid);
-                maxima.set(tid, mine);
-            }
-            __syncthreads();
-            {
-                // (of fewer than `count` there is none at that place, and all are taken)
-                const int i = tid / kRankLanes;
-                const int before = maxima.before(i, kWave);
-                if (tid % kRankLanes == 0 && before == a.count - 1)
-                    bound_key = maxima.key[i], bound_flat = maxima.flat[i];
-            }
-            __syncthreads();
-            const Total bound{bound_key, bound_flat};
-#pragma unroll
-            for (int i = 0; i <= kJoinHeld; ++i)
-                if (t[i].key != 0ull && !better(bound, t[i])) taken.set(atomicAdd(&taken_count, 1), t[i]);
-            __syncthreads();
-            const int n = taken_count;
-            for (int i = tid / kRankLanes; i < n; i += kRanked) {
-                const int before = taken.before(i, n);
-                if (tid % kRankLanes == 0 && before < a.count) kept.set(before, taken.at(i));
-            }
-            kept_count = n < a.count ? n : a.count;
-            __syncthreads();
+        for (int i = 0; i < kJoinHeld; ++i) {
+            const int64_t at = base + i * kJoinThreads + tid;
+            t[i] = nothing;
+            if (at >= all || (uint32_t)(c[i] >> 32) == 0u) continue;
+            // (a part is a thousand tokens or more: there are far fewer candidates than 2^31)
+            const int beam = (int)((uint32_t)at / (uint32_t)(a.parts * a.count));
+            if (score[beam] == none) continue;  // (what is there was left by another call)
+            t[i] = {key_of((double)score[beam] + ((double)logit_of(c[i]) - norm[beam])), place_of(a, beam, c[i])};
         }
-        for (int k = tid; k < a.count; k += kJoinThreads) {
-            const int64_t at = b * a.count + k;
-            const bool there = k < kept_count;
-            const uint32_t flat = there ? kept.flat[k] : 0u;
-            a.out_scores[at] = there ? (float)value_of(kept.key[k]) : none;
-            a.parents[at] = there ? (int32_t)(flat / (uint32_t)a.vocab) : -1;
-            const int token = there ? (int)(flat % (uint32_t)a.vocab) : -1;
-            if (a.wide_ids)
-                ((int64_t *)a.tokens)[at] = token;
-            else
-                ((int32_t *)a.tokens)[at] = token;
+        // with the first block finished beams, with later ones the best so far
+        t[kJoinHeld] = nothing;
+        if (base > 0) {
+            if (tid < kept_count) t[kJoinHeld] = kept.at(tid);
+        } else if (tid < a.beams && a.finished != nullptr) {
+            const int64_t row = b * a.beams + tid;
+            const float s = a.scores[row];
+            if (a.finished[row] != 0 && s != none)
+                t[kJoinHeld] = {key_of((double)s), place_of(a, tid, ~(uint32_t)a.end_id)};
+        }
+        Total mine = t[0];
+#pragma unroll
+        for (int i = 1; i <= kJoinHeld; ++i)
+            if (better(t[i], mine)) mine = t[i];
+        of_thread.set(tid, mine);
+        __syncthreads();
+        if (tid < kWave) {
+            for (int w = 1; w < kJoinWaves; ++w)
+                if (better(of_thread.at(w * kWave + tid), mine)) mine = of_thread.at(w * kWave + tid);
+            maxima.set(tid, mine);
         }
         __syncthreads();
+        {
+            // (of fewer than `count` there is none at that place, and all are taken)
+            const int i = tid / kRankLanes;
+            const int before = maxima.before(i, kWave);
+            if (tid % kRankLanes == 0 && before == a.count - 1) bound_total = maxima.at(i);
+        }
+        __syncthreads();
+        const Total bound = bound_total;
+#pragma unroll
+        for (int i = 0; i <= kJoinHeld; ++i)
+            if (t[i].key != 0ull && !better(bound, t[i])) taken.set(atomicAdd(&taken_count, 1), t[i]);
+        __syncthreads();
+        const int n = taken_count;
+        for (int i = tid / kRankLanes; i < n; i += kRanked) {
+            const int before = taken.before(i, n);
+            if (tid % kRankLanes == 0 && before < a.count) kept.set(before, taken.at(i));
+        }
+        kept_count = n < a.count ? n : a.count;
+        __syncthreads();
+    }
+    for (int k = tid; k < a.count; k += kJoinThreads) {
+        const int64_t at = b * a.count + k;
+        const bool there = k < kept_count;
+        const uint64_t place = there ? kept.place[k] : 0ull;
+        a.out_scores[at] = there ? (float)value_of(kept.key[k]) : none;
+        a.parents[at] = there ? a.beams - 1 - (int)(place >> 32 >> a.token_bits) : -1;
+        const int token = there ? (int)__builtin_amdgcn_ubfe(~(uint32_t)place, 0, a.token_bits) : -1;
+        if (a.wide_ids)
+            ((int64_t *)a.tokens)[at] = token;
+        else
+            ((int32_t *)a.tokens)[at] = token;
     }
 }
 

@@ -204,6 +204,66 @@ def test_nan_and_infinity():
     assert s[2, 0] == INF and t[2, 0] == 5 and p[2, 0] == 1 and torch.isfinite(s[2, 1:]).all()
 
 
+def by_beam_and_logit(logits, scores, count, normalize):
+    """(parents, tokens) by totals in 64 bits, equal ones by beam, then logit, then token;
+    NaN totals before all others."""
+    l, s = as64(logits), as64(scores)
+    b, k, v = l.shape
+    parents, tokens = np.full((b, count), -1), np.full((b, count), -1)
+    with np.errstate(all="ignore"):
+        total = l + s[:, :, None]
+        if normalize:
+            top = l.max(2, keepdims=True)
+            total = (l - (top + np.log(np.exp(l - top).sum(2, keepdims=True)))) + s[:, :, None]
+    beam, token = np.divmod(np.arange(k * v), v)
+    for i in range(b):
+        t, of = total[i].reshape(-1), l[i].reshape(-1)
+        order = np.lexsort((token, -of, beam, np.where(np.isnan(t), 0.0, -t), ~np.isnan(t)))
+        order = order[~(np.isnan(of) | (of == -INF) | (s[i][beam] == -INF))[order]][:count]
+        parents[i, :order.size], tokens[i, :order.size] = beam[order], token[order]
+    return parents, tokens
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_tokens_of_a_beam_go_by_their_logits(name, normalize):
+    """Also where a beam's totals are one number: scores that swallow the logits, logits
+    too small to change a total, NaN and infinity."""
+    torch = torch_()
+    lowest = torch.finfo(torch.float32).min
+    for vocab in (9, 700, 33001):
+        announce("swallowed logits %s %s %d" % (name, normalize, vocab))
+        logits, scores = randn((8, 3, vocab), name, vocab), beam_scores(8, 3, 1)
+        scores[0] = lowest
+        scores[1, 1] = -1e30
+        scores[2] = torch.tensor([1e30, 1e30, -INF])
+        scores[3] = torch.tensor([-INF, -1e12, -INF])
+        logits[4] = (randn((3, vocab), "f32", 5) * 1e-20).to(logits.dtype)  # (float16: zeros of both signs)
+        scores[4] = -1.0
+        scores[5, 1] = float("nan")
+        scores[6] = torch.tensor([0.0, INF, -1.0])
+        logits[7, 2, 4] = float("nan")
+        for count in (1, 6, 64):
+            got = lrs.beam_select(logits, scores, count, normalize=normalize)
+            want_p, want_t = by_beam_and_logit(logits, scores, count, normalize)
+            p, t = got[1].cpu().numpy(), got[2].cpu().numpy()
+            for i in range(8):
+                assert (p[i] == want_p[i]).all() and (t[i] == want_t[i]).all(), (vocab, count, i, p[i], t[i], want_p[i],
+                                                                                 want_t[i])
+            # a search gives the same alone, where its rows are cut into more parts
+            for i in (0, 4, 5):
+                alone = lrs.beam_select(logits[i:i + 1], scores[i:i + 1], count, normalize=normalize)
+                assert all(torch.equal(a.nan_to_num(7.0), b[i:i + 1].nan_to_num(7.0)) for a, b in zip(alone, got))
+    wide = randn((200, 3, 33001), name, 3)
+    parked = torch.full((200, 3), lowest, device="cuda")
+    got = lrs.beam_select(wide, parked, 7, normalize=normalize)
+    for i in (0, 199):
+        alone = lrs.beam_select(wide[i:i + 1], parked[i:i + 1], 7, normalize=normalize)
+        assert all(torch.equal(a, b[i:i + 1]) for a, b in zip(alone, got))
+    want_p, want_t = by_beam_and_logit(wide[:1], parked[:1], 7, normalize)
+    assert (got[1][0].cpu().numpy() == want_p[0]).all() and (got[2][0].cpu().numpy() == want_t[0]).all()
+
+
 def test_beam_strides_and_empty():
     torch = torch_()
     announce("beam strides")
