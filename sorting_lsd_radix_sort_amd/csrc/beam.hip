@@ -191,7 +191,7 @@ LRS_API lrs_status lrs_beam_reorder(const void *d_in, const lrs_beam_layout *in_
     const Places dst{ol.outer_step, ol.batch_step, ol.beam_step, ol.middle_step, ol.row_step};
     a.tiles = (a.vecs + (1 << a.tx_log2) - 1) >> a.tx_log2;
     const int64_t col_tiles = a.tiles + (a.words > 0);
-    const int64_t row_tiles = (a.all_rows + (kThreads >> a.tx_log2) - 1) / (kThreads >> a.tx_log2);
+    const int64_t row_tiles = ((int64_t)a.all_rows + (kThreads >> a.tx_log2) - 1) / (kThreads >> a.tx_log2);
     const dim3 grid((unsigned)std::min(col_tiles, kMaxGridX), (unsigned)std::min(row_tiles, kMaxGridY),
                     (unsigned)((row_tiles + kMaxGridY - 1) / kMaxGridY));
     const __int128 read_bytes = (__int128)a.all_rows * row_bytes * std::min(beams, count);

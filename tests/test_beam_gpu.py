@@ -529,6 +529,20 @@ def test_reorder_far_states_and_many_rows():
     assert torch.equal(many, want)
 
 
+def test_reorder_of_as_many_rows_as_there_may_be():
+    """2^31 - 1 rows of a byte: the grid that covers them is one more than an int counts."""
+    torch = torch_()
+    announce("2^31 - 1 rows")
+    rows = 2**31 - 1
+    states = torch.arange(251, device="cuda", dtype=torch.uint8).repeat(2 * rows // 251 + 1)[:2 * rows]
+    states = states.view(1, 1, rows, 2)[..., 1:]
+    got = lrs.beam_reorder(states, torch.zeros(1, 1, dtype=torch.int32, device="cuda"))
+    assert got.shape == states.shape and got.is_contiguous() and torch.equal(got, states)
+    with pytest.raises(lrs.LrsError):
+        lrs.beam_reorder(states.as_strided((1, 1, rows + 1, 1), (1, 1, 0, 1)),
+                         torch.zeros(1, 1, dtype=torch.int32, device="cuda"))
+
+
 # ------------------------------------------------------------- used together
 
 
