@@ -270,6 +270,18 @@ def _check_temp(temp):
         raise ValueError("temp must be contiguous")
 
 
+def _as_stored(t):
+    """A tensor whose memory holds its values: a copy of one that torch negates when it is
+    read (the imaginary part of a conjugate)."""
+    return t.resolve_neg() if t.is_neg() else t
+
+
+def _check_stored(name, t):
+    """What is written to an output's memory has to be what is read from it."""
+    if t.is_neg():
+        raise ValueError("%s is a view that negates what its memory holds" % name)
+
+
 def _temp_tensor(nbytes, device, temp):
     import torch
     if temp is not None:
@@ -331,6 +343,7 @@ def _check_out(name, t, n, dtype, device):
         raise ValueError("%s holds %d elements, expected %d" % (name, t.numel(), n))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
+    _check_stored(name, t)
     if t.device != device:
         raise ValueError("%s is on %s, the input on %s" % (name, t.device, device))
 
@@ -349,7 +362,7 @@ def sort_keys(keys, begin_bit: int = 0, end_bit: int | None = None, out=None, te
     sfx = key_suffix(keys.dtype)
     end_bit = KEY_BITS[sfx] if end_bit is None else end_bit
     src = keys
-    keys = keys.contiguous()
+    keys = _as_stored(keys).contiguous()
     n = keys.numel()
     given = out
     if out is None:
@@ -389,7 +402,7 @@ def sort_pairs(keys, values, begin_bit: int = 0, end_bit: int | None = None, key
         raise ValueError("values are on %s, keys on %s" % (values.device, keys.device))
     end_bit = KEY_BITS[sfx] if end_bit is None else end_bit
     ksrc, vsrc = keys, values
-    keys = keys.contiguous()
+    keys = _as_stored(keys).contiguous()
     values = values.contiguous()
     n = keys.numel()
     given = keys_out, values_out

@@ -14,7 +14,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _check, _ptr, _stream, load_library
+from . import _as_stored, _check, _ptr, _stream, load_library
 from . import rows as _r
 from .rows import ID_TYPE_CODES, ROW_TYPE_CODES, _CI, _F, _I64, _SZ, _VP, _code
 
@@ -159,7 +159,7 @@ def route_tokens(logits, slots: int, scores: str = "softmax", bias=None, num_gro
         raise _r._host_tensor(logits)
     logits, ld = _r._rows_in(logits, tokens, experts)
     if bias is not None:
-        bias = bias.contiguous()
+        bias = _as_stored(bias).contiguous()
     ids = logits.new_empty(tokens, slots, dtype=dtype)
     weights = logits.new_empty(tokens, slots, dtype=weights_dtype)
     _r._run("lrs_route_tokens", stream, (logits, bias, ids, weights),
@@ -193,7 +193,7 @@ def route_tokens_grad(grad_weights, logits, ids, scores: str = "softmax", normal
     if grad is None:
         grad = logits.new_empty(tokens, experts)
     logits, ld = _r._rows_in(logits, tokens, experts)
-    ids, grad_weights = ids.contiguous(), grad_weights.contiguous()
+    ids, grad_weights = ids.contiguous(), _as_stored(grad_weights).contiguous()
     _r._run("lrs_route_tokens_grad", stream, (logits, ids, grad_weights, grad),
             (code, logits.data_ptr(), ld, tokens, experts, ids.shape[1], score, 1 if normalize else 0, float(scale),
              id_code, ids.data_ptr(), weight_code, grad_weights.data_ptr(), grad.data_ptr(), ld_grad), given)
@@ -234,6 +234,7 @@ def beam_select(logits, scores, count: int, normalize: bool = True, finished=Non
                          (count, vocab))
     if not logits.is_cuda:
         raise _r._host_tensor(logits)
+    logits = _as_stored(logits)
     # one row per beam, equally far apart
     to_batch, step, to_token = logits.stride()
     if beams == 1:
@@ -241,7 +242,7 @@ def beam_select(logits, scores, count: int, normalize: bool = True, finished=Non
     rows = batch * beams
     if rows > 1 and ((batch > 1 and to_batch != beams * step) or step < vocab) or (rows and vocab > 1 and to_token != 1):
         logits, step = logits.contiguous(), vocab
-    scores = scores.contiguous()
+    scores = _as_stored(scores).contiguous()
     if finished is not None:
         finished = finished.contiguous()
     new_scores = scores.new_empty(batch, count)
@@ -280,7 +281,7 @@ _plans: dict = {}  # how states of a shape and strides are reordered, which alon
 
 
 def _beam_plan(shape, strides, dim, size, parents_shape, out_shape, out_strides):
-    """(shape of the new states, batch dimension, sizes for the C call, its layouts)."""
+    """(shape of the new states, sizes for the C call, its layouts)."""
     nd, at = len(shape), int(dim)
     at = at + nd if at < 0 else at
     if not 0 <= at < nd - 1:
@@ -312,25 +313,38 @@ def beam_reorder(states, parents, dim: int = 0, out=None, stream=None):
     (`states` itself for the reordering in place, of at most 64 beams whose memory lies
     apart, which moves only what has another parent), or a new one.  Strides may be any that leave at most three dimensions beside
     batch, beams and a contiguous piece: the filled part of a cache that has room for more
-    will do, with layers in front and heads before or behind the positions."""
+    will do, with layers in front and heads before or behind the positions.  Of views that
+    torch conjugates or negates when they are read the values are moved: by bytes where
+    states and out are such views alike, else from a copy (as `out` alone they are
+    refused)."""
     if parents.dtype is not (_r._types or _r._type_codes())[2]:
         raise TypeError("parents must be int32, not %s" % parents.dtype)
     key = (states.shape, states.stride(), dim, states.dtype, parents.shape,
            out is not None and (out.shape, out.stride()))
     plan = _plans.get(key)
     if plan is None:
-        plan = _beam_plan(states.shape, states.stride(), dim, states.element_size(), parents.shape,
+        plan = states.is_complex(), *_beam_plan(states.shape, states.stride(), dim, states.element_size(), parents.shape,
                           *((None, None) if out is None else (out.shape, out.stride())))
         if len(_plans) >= 4096:
             _plans.clear()
         _plans[key] = plan
-    shape, sizes, from_layout, to_layout = plan
-    _same_device("parents", parents, states)
-    given = out
+    is_complex, shape, sizes, from_layout, to_layout = plan
+    index, given = states.get_device(), out
+    if parents.get_device() != index:
+        raise _r._elsewhere("parents", parents, states)
     if out is not None:
         if out.dtype is not states.dtype:
             raise ValueError("out has dtype %s, expected %s" % (out.dtype, states.dtype))
-        _same_device("out", out, states)
+        if out.get_device() != index:
+            raise _r._elsewhere("out", out, states)
+    if is_complex or states.is_neg() or (out is not None and out.is_neg()):
+        # bytes are moved: what torch conjugates or negates when it is read has to be so on
+        # both sides, or on neither
+        lazy = states.is_conj(), states.is_neg()
+        if lazy != ((False, False) if out is None else (out.is_conj(), out.is_neg())):
+            if out is not None and (out.is_conj() or out.is_neg()):
+                raise ValueError("out is a view that negates or conjugates what its memory holds")
+            return beam_reorder(states.resolve_conj().resolve_neg(), parents, dim, out, stream)
     if not states.is_cuda:
         raise _r._host_tensor(states)
     if out is None:

@@ -12,7 +12,8 @@ require (as under ``torch.no_grad``), but a tensor given as output counts as cha
 in place, so a gradient that still needs its old values is refused by torch.
 
 Matrices may have any row stride; their elements must be contiguous within a row
-(inputs that are not are copied first, outputs are refused).  ``temp``, where a call
+(inputs that are not are copied first, outputs are refused; so are views that torch
+negates when they are read, as the imaginary part of a conjugate).  ``temp``, where a call
 takes it, must be contiguous; one that is too small is not used.  ``stream`` is as for
 ``sort_keys``: None is the current stream of the tensors' device; on any other
 stream the work also waits for what the current one already holds, so that inputs
@@ -22,7 +23,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _check, _check_temp, _ptr, _stream, _stream_of, _written, load_library
+from . import _as_stored, _check, _check_stored, _check_temp, _ptr, _stream, _stream_of, _written, load_library
 
 ID_TYPE_CODES = {"i32": 0, "i64": 1}
 ROW_TYPE_CODES = {"f32": 0, "bf16": 1, "f16": 2}
@@ -192,7 +193,9 @@ def _row_stride(t, rows, cols):
 
 def _rows_in(t, rows, cols):
     """A matrix argument as the library reads it, and its row stride: a copy where a
-    row's elements are not next to each other."""
+    row's elements are not next to each other, or not what the memory holds."""
+    if t.is_neg():
+        t = t.resolve_neg()
     ld = _row_stride(t, rows, cols)
     return (t, ld) if ld is not None else (t.contiguous(), cols)
 
@@ -209,6 +212,7 @@ def _rows_out(name, t, rows, cols, like):
     ld = _row_stride(t, r, c)
     if ld is None:
         raise ValueError("%s must be contiguous within each row" % name)
+    _check_stored(name, t)
     if t.get_device() != like.get_device():
         raise _elsewhere(name, t, like)
     return r, ld
@@ -231,7 +235,7 @@ def _weights(weights, position):
         raise ValueError("weights have shape %s, position %s" % (tuple(weights.shape), tuple(position.shape)))
     if weights.get_device() != position.get_device():
         raise _elsewhere("weights", weights, position)
-    return weights.contiguous(), _row_code("weights", weights.dtype)
+    return _as_stored(weights).contiguous(), _row_code("weights", weights.dtype)
 
 
 def _at(t):

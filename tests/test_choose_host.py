@@ -206,3 +206,27 @@ def test_beam_conveniences_check_before_any_work():
             ((st, p), {}, ValueError, "device tensors")):
         with pytest.raises(error, match=match):
             lrs.beam_reorder(*args, **kw)
+
+
+def test_outputs_that_torch_negates_or_conjugates_when_read_are_refused():
+    """What a call writes is bytes: read through such a view they would be other values."""
+    def negated(*shape):
+        return torch.zeros(*shape, dtype=torch.complex64).conj().imag
+
+    x, ids, g = torch.zeros(4, 1), torch.zeros(4, 1, dtype=torch.int32), torch.zeros(4, 1)
+    assert negated(4, 1).is_neg()
+    for call in (lambda: lrs.route_tokens_grad(g, x, ids, grad=negated(4, 1)),
+                 lambda: lrs.dispatch_rows(x, ids, out=negated(4, 1)),
+                 lambda: lrs.combine_rows(x, ids, out=negated(4, 1)),
+                 lambda: lrs.combine_rows_grad(x, x, ids, None, grad_rows=negated(4, 1)),
+                 lambda: lrs.embedding(x, ids[:, 0], out=negated(4, 1)),
+                 lambda: lrs.embedding_grad(x, ids[:, 0], 4, grad=negated(4, 1)),
+                 lambda: lrs.sort_keys(x[:1], out=negated(1)),
+                 lambda: lrs.beam_reorder(torch.zeros(2, 2, 4), ids[:2], out=negated(2, 1, 4))):
+        with pytest.raises(ValueError, match="view that negates"):
+            call()
+    z = torch.zeros(2, 2, 4, dtype=torch.complex64)
+    with pytest.raises(ValueError, match="negates or conjugates"):
+        lrs.beam_reorder(z, ids[:2], out=z[:, :1].conj())
+    with pytest.raises(ValueError, match="negates or conjugates"):
+        lrs.beam_reorder(torch.zeros(2, 2, 4), ids[:2], out=torch._neg_view(torch.zeros(2, 1, 4)))
