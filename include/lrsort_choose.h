@@ -12,10 +12,11 @@
  *
  * Conventions, beside those of lrsort_rows.h (matrices and their strides, types,
  * streams, temp storage, overlap, refusals before any work is enqueued):
- *  - What is chosen is what the definition's real numbers say, not their roundings to
- *    float32: values are compared as they are, sums of them in float64.  (Between beams
- *    the logarithms of sums count, which are formed from float32 exponentials: see there.)
- *    Equal values go to the lowest id, and a choice is listed from the best down.
+ *  - What is chosen goes by values as they are where they alone decide, and by sums of
+ *    them in float64, not by roundings to float32.  (Between beams the logarithms of sums
+ *    count, which are formed from float32 exponentials: see there.)  Equal values, and
+ *    sums that float64 holds as one number, go to the lowest id, and a choice is listed
+ *    from the best down.
  *  - -infinity takes no part: an expert or a continuation of that value is never
  *    chosen.  A place for which nothing is left gets the id -1 (and the weight 0, or
  *    the score -infinity): an id that lrs_group_tokens and lrs_embedding pass over.
@@ -51,6 +52,10 @@ typedef enum lrs_group_score { LRS_GROUP_MAX = 0, LRS_GROUP_TOP2 = 1 } lrs_group
  * c among their experts, and with s at those ids
  *   w[t,k] = scale * s[t,id] / (sum of s over the chosen ids)   normalize != 0
  *   w[t,k] = scale * s[t,id]                                    normalize == 0
+ *  - Without a bias experts are compared by their logits (with the softmax, where groups
+ *    are kept by their two best, by s), with one by c.  s, c and the scores of groups are
+ *    formed in float64: there a softmax's s is one number from 745 below the token's
+ *    largest logit on, a sigmoid 1 above 37 and one number below -709.
  *  - The bias changes the choice only.  An expert whose logit or bias is -infinity
  *    takes no part; a group without any that does is the last.
  *  - NaN is larger than any number, as sorts have it: a NaN logit is chosen, and so

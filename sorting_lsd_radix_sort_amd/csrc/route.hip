@@ -82,9 +82,10 @@ LRS_API lrs_status lrs_route_tokens(lrs_row_type type, const void *d_logits, int
     const bool grouped = kept_groups < num_groups;
     const bool top2 = grouped && group_score == LRS_GROUP_TOP2, sums = d_bias != nullptr || top2;
     const int size = (int)(experts / num_groups);
+    const uint8_t sigmoid = score != LRS_SCORE_SIGMOID ? 0 : d_bias != nullptr ? 1 : 2;
     Route a{d_bias, d_ids, d_weights, scale, (int)tokens, (int16_t)experts, (int16_t)size, (int16_t)num_groups,
-            (int16_t)kept_groups, (uint8_t)slots, score == LRS_SCORE_SIGMOID, top2, normalize != 0,
-            id_type == LRS_ID_I64, (uint8_t)weight_type, 0, 0};
+            (int16_t)kept_groups, (uint8_t)slots, sigmoid, top2, normalize != 0, id_type == LRS_ID_I64,
+            (uint8_t)weight_type, 0, 0};
     // a token's list of the chosen, and its scores and groups where they are needed
     const int cells = sums || b == 4 ? 8 : grouped ? 4 : 0;
     const int team_bytes = team_align((slots + 2) * (int64_t)sizeof(Chosen) + cells * (experts + num_groups));

@@ -38,7 +38,7 @@ struct Route {
     float scale;
     int tokens;
     int16_t experts, size, groups, kept;  // size: of a group
-    uint8_t slots, sigmoid, top2, normalize, wide_ids, weight_type;
+    uint8_t slots, sigmoid, top2, normalize, wide_ids, weight_type;  // sigmoid: 2 without a bias
     uint8_t lane_groups, lane_groups_log2;  // a group is this many lanes' vectors; 0: it is no such number
 };
 
@@ -82,6 +82,15 @@ __device__ __forceinline__ uint64_t choice64(const Route &a, float l, float bias
     else
         s = sum != sum ? sum : exp64((double)l - (double)top) / sum;
     return key_of(s + (double)bias);
+}
+
+// Whether experts of the kept groups are compared by their logits: a sigmoid rises with
+// its logit also where float64 holds one number for both (1 from 37 on).  With a bias
+// their sums in float64 decide, and such sums are equal.
+template <bool SUMS>
+__device__ __forceinline__ bool by_logits(const Route &a)
+{
+    return SUMS && a.sigmoid == 2;
 }
 
 // The softmax's sum in float64, from memory.
@@ -149,6 +158,13 @@ __device__ void choose_in_64(const T *row, const Route &a, int lane, float top, 
                 for (int i = 0; i < a.size; ++i) cells[g * a.size + i] = 0;
         wave_sync();
     }
+    if (by_logits<SUMS>(a)) {
+#pragma unroll 4
+        for (int i = 0; i < V; ++i) {
+            const int e = i * L + lane;
+            if (e < a.experts && cells[e] != 0) cells[e] = key_of((double)load_logit(row, e));
+        }
+    }
     for (int k = 0; k < a.slots; ++k) {
         uint64_t best = 0;
         uint32_t at = ~0u;
@@ -175,8 +191,9 @@ __device__ __forceinline__ void order_in_64(const T *row, const Route &a, int la
 {
     for (int k = lane; k < n; k += L) {
         const int e = list[k].expert;
-        cells[k] = e < 0 ? 0ull
-                         : choice64<SUMS>(a, load_logit(row, e), SUMS && a.bias != nullptr ? a.bias[e] : 0.0f, top, sum);
+        const float l = e < 0 ? -__builtin_inff() : load_logit(row, e);
+        const float bias = SUMS && a.bias != nullptr && e >= 0 ? a.bias[e] : 0.0f;
+        cells[k] = by_logits<SUMS>(a) ? key_of((double)l) : choice64<SUMS>(a, l, bias, top, sum);
     }
     wave_sync();
     // (a lane has one or a few of them: it reads them all before any is replaced)

@@ -228,6 +228,41 @@ def test_scores_that_float32_cannot_tell_apart(kind, experts):
             np.arange(4)).all()
 
 
+@pytest.mark.parametrize("experts,groups", [(16, 4), (60, 4), (160, 8), (256, 8), (512, 16), (700, 7), (2048, 32)])
+@pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
+def test_sigmoids_that_float64_holds_as_one_number(name, experts, groups):
+    """Without a bias the order within the kept groups is that of the logits, whose sigmoids
+    are all 1 in 64 bits from 38 on; groups of equal sums: the lowest."""
+    announce("saturated sigmoids %s %d" % (name, experts))
+    torch = torch_()
+    rng = np.random.default_rng(experts)
+    l = torch.from_numpy(40 + 20 * rng.random((9, experts))).to(dtype_of(name)).cuda()
+    l[0] = torch.where(torch.arange(experts, device="cuda") % 2 == 0, 41.0, 40.0)
+    l[1] = torch.arange(experts, device="cuda") * (100.0 / experts) + 40
+    l[2] = l[1].flip(0)
+    l[3, ::3] = -INF
+    l[4, experts // 2:] = -INF
+    l[5] = -l[5]  # (far apart in 64 bits; in 32 all are next to 0)
+    if name == "f32":
+        l[6] = -800 - l[6]
+    size, x = experts // groups, as64(l)
+    for kept in (2, groups - 1):
+        for slots in (1, 5, 2 * size if size < 30 else 40):
+            for normalize in (True, False):
+                ids, w = lrs.route_tokens(l, slots, "sigmoid", num_groups=groups, kept_groups=kept, group_score="top2",
+                                          normalize=normalize)
+                for t in range(9):
+                    best = np.sort(scores64(np.where(x[t] == -INF, 0, x[t])[None], "sigmoid")[0].reshape(groups, size) *
+                                   (x[t].reshape(groups, size) != -INF), 1)[:, -2:].sum(1)
+                    stay = np.argsort(-best, kind="stable")[:kept]
+                    out = ~np.isin(np.arange(experts) // size, stay) | (x[t] == -INF)
+                    want = np.argsort(np.where(out, INF, -x[t]), kind="stable")[:slots]
+                    want = np.where(out[want], -1, want)
+                    assert (ids[t].cpu().numpy() == want).all(), (t, kept, slots, ids[t].tolist(), want.tolist())
+                ww, r = reference_weights(x, ids.cpu().numpy(), "sigmoid", normalize, 1.0)
+                near(w, ww, np.abs(ww) * r)
+
+
 @pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("experts", [20, 128, 700])
