@@ -101,7 +101,9 @@ lrs_status beam_entry(void *d_temp, size_t *temp_bytes, lrs_row_type type, const
 // States of more bytes than the last-level cache keeps beside what is written are read past
 // the caches: of 16 searches of 8 beams (537 MB) in place in 133 us instead of 149, into
 // others in 153 instead of 159, 201 MB in place in 52 instead of 57.  134 MB would take 35
-// instead of 32, and 67 MB written eight times over 108 instead of 87.
+// instead of 32, and 67 MB written eight times over 108 instead of 87.  (Not narrow rows of
+// more than 16 beams in place, where a lane loads a state for each of its 64 beams, a
+// needed one again for those that need none: from the caches.)
 constexpr int64_t kReadPastBytes = (int64_t)160 << 20;
 
 // A state's memory from its first to its last byte, and whether its rows lie apart.
@@ -196,10 +198,14 @@ LRS_API lrs_status lrs_beam_reorder(const void *d_in, const lrs_beam_layout *in_
                     (unsigned)((row_tiles + kMaxGridY - 1) / kMaxGridY));
     const __int128 read_bytes = (__int128)a.all_rows * row_bytes * std::min(beams, count);
     auto run = [&](auto w, auto most, auto wave) {
-        with_bool(read_bytes >= kReadPastBytes, [&](auto nt) {
+        auto launch = [&](auto nt) {
             reorder_kernel<decltype(w), most.value, wave.value, nt.value>
                 <<<grid, kThreads, 0, stream>>>(in_at, (char *)d_out, d_parents, src, dst, a);
-        });
+        };
+        if constexpr (most.value > 16 && !wave.value)
+            launch(std::false_type{});
+        else
+            with_bool(read_bytes >= kReadPastBytes, launch);
     };
     auto with_word = [&](auto most, auto wave) {
         if (word == 4)

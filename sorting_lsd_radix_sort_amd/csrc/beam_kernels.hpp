@@ -612,7 +612,8 @@ __device__ __forceinline__ void move_lane_column(const char *in, int64_t in_step
         }
     } else {
         // (a beam whose state is not needed loads another's again, or the first, which is
-        // always there)
+        // always there: what is loaded again comes from the caches)
+        static_assert(!NT, "loads that the caches answer do not go past them");
         int spare = 0;
 #pragma unroll
         for (int j = MOST - 1; j >= 0; --j) spare = needed(j) ? p[j] : spare;
