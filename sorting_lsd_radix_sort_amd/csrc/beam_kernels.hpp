@@ -70,14 +70,19 @@ struct Scan {
 // registers: first the lanes' maxima; then, with the largest of them known, (SUM) the
 // part's sum of exponentials and the vectors that hold candidates.  A bound for these:
 // the `count`-th largest of 64 maxima, each over an equal share of the part, so that
-// some 64 ln(64 / (64 - count)) logits reach it (18 for 16, above that the more).  Their
-// vectors are queued in LDS and taken apart there, a logit a thread.  (Where ties make
-// them too many, a wave keeps its best in a list of its own: 512 rows of 131,072 bf16
-// logits in 71 us with the join if all are equal, 31 if none.)
+// some 64 (1 / 64 + 1 / 63 + .. + 1 / (65 - count)) logits reach it (18 for 16, 87 for 48,
+// 170 for 60, 304 for 64).  Their vectors are queued in LDS and taken apart there, a logit
+// a thread.  Where they are more than the list's 256, by ties or because `count` is nearly
+// 64 (a third of the parts at 63, most at 64), a wave keeps its best in a list of its own:
+// 512 rows of 131,072 bf16 logits in 71 us with the join if all are equal, 31 if none; the
+// scan alone 26 for 16 of them, 32 for 48, 49 for 60, 66 for 63, 82 for 64.
 //
 // The part's sum: exponents by base 2 relative to the part's largest logit, eight or four
 // of them added in float32, the rest in float64: its logarithm is off by 5e-8 on average,
-// the share of log2(e)'s rounding (1.3e-8 of a logit's distance from the largest).
+// the share of log2(e)'s rounding (1.3e-8 of a logit's distance from the largest).  These
+// are fewer bits than float64 exponentials would keep, which are some twenty instructions
+// of float64 a logit where these are six of float32: totals of two beams that are closer
+// than their logarithms' errors may change places.
 //
 // Bound by HBM and by instructions about equally: 512 rows of 131,072 bf16 logits in 26
 // us, 134 MB at 5.2 TB/s (22 us without the sums, which are 6 instructions a logit and
@@ -348,8 +353,10 @@ struct Totals {
 // One workgroup per search: the beams' log sums from their parts; then the candidates of
 // all parts at once, a few a thread, those that do not reach the `count`-th largest of 64
 // maxima left out, the others ranked by counting.  Bound by latency: 5 us for 4 beams of
-// 32,000 logits, 6 for 64 searches of 8 beams of 131,072 (512 candidates each); with 512
-// threads half a microsecond more, with 256 1.5.  Ranking every list's best first, then
+// 32,000 logits, 6 for 64 searches of 8 beams of 131,072 (1,024 candidates each); with 512
+// threads half a microsecond more, with 256 1.5.  For 32 of beams of like scores 23, 48 17,
+// 62 28, 63 84, 64 163: more candidates reach a bound of 64 maxima, the more where `count`
+// divides 64 and so each of the 64 is over places of one rank.  Ranking every list's best first, then
 // the lists' next places in rounds, took 17 to 33.
 __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(Join a, int batch)
 {

@@ -263,8 +263,16 @@ __device__ __forceinline__ void sort_down(uint32_t (&k)[N])
 // bf16 7.5.  4 tokens of 128 experts take 3.7, most of it a launch's own time.  Sixteen
 // lanes a token up to 256 experts (with 32 it takes 18.9 and 11.7 us), 32 up to 512 (29
 // us; 36 with 16).  Taking off the best by a search through all of a lane's keys instead
-// of from sorted ones took 24 us, and the choice of a close token wholly in float64 16
-// more.
+// of from sorted ones took 24 us; the choice of a close token wholly in float64 16 more.
+//
+// What float64 costs where most tokens need it (the same sizes, calls in a graph, one
+// group / kept by the best / by the two best; 14 / 16 / 18 us by sigmoid with a bias where
+// few do, 17 / 19 / 25 by softmax).  `error` is absolute, so scores near zero are all close:
+// softmax of logits of standard deviation 4 with a bias 41 / 50 / 48, of 20 46 / 64 / 60;
+// sigmoids around exp(-20) with a bias that tells them apart 14 / 17 / 40, without one by
+// the two best 57; all logits and biases equal 32 / 53 / 54 by sigmoid, 39 / 65 / 66 by
+// softmax.  A bias of -1e30 that leaves one expert of each group makes all groups by two
+// close: 28 by sigmoid, 34 by softmax, where -infinity takes 14 and 13.
 template <typename T, int L, int V, bool SUMS>
 __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict__ logits, int64_t ld, Route a,
                                                              int team_bytes)
@@ -316,11 +324,16 @@ __global__ __launch_bounds__(kTeamThreads) void route_kernel(const T *__restrict
         if (sum == 0.0f) sum = 1.0f;
     }
 
-    // What is compared, as an order key: the logits, or the scores with their bias, off by
-    // at most `error` but for that sum's rounding.  An exponential is off by (1.3 |d| + 2)
-    // 2^-24 of itself; a sigmoid by a quarter of that (and |l| s (1 - s) is below 0.23), an
-    // addition and a reciprocal, together less than 4 * 2^-24; a softmax's score by that
-    // (|d| s is below 0.37 of the largest), and by the V + 6 additions of its sum.
+    // What is compared, as an order key: the logits, or the scores with their bias, a pair
+    // of them off by at most 2 `error` but for the rounding of the sums with the bias, which
+    // is counted where they are compared.  In units of 2^-24: an exponential is off by 2.3 |d|
+    // + 2 of itself (the difference, its product with the rounded log2(e), the exponential).
+    // A sigmoid: 1.3 |l| + 2 (no difference) times s (1 - s), below 0.8, an addition and a
+    // reciprocal, together less than 4.  A softmax's score, of 1 / sum at most: 2.1 and a
+    // product, less than 4 / sum; and the error of 1 / sum, which is the same for all scores
+    // of a token and so counts once in their difference: V + 6 additions, a quotient, and the
+    // terms' own 2 |d| + 2 with |d| their mean, weighted, 5.1 at most for 2,048 experts: less
+    // than (V + 20) / sum.  Together 8 + V + 20, within 2 (V + 16).
     float error = 0.0f;
     bool close = false;  // too close for float32
     uint32_t key[V];
@@ -598,9 +611,10 @@ struct Share {
 
 // A row of gradients is put together in LDS (zeros, and a share at each chosen expert)
 // and stored in vectors.  WHOLE: the softmax without normalisation, where every logit
-// has its share.  Bound by latency, a wave's loads, then its stores: 16,384 tokens of 256
-// float32 logits in 10 us (35 MB, 3.5 TB/s; by the bytes 5), 7.6 where the logits of the
-// chosen alone are read.
+// has its share, p = s * (1 / sum): two roundings, 2^-24 more than a division for each, with
+// which the calls below take 11.0 us in a graph instead of 10.6.  Bound by latency, a wave's
+// loads, then its stores: 16,384 tokens of 256 float32 logits in 10 us (35 MB, 3.5 TB/s; by
+// the bytes 5), 7.6 where the logits of the chosen alone are read.
 template <typename T, int L, int V, bool WHOLE>
 __global__ __launch_bounds__(kTeamThreads) void route_grad_kernel(const T *logits, int64_t ld, T *grad_logits,
                                                                   int64_t ld_grad, RouteGrad a, int team_bytes)
