@@ -204,12 +204,12 @@ def beam_select(logits, scores, count: int, normalize: bool = True, finished=Non
                 temp=None, stream=None):
     """The `count` best continuations of each search: of all totals scores[b, i] +
     log_softmax(logits[b, i])[v] (normalize False: + logits[b, i, v]) the largest, equal
-    ones by the lowest i, then the largest logit, then the lowest v.  logits (batch, beams, vocab); scores (batch, beams),
-    float32.  Returns (new scores, parents, tokens), each (batch, count): float32, the
-    beam i as int32, the token v as `dtype` (int32 by default, or int64).  A beam of score
-    -inf takes no part.  finished (batch, beams), bool or uint8: such a beam offers only
-    the token end_id, at its own score.  Where nothing is left the score is -inf, parent
-    and token -1.  At most 64 continuations of at most 1024 beams."""
+    ones by the lowest i, then the largest logit, then the lowest v.  logits (batch, beams,
+    vocab); scores (batch, beams), float32.  Returns (new scores, parents, tokens), each
+    (batch, count): float32, the beam i as int32, the token v as `dtype` (int32 by default,
+    or int64).  A beam of score -inf takes no part.  finished (batch, beams), bool or uint8:
+    such a beam offers only the token end_id, at its own score.  Where nothing is left the
+    score is -inf, parent and token -1.  At most 64 continuations of at most 1024 beams."""
     code = _r._row_code("logits", logits.dtype)
     if logits.dim() != 3:
         raise ValueError("logits must have the shape (batch, beams, vocab), not %s" % (tuple(logits.shape),))
@@ -311,20 +311,21 @@ def beam_reorder(states, parents, dim: int = 0, out=None, stream=None):
     bytes, with the batch in dimension `dim` and the beams in the next; parents (batch,
     count), int32, as beam_select returns them.  Returns `out`, a tensor of that shape
     (`states` itself for the reordering in place, of at most 64 beams whose memory lies
-    apart, which moves only what has another parent), or a new one.  Strides may be any that leave at most three dimensions beside
-    batch, beams and a contiguous piece: the filled part of a cache that has room for more
-    will do, with layers in front and heads before or behind the positions.  Of views that
-    torch conjugates or negates when they are read the values are moved: by bytes where
-    states and out are such views alike, else from a copy (as `out` alone they are
-    refused)."""
+    apart, which moves only what has another parent), or a new one.  Strides may be any
+    that leave at most three dimensions beside batch, beams and a contiguous piece: the
+    filled part of a cache that has room for more will do, with layers in front and heads
+    before or behind the positions.  Of views that torch conjugates or negates when they
+    are read the values are moved, by bytes where out is such a view too; out alone may
+    not be one."""
     if parents.dtype is not (_r._types or _r._type_codes())[2]:
         raise TypeError("parents must be int32, not %s" % parents.dtype)
     key = (states.shape, states.stride(), dim, states.dtype, parents.shape,
            out is not None and (out.shape, out.stride()))
     plan = _plans.get(key)
     if plan is None:
-        plan = states.is_complex(), *_beam_plan(states.shape, states.stride(), dim, states.element_size(), parents.shape,
-                          *((None, None) if out is None else (out.shape, out.stride())))
+        plan = states.is_complex(), *_beam_plan(states.shape, states.stride(), dim, states.element_size(),
+                                                parents.shape,
+                                                *((None, None) if out is None else (out.shape, out.stride())))
         if len(_plans) >= 4096:
             _plans.clear()
         _plans[key] = plan
